@@ -22,9 +22,14 @@ KQ_Q4_1 = KQ_AFFINE4_G32   # the same scale-and-minimum 4-bit block
 FORMATS = {"q8_0": KQ_Q8_0, "q4_0": KQ_Q4_0, "affine4": KQ_AFFINE4_G32, "q5_0": KQ_Q5_0, "q5_1": KQ_Q5_1,
            "q4_1": KQ_Q4_1}
 KQ_OK, KQ_ERR_ARG, KQ_ERR_FORMAT, KQ_ERR_SHAPE, KQ_ERR_ALIGN, KQ_ERR_RANGE, KQ_ERR_HIP = 0, -1, -2, -3, -4, -5, -6
+KQ_F32, KQ_F16, KQ_BF16 = 0, 1, 2
+TYPES = {"f32": KQ_F32, "f16": KQ_F16, "bf16": KQ_BF16}
 KQ_MAX_M = 64
 KQ_MAX_K = 1 << 20       # inputs per row
 KQ_MAX_N = 0x7FFFFFFF   # output rows per call
+KQ_MX4_MAX_ROWS = 1 << 25
+KQ_MOE_MAX_EXPERTS = 1024
+KQ_MOE_MAX_DIM = 65536
 
 # Every symbol include/kq.h declares, with (restype, argtypes).
 _I64, _I32, _P = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p
@@ -51,6 +56,15 @@ SIGNATURES = {
     "kq_moe_gemv": (_I32, [_I32, _P, _P, _P, _P, _P, _I64, _I64, _I32, _I32, _I32, _I32, _P, _I64, _P]),
     "kq_moe_ffn_workspace_bytes": (_I64, [_I64, _I64, _I32, _I32]),
     "kq_moe_ffn": (_I32, [_I32, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I32, _I32, _I32, _P, _I64, _P]),
+    "kq_mx4_quantize": (_I32, [_I32, _P, _I64, _P, _P, _I64, _I64, _P]),
+    "kq_mx4_dequantize": (_I32, [_P, _P, _I32, _P, _I64, _I64, _I64, _P]),
+    "kq_mx4_gemv": (_I32, [_P, _P, _I32, _P, _P, _I64, _I64, _I32, _P]),
+    "kq_mx4_gemm": (_I32, [_P, _P, _P, _P, _I32, _P, _I64, _I64, _I64, _P]),
+    "kq_moe_route_workspace_bytes": (_I64, [_I32, _I32]),
+    "kq_moe_route": (_I32, [_I32, _P, _I32, _P, _I32, _I64, _I32, _I32, _I32, _P, _P, _P, _I64, _P]),
+    "kq_mx4_moe_layer_workspace_bytes": (_I64, [_I64, _I64, _I32, _I32, _I32]),
+    "kq_mx4_moe_layer": (_I32, [_I32, _P, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I32, _I32, _I32,
+                                _I32, _P, _I64, _P]),
     "kq_argmax_workspace_bytes": (_I64, [_I64, _I32]),
     "kq_argmax": (_I32, [_P, _I64, _I32, _P, _P, _I64, _P]),
     "kq_f32_to_f16": (_I32, [_P, _P, _I64]),
@@ -123,6 +137,12 @@ def _fmt(fmt) -> int:
     if isinstance(fmt, str):
         return FORMATS[fmt]
     return int(fmt)
+
+
+def _type(t) -> int:
+    if isinstance(t, str):
+        return TYPES[t]
+    return int(t)
 
 
 def _ptr(t) -> int | None:
@@ -271,6 +291,58 @@ def kq_argmax_workspace_bytes(N: int, M: int) -> int:
 def kq_argmax(y, N: int, M: int, out, workspace, workspace_bytes: int, stream=None) -> None:
     _check(lib().kq_argmax(_ptr(y), N, M, _ptr(out), _ptr(workspace), workspace_bytes, _stream(stream)),
            "kq_argmax")
+
+
+def kq_mx4_quantize(xtype, x, ldx: int, codes, scales, R: int, K: int, stream=None) -> None:
+    """codes uint8 [R][K/2] and scales uint8 [R][K/32] of x (R rows of K elements, ldx apart), all device."""
+    _check(lib().kq_mx4_quantize(_type(xtype), _ptr(x), ldx, _ptr(codes), _ptr(scales), R, K, _stream(stream)),
+           "kq_mx4_quantize")
+
+
+def kq_mx4_dequantize(codes, scales, otype, out, ldo: int, R: int, K: int, stream=None) -> None:
+    """The values of a microscaled matrix into out (R rows of K elements, ldo apart)."""
+    _check(lib().kq_mx4_dequantize(_ptr(codes), _ptr(scales), _type(otype), _ptr(out), ldo, R, K, _stream(stream)),
+           "kq_mx4_dequantize")
+
+
+def kq_mx4_gemv(codes, scales, xtype, x, y, N: int, K: int, M: int, stream=None) -> None:
+    """y[M][N] (fp32) = microscaled W[N][K] @ x[M][K]^T, M <= KQ_MAX_M."""
+    _check(lib().kq_mx4_gemv(_ptr(codes), _ptr(scales), _type(xtype), _ptr(x), _ptr(y), N, K, M, _stream(stream)),
+           "kq_mx4_gemv")
+
+
+def kq_mx4_gemm(a_codes, a_scales, w_codes, w_scales, ytype, y, M: int, N: int, K: int, stream=None) -> None:
+    """y[M][N] = A[M][K] @ W[N][K]^T, both microscaled."""
+    _check(lib().kq_mx4_gemm(_ptr(a_codes), _ptr(a_scales), _ptr(w_codes), _ptr(w_scales), _type(ytype), _ptr(y),
+                             M, N, K, _stream(stream)), "kq_mx4_gemm")
+
+
+def kq_moe_route_workspace_bytes(M: int, n_experts: int) -> int:
+    return _check(lib().kq_moe_route_workspace_bytes(M, n_experts), "kq_moe_route_workspace_bytes")
+
+
+def kq_moe_route(xtype, x, wtype, W, M: int, K: int, n_experts: int, top_k: int, renorm, ids, weights, workspace,
+                 workspace_bytes: int, stream=None) -> None:
+    """ids (int32) and softmax weights (fp32), both [M][top_k], of the experts of largest W[n_experts][K] @ x[m]."""
+    _check(lib().kq_moe_route(_type(xtype), _ptr(x), _type(wtype), _ptr(W), M, K, n_experts, top_k, int(renorm),
+                              _ptr(ids), _ptr(weights), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "kq_moe_route")
+
+
+def kq_mx4_moe_layer_workspace_bytes(hidden: int, inter: int, M: int, top_k: int, n_experts: int) -> int:
+    return _check(lib().kq_mx4_moe_layer_workspace_bytes(hidden, inter, M, top_k, n_experts),
+                  "kq_mx4_moe_layer_workspace_bytes")
+
+
+def kq_mx4_moe_layer(xtype, x, wtype, router, gate_codes, gate_scales, up_codes, up_scales, down_codes, down_scales, y,
+                     ids, weights, hidden: int, inter: int, M: int, top_k: int, n_experts: int, renorm, workspace,
+                     workspace_bytes: int, stream=None) -> None:
+    """y[M][hidden] (fp32) = the routed experts' gated FFN of x[M][hidden]; ids and weights as kq_moe_route."""
+    _check(lib().kq_mx4_moe_layer(_type(xtype), _ptr(x), _type(wtype), _ptr(router), _ptr(gate_codes),
+                                  _ptr(gate_scales), _ptr(up_codes), _ptr(up_scales), _ptr(down_codes),
+                                  _ptr(down_scales), _ptr(y), _ptr(ids), _ptr(weights), hidden, inter, M, top_k,
+                                  n_experts, int(renorm), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "kq_mx4_moe_layer")
 
 
 def kq_shortlist_copy_bytes(N: int, K: int) -> int:

@@ -682,4 +682,197 @@ int kq_shortlist_argmax(const void* W, const void* W_copy, const uint16_t* x, in
   return hip_status(kq::launch_shortlist_argmax(a), "kq_shortlist_argmax");
 }
 
+// ---- microscaled 4-bit matrices, the router and the whole layer
+
+namespace {
+
+bool valid_type(int t) { return t == KQ_F32 || t == KQ_F16 || t == KQ_BF16; }
+int type_size(int t) { return t == KQ_F32 ? 4 : 2; }
+
+int check_mx4_k(int64_t K, const char* what) {
+  if (K <= 0 || K % 32 != 0 || K > KQ_MAX_K)
+    return fail(KQ_ERR_SHAPE, "%s=%lld must be a positive multiple of 32 and <= %d", what, (long long)K, KQ_MAX_K);
+  return KQ_OK;
+}
+
+int check_mx4_rows(int64_t R, const char* what) {
+  if (R < 0 || R > KQ_MX4_MAX_ROWS) return fail(KQ_ERR_ARG, "%s=%lld must be in [0, %d]", what, (long long)R, KQ_MX4_MAX_ROWS);
+  return KQ_OK;
+}
+
+// Common checks of the two conversions; *empty where there is nothing to do.
+int check_convert(const char* who, int type, const void* dense, int64_t ld, const void* codes, const void* scales,
+                  int64_t R, int64_t K, bool* empty) {
+  *empty = false;
+  int st = check_mx4_k(K, "K");
+  if (st) return st;
+  if ((st = check_mx4_rows(R, "R"))) return st;
+  if (!valid_type(type)) return fail(KQ_ERR_ARG, "%s: unknown type %d", who, type);
+  if (ld < K || ld > (int64_t)1 << 35) return fail(KQ_ERR_ARG, "%s: row stride %lld must be in [K, 2^35]", who, (long long)ld);
+  if (R == 0) {
+    *empty = true;
+    return KQ_OK;
+  }
+  if (!dense || !codes || !scales) return fail(KQ_ERR_ARG, "%s: null pointer", who);
+  if (!aligned(dense, type_size(type))) return fail(KQ_ERR_ALIGN, "%s: elements must be aligned to their size", who);
+  if (!aligned(codes, 16) || !aligned(scales, 4))
+    return fail(KQ_ERR_ALIGN, "%s: codes must be 16-byte and scales 4-byte aligned", who);
+  if (!kq::mx4_walk_fits(R, K, ld)) return fail(KQ_ERR_ARG, "%s: too many strided rows", who);
+  return KQ_OK;
+}
+
+int check_route(const char* who, int xtype, const void* x, int wtype, const void* W, int M, int64_t K, int n_experts,
+                int top_k, int renorm, bool* empty) {
+  *empty = false;
+  int st = check_mx4_k(K, "K");
+  if (st) return st;
+  if (!valid_type(xtype) || !valid_type(wtype)) return fail(KQ_ERR_ARG, "%s: unknown type", who);
+  if (M < 0 || M > KQ_MAX_M) return fail(KQ_ERR_ARG, "M=%d must be in [0, %d]", M, KQ_MAX_M);
+  if (n_experts < 1 || n_experts > KQ_MOE_MAX_EXPERTS)
+    return fail(KQ_ERR_ARG, "n_experts=%d must be in [1, %d]", n_experts, KQ_MOE_MAX_EXPERTS);
+  if (top_k < 1 || top_k > n_experts || top_k > 64)
+    return fail(KQ_ERR_ARG, "top_k=%d must be in [1, min(n_experts, 64)]", top_k);
+  if (renorm != 0 && renorm != 1) return fail(KQ_ERR_ARG, "renorm must be 0 or 1");
+  if (M == 0) {
+    *empty = true;
+    return KQ_OK;
+  }
+  if (!x || !W) return fail(KQ_ERR_ARG, "%s: null pointer", who);
+  if (!aligned(x, 16) || !aligned(W, 16)) return fail(KQ_ERR_ALIGN, "%s: x and the router must be 16-byte aligned", who);
+  return KQ_OK;
+}
+
+int check_workspace(const char* who, const void* workspace, int64_t given, int64_t need) {
+  if (!workspace || given < need) return fail(KQ_ERR_ARG, "%s: workspace of %lld bytes needed", who, (long long)need);
+  if (!aligned(workspace, 16)) return fail(KQ_ERR_ALIGN, "%s: workspace must be 16-byte aligned", who);
+  return KQ_OK;
+}
+
+const uint8_t* bytes(const void* p) { return static_cast<const uint8_t*>(p); }
+
+}  // namespace
+
+int kq_mx4_quantize(int type, const void* x, int64_t ldx, void* codes, void* scales, int64_t R, int64_t K,
+                    void* stream) {
+  bool empty;
+  const int st = check_convert("kq_mx4_quantize", type, x, ldx, codes, scales, R, K, &empty);
+  if (st) return st;
+  if (empty) return ok();
+  return hip_status(kq::launch_mx4_quantize(type, x, ldx, codes, scales, R, K, static_cast<hipStream_t>(stream)),
+                    "kq_mx4_quantize");
+}
+
+int kq_mx4_dequantize(const void* codes, const void* scales, int type, void* out, int64_t ldo, int64_t R, int64_t K,
+                      void* stream) {
+  bool empty;
+  const int st = check_convert("kq_mx4_dequantize", type, out, ldo, codes, scales, R, K, &empty);
+  if (st) return st;
+  if (empty) return ok();
+  return hip_status(kq::launch_mx4_dequantize(codes, scales, type, out, ldo, R, K, static_cast<hipStream_t>(stream)),
+                    "kq_mx4_dequantize");
+}
+
+int kq_mx4_gemv(const void* codes, const void* scales, int type, const void* x, float* y, int64_t N, int64_t K, int M,
+                void* stream) {
+  int st = check_mx4_k(K, "K");
+  if (st) return st;
+  if ((st = check_mx4_rows(N, "N"))) return st;
+  if (!valid_type(type)) return fail(KQ_ERR_ARG, "kq_mx4_gemv: unknown type %d", type);
+  if (M < 0 || M > KQ_MAX_M) return fail(KQ_ERR_ARG, "M=%d must be in [0, %d]", M, KQ_MAX_M);
+  if (M == 0 || N == 0) return ok();
+  if (!codes || !scales || !x || !y) return fail(KQ_ERR_ARG, "kq_mx4_gemv: null pointer");
+  if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(x, 16) || !aligned(y, 4))
+    return fail(KQ_ERR_ALIGN, "kq_mx4_gemv: codes and x must be 16-byte, scales and y 4-byte aligned");
+  const kq::Mx4GemvArgs a{bytes(codes), bytes(scales), type, x, y, N, K, M, static_cast<hipStream_t>(stream)};
+  return hip_status(kq::launch_mx4_gemv(a), "kq_mx4_gemv");
+}
+
+int kq_mx4_gemm(const void* a_codes, const void* a_scales, const void* w_codes, const void* w_scales, int type,
+                void* y, int64_t M, int64_t N, int64_t K, void* stream) {
+  int st = check_mx4_k(K, "K");
+  if (st) return st;
+  if ((st = check_mx4_rows(M, "M"))) return st;
+  if ((st = check_mx4_rows(N, "N"))) return st;
+  if (!valid_type(type)) return fail(KQ_ERR_ARG, "kq_mx4_gemm: unknown type %d", type);
+  if (M == 0 || N == 0) return ok();
+  if (!a_codes || !a_scales || !w_codes || !w_scales || !y) return fail(KQ_ERR_ARG, "kq_mx4_gemm: null pointer");
+  if (!aligned(a_codes, 16) || !aligned(w_codes, 16) || !aligned(y, 16) || !aligned(a_scales, 4) || !aligned(w_scales, 4))
+    return fail(KQ_ERR_ALIGN, "kq_mx4_gemm: codes and y must be 16-byte, scales 4-byte aligned");
+  if (!kq::mx4_gemm_fits(M, N)) return fail(KQ_ERR_ARG, "kq_mx4_gemm: M x N is beyond the grid");
+  const kq::Mx4GemmArgs a{bytes(a_codes), bytes(a_scales), bytes(w_codes), bytes(w_scales), type, y, M, N, K,
+                          static_cast<hipStream_t>(stream)};
+  return hip_status(kq::launch_mx4_gemm(a), "kq_mx4_gemm");
+}
+
+int64_t kq_moe_route_workspace_bytes(int M, int n_experts) {
+  if (M < 0 || M > KQ_MAX_M) return fail(KQ_ERR_ARG, "M=%d must be in [0, %d]", M, KQ_MAX_M);
+  if (n_experts < 1 || n_experts > KQ_MOE_MAX_EXPERTS)
+    return fail(KQ_ERR_ARG, "n_experts=%d must be in [1, %d]", n_experts, KQ_MOE_MAX_EXPERTS);
+  return kq::route_workspace_bytes(M, n_experts);
+}
+
+int kq_moe_route(int xtype, const void* x, int wtype, const void* W, int M, int64_t K, int n_experts, int top_k,
+                 int renorm, int32_t* ids, float* weights, void* workspace, int64_t workspace_bytes, void* stream) {
+  bool empty;
+  int st = check_route("kq_moe_route", xtype, x, wtype, W, M, K, n_experts, top_k, renorm, &empty);
+  if (st) return st;
+  if (empty) return ok();
+  if (!ids || !weights) return fail(KQ_ERR_ARG, "kq_moe_route: null pointer");
+  if (!aligned(ids, 4) || !aligned(weights, 4)) return fail(KQ_ERR_ALIGN, "kq_moe_route: ids and weights must be 4-byte aligned");
+  if ((st = check_workspace("kq_moe_route", workspace, workspace_bytes, kq::route_workspace_bytes(M, n_experts)))) return st;
+  const kq::RouteArgs a{xtype, x, wtype, W, M, K, n_experts, top_k, renorm, ids, weights, workspace,
+                        static_cast<hipStream_t>(stream)};
+  return hip_status(kq::launch_route(a), "kq_moe_route");
+}
+
+static int check_moe_layer_dims(int64_t hidden, int64_t inter) {
+  int st = check_mx4_k(hidden, "hidden");
+  if (st) return st;
+  if ((st = check_mx4_k(inter, "inter"))) return st;
+  if (hidden > KQ_MOE_MAX_DIM || inter > KQ_MOE_MAX_DIM)
+    return fail(KQ_ERR_SHAPE, "hidden=%lld and inter=%lld must be <= %d", (long long)hidden, (long long)inter, KQ_MOE_MAX_DIM);
+  return KQ_OK;
+}
+
+int64_t kq_mx4_moe_layer_workspace_bytes(int64_t hidden, int64_t inter, int M, int top_k, int n_experts) {
+  const int st = check_moe_layer_dims(hidden, inter);
+  if (st) return st;
+  if (M < 0 || M > KQ_MAX_M) return fail(KQ_ERR_ARG, "M=%d must be in [0, %d]", M, KQ_MAX_M);
+  if (n_experts < 1 || n_experts > KQ_MOE_MAX_EXPERTS)
+    return fail(KQ_ERR_ARG, "n_experts=%d must be in [1, %d]", n_experts, KQ_MOE_MAX_EXPERTS);
+  if (top_k < 1 || top_k > n_experts || top_k > 64)
+    return fail(KQ_ERR_ARG, "top_k=%d must be in [1, min(n_experts, 64)]", top_k);
+  return kq::mx4_moe_workspace_bytes(hidden, inter, M, top_k, n_experts);
+}
+
+int kq_mx4_moe_layer(int xtype, const void* x, int wtype, const void* router, const void* gate_codes,
+                     const void* gate_scales, const void* up_codes, const void* up_scales, const void* down_codes,
+                     const void* down_scales, float* y, int32_t* ids, float* weights, int64_t hidden, int64_t inter,
+                     int M, int top_k, int n_experts, int renorm, void* workspace, int64_t workspace_bytes,
+                     void* stream) {
+  int st = check_moe_layer_dims(hidden, inter);
+  if (st) return st;
+  bool empty;
+  if ((st = check_route("kq_mx4_moe_layer", xtype, x, wtype, router, M, hidden, n_experts, top_k, renorm, &empty))) return st;
+  if (empty) return ok();
+  const void* planes[6] = {gate_codes, up_codes, down_codes, gate_scales, up_scales, down_scales};
+  for (int i = 0; i < 6; ++i) {
+    if (!planes[i]) return fail(KQ_ERR_ARG, "kq_mx4_moe_layer: null pointer");
+    if (!aligned(planes[i], i < 3 ? 16 : 4))
+      return fail(KQ_ERR_ALIGN, "kq_mx4_moe_layer: codes must be 16-byte and scales 4-byte aligned");
+  }
+  if (!y || !ids || !weights) return fail(KQ_ERR_ARG, "kq_mx4_moe_layer: null pointer");
+  if (!aligned(y, 4) || !aligned(ids, 4) || !aligned(weights, 4))
+    return fail(KQ_ERR_ALIGN, "kq_mx4_moe_layer: y, ids and weights must be 4-byte aligned");
+  const int64_t need = kq::mx4_moe_workspace_bytes(hidden, inter, M, top_k, n_experts);
+  if ((st = check_workspace("kq_mx4_moe_layer", workspace, workspace_bytes, need))) return st;
+  kq::Mx4MoeArgs a;
+  a.route = kq::RouteArgs{xtype, x, wtype, router, M, hidden, n_experts, top_k, renorm, ids, weights, workspace,
+                          static_cast<hipStream_t>(stream)};
+  for (int i = 0; i < 3; ++i) a.codes[i] = bytes(planes[i]), a.scales[i] = bytes(planes[3 + i]);
+  a.y = y;
+  a.inter = inter;
+  return hip_status(kq::launch_mx4_moe(a), "kq_mx4_moe_layer");
+}
+
 }  // extern "C"

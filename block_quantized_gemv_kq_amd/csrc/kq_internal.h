@@ -210,6 +210,69 @@ int stack_device_info(int* cus);
 int copy_to_device(void* dst, const void* src, int64_t bytes, hipStream_t stream);
 int read_from_device(void* dst, const void* src, int64_t bytes, hipStream_t stream);
 
+// ---- microscaled 4-bit matrices (kq_mx4*.hip)
+// Whether the quantise and dequantise grids reach this shape.
+bool mx4_walk_fits(int64_t R, int64_t K, int64_t ld);
+int launch_mx4_quantize(int type, const void* x, int64_t ldx, void* codes, void* scales, int64_t R, int64_t K,
+                        hipStream_t stream);
+int launch_mx4_dequantize(const void* codes, const void* scales, int type, void* out, int64_t ldo, int64_t R,
+                          int64_t K, hipStream_t stream);
+struct Mx4GemvArgs {
+  const uint8_t* codes;     // [N][K/2]
+  const uint8_t* scales;    // [N][K/32]
+  int type;                 // kq_type of x
+  const void* x;            // [M][K]
+  float* y;                 // [M][N]
+  int64_t N;
+  int64_t K;
+  int M;
+  hipStream_t stream;
+};
+int launch_mx4_gemv(const Mx4GemvArgs& a);
+struct Mx4GemmArgs {
+  const uint8_t* a_codes;   // [M][K/2]
+  const uint8_t* a_scales;  // [M][K/32]
+  const uint8_t* w_codes;   // [N][K/2]
+  const uint8_t* w_scales;  // [N][K/32]
+  int type;                 // kq_type of y
+  void* y;                  // [M][N]
+  int64_t M;
+  int64_t N;
+  int64_t K;
+  hipStream_t stream;
+};
+// Whether the product's grid reaches this shape.
+bool mx4_gemm_fits(int64_t M, int64_t N);
+int launch_mx4_gemm(const Mx4GemmArgs& a);
+
+// ---- the router and the whole mixture-of-experts layer (kq_mx4_moe.hip)
+struct RouteArgs {
+  int xtype;                // kq_type of x
+  const void* x;            // [M][K]
+  int wtype;                // kq_type of the router's rows
+  const void* W;            // [E][K]
+  int M;
+  int64_t K;
+  int E;
+  int top_k;
+  int renorm;
+  int32_t* ids;             // [M][top_k]
+  float* weights;           // [M][top_k]
+  void* ws;
+  hipStream_t stream;
+};
+int64_t route_workspace_bytes(int M, int E);
+int launch_route(const RouteArgs& a);
+struct Mx4MoeArgs {
+  RouteArgs route;          // K = hidden
+  const uint8_t* codes[3];  // gate, up [E][inter][hidden/2], down [E][hidden][inter/2]
+  const uint8_t* scales[3];
+  float* y;                 // [M][hidden]
+  int64_t inter;
+};
+int64_t mx4_moe_workspace_bytes(int64_t hidden, int64_t inter, int M, int top_k, int E);
+int launch_mx4_moe(const Mx4MoeArgs& a);
+
 int64_t argmax_partials(int64_t N);
 int launch_argmax(const float* y, int64_t N, int M, int32_t* out, void* ws, hipStream_t stream);
 int launch_argmax_final(const void* part, int nparts, int M, int32_t* out, hipStream_t stream);

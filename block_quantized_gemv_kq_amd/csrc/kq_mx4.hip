@@ -1,0 +1,276 @@
+// kq_mx4.hip — microscaled 4-bit matrices: quantising, dequantising, and the
+// product with a few activation columns (decode and verify passes).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kq_internal.h"
+#include "kq_mx4_dev.h"
+
+namespace kqd {
+
+// Eight consecutive values of type T at p as fp32 (exact). VEC: p is aligned
+// for 16-byte loads.
+template <int T, bool VEC>
+__device__ __forceinline__ void load8(const void* p, float (&f)[8]) {
+  if constexpr (T == T_F32) {
+    const float* q = static_cast<const float*>(p);
+    if constexpr (VEC) {
+      const v4f a = *reinterpret_cast<const v4f*>(q), b = *reinterpret_cast<const v4f*>(q + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = a[j], f[4 + j] = b[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = q[j];
+    }
+  } else {
+    uint16_t h[8];
+    const uint16_t* q = static_cast<const uint16_t*>(p);
+    if constexpr (VEC) {
+      const u32x4 a = *reinterpret_cast<const u32x4*>(q);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[2 * j] = (uint16_t)a[j], h[2 * j + 1] = (uint16_t)(a[j] >> 16);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] = q[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      f[j] = T == T_F16 ? (float)__builtin_bit_cast(_Float16, h[j]) : __builtin_bit_cast(float, (uint32_t)h[j] << 16);
+  }
+}
+
+// Quantise: four lanes per block of 32, eight values each. The scale byte is
+// the exponent field of the block's largest magnitude less two, not below
+// zero: floor(log2(amax)) - 2 with the bias of 127, so the largest value lands
+// in [4, 8) (a denormal or zero amax gives byte 0). The conversion instruction
+// divides by the scale exactly, rounds to the nearest code (even on ties) and
+// saturates at 6. Magnitudes are compared as integers, which orders NaN above
+// infinity above every number, so one comparison finds a block that has any.
+template <int T, bool VEC>
+__global__ __launch_bounds__(256) void k_mx4_quantize(const uint8_t* __restrict__ x, int64_t ldx_bytes,
+                                                      uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
+                                                      int64_t row_groups, uint32_t chunks) {
+  const uint32_t row = blockIdx.x / chunks, chunk = blockIdx.x - row * chunks;
+  const int64_t i = (int64_t)chunk * 256 + threadIdx.x;   // group of eight values within the row
+  if (i >= row_groups) return;                            // whole blocks leave together (row_groups % 4 == 0)
+  float f[8];
+  load8<T, VEC>(x + (int64_t)row * ldx_bytes + i * (8 * TypeSize<T>::v), f);
+  uint32_t amax = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) amax = max(amax, __builtin_bit_cast(uint32_t, f[j]) & 0x7fffffffu);
+  amax = max(amax, (uint32_t)__builtin_amdgcn_mov_dpp((int)amax, 0xB1, 0xF, 0xF, true));   // lane ^ 1
+  amax = max(amax, (uint32_t)__builtin_amdgcn_mov_dpp((int)amax, 0x4E, 0xF, 0xF, true));   // lane ^ 2
+  const bool finite = amax < 0x7f800000u;
+  const uint32_t e = amax >> 23;
+  const uint32_t s = finite ? (e > 2u ? e - 2u : 0u) : 255u;
+  const float sc = scale_of(finite ? s : 127u);
+  uint32_t d = 0;
+  d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, f[0], f[1], sc, 0);
+  d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, f[2], f[3], sc, 1);
+  d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, f[4], f[5], sc, 2);
+  d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, f[6], f[7], sc, 3);
+  const int64_t o = (int64_t)row * row_groups + i;
+  reinterpret_cast<uint32_t*>(codes)[o] = finite ? d : 0u;
+  if ((threadIdx.x & 3) == 0) scales[o >> 2] = (uint8_t)s;
+}
+
+// Dequantise: eight values per lane, each code times its scale rounded to T
+// (exact in fp32 and bf16 up to their largest finite value).
+template <int T, bool VEC>
+__global__ __launch_bounds__(256) void k_mx4_dequantize(const uint8_t* __restrict__ codes,
+                                                        const uint8_t* __restrict__ scales, uint8_t* __restrict__ out,
+                                                        int64_t ldo_bytes, int64_t row_groups, uint32_t chunks) {
+  const uint32_t row = blockIdx.x / chunks, chunk = blockIdx.x - row * chunks;
+  const int64_t i = (int64_t)chunk * 256 + threadIdx.x;
+  if (i >= row_groups) return;
+  const int64_t o = (int64_t)row * row_groups + i;
+  const uint32_t d = reinterpret_cast<const uint32_t*>(codes)[o];
+  const float sc = scale_of(scales[o >> 2]);
+  uint8_t* p = out + (int64_t)row * ldo_bytes + i * (8 * TypeSize<T>::v);
+  if constexpr (T == T_BF16) {
+    const v8b v = codes_bf16(d, sc);
+    if constexpr (VEC) {
+      *reinterpret_cast<v8b*>(p) = v;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) reinterpret_cast<__bf16*>(p)[j] = v[j];
+    }
+  } else {
+    float f[8];
+    const v2f a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, sc, 0);
+    const v2f b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, sc, 1);
+    const v2f c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, sc, 2);
+    const v2f e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, sc, 3);
+    f[0] = a[0], f[1] = a[1], f[2] = b[0], f[3] = b[1], f[4] = c[0], f[5] = c[1], f[6] = e[0], f[7] = e[1];
+    if constexpr (T == T_F32) {
+      if constexpr (VEC) {
+        reinterpret_cast<v4f*>(p)[0] = v4f{f[0], f[1], f[2], f[3]};
+        reinterpret_cast<v4f*>(p)[1] = v4f{f[4], f[5], f[6], f[7]};
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) reinterpret_cast<float*>(p)[j] = f[j];
+      }
+    } else {
+      v8h v;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = (_Float16)f[j];
+      if constexpr (VEC) {
+        *reinterpret_cast<v8h*>(p) = v;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) reinterpret_cast<_Float16*>(p)[j] = v[j];
+      }
+    }
+  }
+}
+
+// y[m][n] for RT tiles of 16 weight rows and up to 16 CT columns. The waves of
+// a workgroup share the rows and split K; their partial sums meet in LDS and
+// are added in wave order. Dynamic LDS: waves * RT * CT KiB.
+template <int XT, int CT, int RT, int U, bool AL>
+__global__ __launch_bounds__(1024) void k_mx4_gemv(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+                                                   const void* __restrict__ x, float* __restrict__ y, int N, int K,
+                                                   int M, int waves) {
+  extern __shared__ v4f red[];   // [wave][RT][CT][64]
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int nblk = K / 32, nchunk = (nblk + 3) / 4;
+  const int64_t row0 = (int64_t)blockIdx.x * (16 * RT);
+  rsrc_t rc[RT], rs[RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const int64_t left = (int64_t)N - row0 - 16 * t;
+    const int rows = left < 0 ? 0 : left < 16 ? (int)left : 16;
+    mx4_rows(codes, scales, rows ? row0 + 16 * t : 0, rows, nblk, rc[t], rs[t]);
+  }
+  const uint32_t xrow = (uint32_t)K * TypeSize<XT>::v;
+  const rsrc_t rx = make_rsrc(x, (uint32_t)M * xrow);
+  uint32_t xoff[CT];
+#pragma unroll
+  for (int u = 0; u < CT; ++u) {
+    const int m = 16 * u + (lane & 15);
+    xoff[u] = m < M ? (uint32_t)m * xrow : OOB;
+  }
+  v4f acc[RT][CT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int u = 0; u < CT; ++u) acc[t][u] = v4f{0.f, 0.f, 0.f, 0.f};
+  const int c0 = (int)((int64_t)nchunk * wave / waves), c1 = (int)((int64_t)nchunk * (wave + 1) / waves);
+  mx4_tile<XT, CT, RT, U, AL>(rc, rs, rx, xoff, nblk, c0, c1, acc);
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int u = 0; u < CT; ++u) red[((wave * RT + t) * CT + u) * 64 + lane] = acc[t][u];
+  __syncthreads();
+  for (int i = threadIdx.x; i < RT * CT * 64; i += 64 * waves) {
+    v4f s = red[i];
+    for (int w = 1; w < waves; ++w) s += red[w * (RT * CT * 64) + i];
+    const int l = i & 63, u = (i >> 6) % CT, t = (i >> 6) / CT;
+    const int64_t n = row0 + 16 * t + (l & 15);
+    if (n >= N) continue;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int m = 16 * u + 4 * (l >> 4) + j;
+      if (m < M) y[(int64_t)m * N + n] = s[j];
+    }
+  }
+}
+
+}  // namespace kqd
+
+namespace kq {
+
+using namespace kqd;
+
+namespace {
+
+// Rows as the kernels walk them: contiguous rows are one long row.
+struct Walk {
+  int64_t rows, groups;
+  uint32_t chunks;
+  uint64_t blocks;
+};
+Walk walk_of(int64_t R, int64_t K, bool contiguous) {
+  Walk w;
+  w.rows = contiguous ? 1 : R;
+  w.groups = (contiguous ? R * K : K) / 8;
+  const int64_t chunks = (w.groups + 255) / 256;
+  w.chunks = (uint32_t)chunks;
+  w.blocks = (uint64_t)w.rows * (uint64_t)chunks;
+  return w;
+}
+
+}  // namespace
+
+bool mx4_walk_fits(int64_t R, int64_t K, int64_t ld) {
+  return walk_of(R, K, ld == K).blocks <= 0xffffffffull / 256;   // a grid has less than 2^32 threads
+}
+
+int launch_mx4_quantize(int type, const void* x, int64_t ldx, void* codes, void* scales, int64_t R, int64_t K,
+                        hipStream_t stream) {
+  const Walk w = walk_of(R, K, ldx == K);
+  const int size = type == KQ_F32 ? 4 : 2;
+  const bool vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (w.rows == 1 || ldx * size % 16 == 0);
+  dispatch_log("k_mx4_quantize", -1, R, K, 0, (unsigned)w.blocks, 1, 256, 0, "type=%d vec=%d", type, (int)vec);
+#define KQ_LAUNCH(T, V)                                                                                        \
+  hipLaunchKernelGGL((k_mx4_quantize<T, V>), dim3((unsigned)w.blocks), dim3(256), 0, stream,                   \
+                     static_cast<const uint8_t*>(x), ldx* size, static_cast<uint8_t*>(codes),                  \
+                     static_cast<uint8_t*>(scales), w.groups, w.chunks)
+  if (type == KQ_F32) { if (vec) KQ_LAUNCH(T_F32, true); else KQ_LAUNCH(T_F32, false); }
+  else if (type == KQ_F16) { if (vec) KQ_LAUNCH(T_F16, true); else KQ_LAUNCH(T_F16, false); }
+  else { if (vec) KQ_LAUNCH(T_BF16, true); else KQ_LAUNCH(T_BF16, false); }
+#undef KQ_LAUNCH
+  return (int)hipGetLastError();
+}
+
+int launch_mx4_dequantize(const void* codes, const void* scales, int type, void* out, int64_t ldo, int64_t R,
+                          int64_t K, hipStream_t stream) {
+  const Walk w = walk_of(R, K, ldo == K);
+  const int size = type == KQ_F32 ? 4 : 2;
+  const bool vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0 && (w.rows == 1 || ldo * size % 16 == 0);
+  dispatch_log("k_mx4_dequantize", -1, R, K, 0, (unsigned)w.blocks, 1, 256, 0, "type=%d vec=%d", type, (int)vec);
+#define KQ_LAUNCH(T, V)                                                                                        \
+  hipLaunchKernelGGL((k_mx4_dequantize<T, V>), dim3((unsigned)w.blocks), dim3(256), 0, stream,                 \
+                     static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales),                  \
+                     static_cast<uint8_t*>(out), ldo* size, w.groups, w.chunks)
+  if (type == KQ_F32) { if (vec) KQ_LAUNCH(T_F32, true); else KQ_LAUNCH(T_F32, false); }
+  else if (type == KQ_F16) { if (vec) KQ_LAUNCH(T_F16, true); else KQ_LAUNCH(T_F16, false); }
+  else { if (vec) KQ_LAUNCH(T_BF16, true); else KQ_LAUNCH(T_BF16, false); }
+#undef KQ_LAUNCH
+  return (int)hipGetLastError();
+}
+
+namespace {
+
+template <int XT, int CT, int RT, int U>
+int gemv_cfg(const Mx4GemvArgs& a) {
+  const int nchunk = (int)((a.K / 32 + 3) / 4);
+  int waves = (nchunk + U - 1) / U;   // one batch of loads per wave
+  const int most = 64 / (RT * CT) < 16 ? 64 / (RT * CT) : 16;   // LDS: 64 KiB of partial sums
+  waves = waves < 1 ? 1 : waves > most ? most : waves;
+  const unsigned grid = (unsigned)((a.N + 16 * RT - 1) / (16 * RT));
+  const size_t lds = (size_t)waves * RT * CT * 1024;
+  dispatch_log("k_mx4_gemv", -1, a.N, a.K, a.M, grid, 1, (unsigned)(64 * waves), lds, "type=%d ct=%d rt=%d", XT, CT, RT);
+  if (a.K % 128 == 0)
+    hipLaunchKernelGGL((k_mx4_gemv<XT, CT, RT, U, true>), dim3(grid), dim3(64 * waves), lds, a.stream, a.codes,
+                       a.scales, a.x, a.y, (int)a.N, (int)a.K, a.M, waves);
+  else
+    hipLaunchKernelGGL((k_mx4_gemv<XT, CT, RT, U, false>), dim3(grid), dim3(64 * waves), lds, a.stream, a.codes,
+                       a.scales, a.x, a.y, (int)a.N, (int)a.K, a.M, waves);
+  return (int)hipGetLastError();
+}
+
+template <int XT>
+int gemv_type(const Mx4GemvArgs& a) {
+  if (a.M <= 16) return gemv_cfg<XT, 1, 1, XT == T_F32 ? 2 : 4>(a);
+  if (a.M <= 32) return gemv_cfg<XT, 2, 1, XT == T_F32 ? 1 : 2>(a);
+  return gemv_cfg<XT, 4, 1, 1>(a);
+}
+
+}  // namespace
+
+int launch_mx4_gemv(const Mx4GemvArgs& a) {
+  return a.type == KQ_F32 ? gemv_type<T_F32>(a) : a.type == KQ_F16 ? gemv_type<T_F16>(a) : gemv_type<T_BF16>(a);
+}
+
+}  // namespace kq

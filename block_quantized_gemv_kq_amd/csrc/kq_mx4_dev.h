@@ -1,0 +1,271 @@
+// kq_mx4_dev.h — device-side building blocks of the microscaled 4-bit kernels.
+//
+// A microscaled matrix is two planes: codes [R][K/2] (element 2i in the low
+// nibble of byte i; sign, two exponent bits, one mantissa bit: 0, 0.5, 1, 1.5,
+// 2, 3, 4, 6) and scales [R][K/32], one byte s per 32 elements of a row that
+// stands for 2^(s-127) (255: NaN). The value of an element is code * scale.
+//
+// gfx950 converts pairs of codes to fp32, fp16 or bf16 with a scale in one
+// instruction. Its scale operand is an fp32 whose exponent field is read, so
+// s << 23 is the scale for every byte: 0 stands for 2^-127 and 255 gives NaN.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kq_dev.h"
+
+namespace kqd {
+
+enum { T_F32 = 0, T_F16 = 1, T_BF16 = 2 };   // kq_type
+template <int T> struct TypeSize { static constexpr int v = T == T_F32 ? 4 : 2; };
+
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef double v4d __attribute__((ext_vector_type(4)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ uint32_t ld8(rsrc_t r, uint32_t off) {
+  return (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r, off, 0, 0);
+}
+
+// By value: this compiler takes element 0 for every element when a vector's
+// element is bit-cast in place.
+__device__ __forceinline__ float bits_f32(uint32_t v) { return __builtin_bit_cast(float, v); }
+
+__device__ __forceinline__ float scale_of(uint32_t byte) { return __builtin_bit_cast(float, byte << 23); }
+
+// fp32 value of a scale byte (NaN for 255), through the code of 1.
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+  const v2f one = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(0x22u, scale_of(byte), 0);
+  return one[0];
+}
+
+// Eight codes (one dword) times their scale as bf16: exact wherever bf16
+// reaches (every code and scale up to its largest finite value).
+__device__ __forceinline__ v8b codes_bf16(uint32_t d, float scale) {
+  const v2b a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 0);
+  const v2b b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 1);
+  const v2b c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 2);
+  const v2b e = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 3);
+  return v8b{a[0], a[1], b[0], b[1], c[0], c[1], e[0], e[1]};
+}
+
+// Eight codes as fp16, unscaled (exact).
+__device__ __forceinline__ v8h codes_f16(uint32_t d) {
+  const v2h a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(d, 1.0f, 0);
+  const v2h b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(d, 1.0f, 1);
+  const v2h c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(d, 1.0f, 2);
+  const v2h e = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(d, 1.0f, 3);
+  return v8h{a[0], a[1], b[0], b[1], c[0], c[1], e[0], e[1]};
+}
+
+// 4x4 transposition between the four 16-lane groups of a wave and the four
+// dwords each lane holds: afterwards dword s of a lane in group g is dword g
+// of the lane 16 s + (lane & 15). The swaps are written out with their wait
+// states: the compiler does not track them through inline assembly.
+__device__ __forceinline__ void transpose_groups(uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  asm("s_nop 1\n\t"
+      "v_permlane32_swap_b32 %0, %2\n\t"
+      "v_permlane32_swap_b32 %1, %3\n\t"
+      "s_nop 1\n\t"
+      "v_permlane16_swap_b32 %0, %1\n\t"
+      "v_permlane16_swap_b32 %2, %3\n\t"
+      "s_nop 1"
+      : "+v"(a), "+v"(b), "+v"(c), "+v"(d));
+}
+
+// ---- The product of a weight tile with a few columns, one wave's share.
+//
+// v_mfma_f32_16x16x32 with the columns' values as its A operand and 16 weight
+// rows as B: lane (r = lane & 15, g = lane >> 4) supplies column r and weight
+// row r, and result element i of the lane is y[column 4 g + i][row r].
+// K is walked in chunks of 128 (four blocks); a lane loads the 16 bytes of
+// block 4c + g of its weight row, so a wave reads 64 contiguous bytes of each
+// row per load.
+//
+// bf16 columns: the four matrix instructions of a chunk take dword s of every
+// lane, so lane group g contributes elements 8s..8s+7 of block 4c + g, and the
+// conversion applies each lane's own scale: the operand is the exact weight.
+// fp32 columns: the same with the value split into three bf16 pieces of eight
+// bits each (24 in all: exact), three matrix instructions each.
+// fp16 columns: bf16 cannot hold them and fp16 cannot hold the scales, so the
+// codes go in unscaled and the scale multiplies each block's fp32 result; for
+// that the codes are transposed among the lane groups first, and matrix
+// instruction s covers the 32 elements of block 4c + s.
+template <int XT, int CT>
+struct XChunk {
+  u32x4 v[CT][XT == T_F32 ? 8 : 4];
+};
+
+template <int XT, int CT>
+__device__ __forceinline__ void load_x_chunk(rsrc_t rx, const uint32_t (&xoff)[CT], int c, int nblk, int g,
+                                             XChunk<XT, CT>& x) {
+#pragma unroll
+  for (int t = 0; t < CT; ++t) {
+    if constexpr (XT == T_F16) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const int b = 4 * c + s;
+        x.v[t][s] = ld128(rx, b < nblk ? xoff[t] + (uint32_t)b * 64u + (uint32_t)g * 16u : OOB);
+      }
+    } else {
+      constexpr uint32_t BLK = 32 * TypeSize<XT>::v;
+      const int b = 4 * c + g;
+      const uint32_t o = b < nblk ? xoff[t] + (uint32_t)b * BLK : OOB;
+#pragma unroll
+      for (int s = 0; s < (int)BLK / 16; ++s) x.v[t][s] = ld128(rx, o + 16u * s);
+    }
+  }
+}
+
+template <int RT>
+struct WChunk {
+  u32x4 codes[RT];
+  uint32_t scale[RT];   // fp16 columns: the four bytes of the chunk; others: the byte of the lane's block
+};
+
+// AL: rows hold whole chunks (K a multiple of 128), so a chunk's four scale
+// bytes are one aligned dword; otherwise they are loaded one by one, blocks
+// past the row's end reading zero.
+template <int XT, int RT, bool AL>
+__device__ __forceinline__ void load_w_chunk(const rsrc_t (&rc)[RT], const rsrc_t (&rs)[RT], int c, int nblk, int r,
+                                             int g, WChunk<RT>& w) {
+  const int b = 4 * c + g;
+  const uint32_t co = b < nblk ? ((uint32_t)r * (uint32_t)nblk + (uint32_t)b) * 16u : OOB;
+#pragma unroll
+  for (int t = 0; t < RT; ++t) w.codes[t] = ld128(rc[t], co);
+  const uint32_t so = (uint32_t)r * (uint32_t)nblk + 4u * (uint32_t)c;
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    if constexpr (AL) {
+      const uint32_t d = ld32(rs[t], 4 * c < nblk ? so : OOB);
+      w.scale[t] = d;
+    } else if constexpr (XT == T_F16) {
+      uint32_t d = 0;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) d |= ld8(rs[t], 4 * c + s < nblk ? so + s : OOB) << (8 * s);
+      w.scale[t] = d;
+    } else {
+      w.scale[t] = ld8(rs[t], b < nblk ? so + g : OOB) << (8 * g);
+    }
+  }
+}
+
+// bf16 pieces of eight fp32 values: each is the leading eight significant bits
+// of what the earlier ones leave, so hi + mid + lo is the value (truncating
+// keeps the largest finite values finite). An infinity goes into hi alone.
+__device__ __forceinline__ void split3(const float (&x)[8], v8b& hi, v8b& mid, v8b& lo) {
+  u32x4 h, m, l;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t b0[2], b1[2], b2[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float v = x[2 * j + k];
+      b0[k] = __builtin_bit_cast(uint32_t, v);
+      const float vh = __builtin_bit_cast(float, b0[k] & 0xffff0000u);
+      const float r1 = v == vh ? 0.0f : v - vh;
+      b1[k] = __builtin_bit_cast(uint32_t, r1);
+      b2[k] = __builtin_bit_cast(uint32_t, r1 - __builtin_bit_cast(float, b1[k] & 0xffff0000u));
+    }
+    h[j] = perm(b0[1], b0[0], 0x07060302u);   // the upper halves of both
+    m[j] = perm(b1[1], b1[0], 0x07060302u);
+    l[j] = perm(b2[1], b2[0], 0x07060302u);
+  }
+  hi = __builtin_bit_cast(v8b, h);
+  mid = __builtin_bit_cast(v8b, m);
+  lo = __builtin_bit_cast(v8b, l);
+}
+
+template <int XT, int CT, int RT>
+__device__ __forceinline__ void chunk_products(const XChunk<XT, CT>& x, WChunk<RT>& w, int g, v4f (&acc)[RT][CT]) {
+  if constexpr (XT == T_F16) {
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      uint32_t a = w.codes[t].x, b = w.codes[t].y, c = w.codes[t].z, d = w.codes[t].w;
+      transpose_groups(a, b, c, d);
+      const uint32_t e[4] = {a, b, c, d};
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const v8h wb = codes_f16(e[s]);
+        const float sc = scale_value((w.scale[t] >> (8 * s)) & 255u);
+#pragma unroll
+        for (int u = 0; u < CT; ++u) {
+          const v4f p = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, x.v[u][s]), wb,
+                                                               v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[t][u][i] = __builtin_fmaf(sc, p[i], acc[t][u][i]);
+        }
+      }
+    }
+  } else {
+    float sc[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) sc[t] = scale_of((w.scale[t] >> (8 * g)) & 255u);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      v8b wb[RT];
+#pragma unroll
+      for (int t = 0; t < RT; ++t) wb[t] = codes_bf16(w.codes[t][s], sc[t]);
+#pragma unroll
+      for (int u = 0; u < CT; ++u) {
+        if constexpr (XT == T_BF16) {
+          const v8b xa = __builtin_bit_cast(v8b, x.v[u][s]);
+#pragma unroll
+          for (int t = 0; t < RT; ++t)
+            acc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa, wb[t], acc[t][u], 0, 0, 0);
+        } else {
+          float f[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            f[j] = bits_f32(x.v[u][2 * s][j]);
+            f[4 + j] = bits_f32(x.v[u][2 * s + 1][j]);
+          }
+          v8b hi, mid, lo;
+          split3(f, hi, mid, lo);
+#pragma unroll
+          for (int t = 0; t < RT; ++t) {
+            acc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, wb[t], acc[t][u], 0, 0, 0);
+            acc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(mid, wb[t], acc[t][u], 0, 0, 0);
+            acc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, wb[t], acc[t][u], 0, 0, 0);
+          }
+        }
+      }
+    }
+  }
+}
+
+// acc += the products of chunks [c0, c1) (wave-uniform). rc[t], rs[t]: the
+// code and scale rows of tile t (rows past the matrix read zero); xoff: byte
+// offset of the lane's column in rx, OOB for none. U chunks are in flight.
+template <int XT, int CT, int RT, int U, bool AL>
+__device__ __forceinline__ void mx4_tile(const rsrc_t (&rc)[RT], const rsrc_t (&rs)[RT], rsrc_t rx,
+                                         const uint32_t (&xoff)[CT], int nblk, int c0, int c1, v4f (&acc)[RT][CT]) {
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  for (int c = c0; c < c1; c += U) {
+    WChunk<RT> w[U];
+    XChunk<XT, CT> x[U];
+    // chunks past c1 read zero codes
+#pragma unroll
+    for (int u = 0; u < U; ++u) load_w_chunk<XT, RT, AL>(rc, rs, c + u < c1 ? c + u : nblk, nblk, r, g, w[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) load_x_chunk<XT, CT>(rx, xoff, c + u < c1 ? c + u : nblk, nblk, g, x[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) chunk_products<XT, CT, RT>(x[u], w[u], g, acc);
+  }
+}
+
+// Rows [row0, row0 + rows) of the planes of a matrix as buffers.
+__device__ __forceinline__ void mx4_rows(const uint8_t* codes, const uint8_t* scales, int64_t row0, int rows, int nblk,
+                                         rsrc_t& rc, rsrc_t& rs) {
+  rc = make_rsrc(codes + row0 * ((int64_t)nblk * 16), (uint32_t)rows * (uint32_t)nblk * 16u);
+  rs = make_rsrc(scales + row0 * (int64_t)nblk, (uint32_t)rows * (uint32_t)nblk);
+}
+
+}  // namespace kqd

@@ -78,6 +78,9 @@ typedef enum kq_status {
   KQ_ERR_HIP = -6      /* HIP launch/runtime error (message in kq_last_error) */
 } kq_status;
 
+/* Element types of the kq_mx4_* calls and of the router. */
+typedef enum kq_type { KQ_F32 = 0, KQ_F16 = 1, KQ_BF16 = 2 } kq_type;
+
 #define KQ_MAX_M 64            /* activation columns per call */
 #define KQ_MAX_K (1 << 20)     /* inputs per row */
 #define KQ_MAX_N 0x7fffffff    /* output rows per call */
@@ -284,6 +287,131 @@ int kq_gemv_argmax(int fmt, const void* W, const uint16_t* x, float* y,
 #define KQ_NOALLOC_SCRATCH_BYTES (1 << 20)
 int kq_gemv_argmax_noalloc(int fmt, const void* W, const uint16_t* x, float* y,
                            int64_t N, int64_t K, int M, int32_t* out, void* stream);
+
+/* ---- Microscaled 4-bit matrices (MXFP4) ----
+ * Kinetic docs, "Supported models", list MXFP4 among the weights the engine
+ * reads; the pages print no layout. The reading taken is the public OCP
+ * microscaling format: 32 consecutive elements of a row share one scale, a
+ * byte s standing for 2^(s - 127) (255: NaN), and each element is a 4-bit
+ * code: sign, two exponent bits, one mantissa bit, in magnitude 0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6. An element's value is its code times the scale.
+ *
+ * An R x K matrix (K a multiple of 32, at most KQ_MAX_K) is two planes, so
+ * that a row's codes are whole 16-byte pieces and both planes are what the
+ * matrix cores take:
+ *   codes:  uint8 [R][K/2], element 2i of a row in the low nibble of its byte
+ *           i and element 2i + 1 in the high nibble; 16-byte aligned.
+ *   scales: uint8 [R][K/32]; 4-byte aligned.
+ * A matrix has at most KQ_MX4_MAX_ROWS rows. Values whose magnitude reaches
+ * 2^128 (scale byte 254 with codes of 2 and more) count as infinite.
+ *
+ * All matrices of these calls are in device memory. No buffer a call writes
+ * may overlap one it reads. */
+#define KQ_MX4_MAX_ROWS (1 << 25)
+
+/* kq_mx4_quantize — planes of x (device, R rows of K elements of type `type`,
+ * row r starting ldx * r elements after x; ldx >= K). Per block of 32 with
+ * amax its largest magnitude:
+ *   s = clamp(floor(log2(amax)) - 2 + 127, 0, 254) (0 for a block of zeros), so
+ *   the largest element becomes 4 to 6 or is just above 6;
+ *   each code is the nearest to x / 2^(s - 127), the one with an even mantissa
+ *   bit on ties, at most 6 in magnitude; its sign is x's (of zeros too).
+ * A block that holds an infinity or a NaN gets the scale byte 255 and codes 0:
+ * all its values are NaN. The arithmetic is exact up to that rounding, so the
+ * planes do not depend on the kernel.
+ *   x need only be aligned to its elements; rows aligned to 16 bytes are faster.
+ * R == 0 is a valid empty call.
+ * Errors: KQ_ERR_ARG (null, unknown type, R out of range, ldx < K or > 2^35, or
+ * more strided rows than a grid reaches), KQ_ERR_SHAPE, KQ_ERR_ALIGN, KQ_ERR_HIP. */
+int kq_mx4_quantize(int type, const void* x, int64_t ldx, void* codes, void* scales, int64_t R, int64_t K,
+                    void* stream);
+
+/* kq_mx4_dequantize — the values of the planes as elements of type `type`,
+ * row r at ldo * r elements after out. Exact in fp32 and bf16; rounded to
+ * nearest even (infinite past the largest finite value) in fp16.
+ * Arguments otherwise and errors as kq_mx4_quantize. */
+int kq_mx4_dequantize(const void* codes, const void* scales, int type, void* out, int64_t ldo, int64_t R, int64_t K,
+                      void* stream);
+
+/* kq_mx4_gemv — kq_gemv with microscaled weights: y[m][n] = sum_k w[n][k] *
+ * x[m][k] for m < M <= KQ_MAX_M, n < N (Kinetic docs, "What makes it fast":
+ * the few columns of a decode step or verify pass ride on one read of W).
+ *   codes, scales: the planes of the N x K weights.
+ *   x: device, [M][K] of type `type`, 16-byte aligned. y: device, fp32 [M][N].
+ * Weights and activations enter the products exactly (16-bit types as they
+ * are, fp32 as three bf16 pieces holding its 24 bits; pieces below 2^-133 are
+ * dropped); sums are fp32 in a fixed order, so results are deterministic.
+ * M == 0 or N == 0 is a valid empty call.
+ * Errors: KQ_ERR_ARG, KQ_ERR_SHAPE, KQ_ERR_ALIGN, KQ_ERR_HIP. */
+int kq_mx4_gemv(const void* codes, const void* scales, int type, const void* x, float* y, int64_t N, int64_t K, int M,
+                void* stream);
+
+/* kq_mx4_gemm — the product of two microscaled matrices, for prompts and
+ * other passes of many rows: y[m][n] = sum_k a[m][k] * w[n][k].
+ *   a_*: planes of the M x K activations (kq_mx4_quantize), w_*: of the N x K
+ *   weights. y: device, [M][N] of type `type`, rounded once from fp32;
+ *   aligned to 16 bytes.
+ * Products of codes are exact and summed in fp32 in an order fixed by the
+ * shape; sums below 2^-126 in magnitude may be returned as zero.
+ * M == 0 or N == 0 is a valid empty call; M, N <= KQ_MX4_MAX_ROWS.
+ * Errors: as kq_mx4_gemv, and KQ_ERR_ARG where M * N is beyond the grid
+ * (about 2^38). */
+int kq_mx4_gemm(const void* a_codes, const void* a_scales, const void* w_codes, const void* w_scales, int type,
+                void* y, int64_t M, int64_t N, int64_t K, void* stream);
+
+/* ---- The router and the whole mixture-of-experts layer ---- */
+#define KQ_MOE_MAX_EXPERTS 1024
+#define KQ_MOE_MAX_DIM 65536
+
+/* Workspace bytes kq_moe_route needs (negative: the error of an invalid shape). */
+int64_t kq_moe_route_workspace_bytes(int M, int n_experts);
+
+/* kq_moe_route — the experts of each token (kinfer page, "Models bigger than
+ * the machine": a few experts of many per token; the pages do not name the
+ * router, the usual one is the reading taken): with l[e] = sum_k x[m][k] *
+ * W[e][k],
+ *   ids[m]: the top_k experts of largest l, the largest first; the lower index
+ *           first among equals; a NaN counts as minus infinity in this order.
+ *   weights[m][j]: exp(l[ids[m][j]]) over the sum of exp(l) of the chosen
+ *           (renorm 1) or of all experts (renorm 0); where a logit that enters
+ *           the sum is NaN or infinite, the weights are NaN.
+ * Both are as kq_moe_gemv, kq_moe_ffn take them. Logits and softmax are
+ * computed in 64 bits: the choice is that of exact arithmetic unless two
+ * logits agree to about 50 bits.
+ *   x: device, [M][K] of xtype, M <= KQ_MAX_M; W: device, [n_experts][K] of
+ *   wtype, n_experts <= KQ_MOE_MAX_EXPERTS; both 16-byte aligned; K a multiple
+ *   of 32. top_k <= min(n_experts, 64). ids: device int32 [M][top_k]; weights:
+ *   device fp32 [M][top_k]. workspace: device, 16-byte aligned, scratch.
+ * M == 0 is a valid empty call.
+ * Errors: KQ_ERR_ARG, KQ_ERR_SHAPE, KQ_ERR_ALIGN, KQ_ERR_HIP. */
+int kq_moe_route(int xtype, const void* x, int wtype, const void* W, int M, int64_t K, int n_experts, int top_k,
+                 int renorm, int32_t* ids, float* weights, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes kq_mx4_moe_layer needs (negative: the error of an invalid shape). */
+int64_t kq_mx4_moe_layer_workspace_bytes(int64_t hidden, int64_t inter, int M, int top_k, int n_experts);
+
+/* kq_mx4_moe_layer — a whole mixture-of-experts layer for a few tokens:
+ * kq_moe_route, then the chosen experts' gated FFN with microscaled weights
+ * and the weighted sum, with no host synchronisation (only the experts in use
+ * are read, each once per call for all of its tokens):
+ *   for token m, rank j, expert e = ids[m][j]:
+ *     h = silu(Gate_e x_m) * (Up_e x_m), silu(z) = z / (1 + e^-z), in fp32
+ *     y[m] = sum_j weights[m][j] * (Down_e h)
+ *   gate_*, up_*: planes of [n_experts][inter] rows of hidden elements; down_*:
+ *   planes of [n_experts][hidden] rows of inter elements (experts back to back).
+ *   router: device, [n_experts][hidden] of wtype. x: device, [M][hidden] of
+ *   xtype. y: device, fp32 [M][hidden]. ids, weights: written as kq_moe_route
+ *   does. hidden and inter: multiples of 32, at most KQ_MOE_MAX_DIM.
+ * h is not rounded below fp32. Sums are in an order fixed by the shape and the
+ * routes, so results are deterministic. Alignment as kq_moe_route and
+ * kq_mx4_gemv; workspace 16-byte aligned, scratch, not shared by calls that
+ * overlap in time. M == 0 is a valid empty call.
+ * Errors: KQ_ERR_ARG, KQ_ERR_SHAPE, KQ_ERR_ALIGN, KQ_ERR_HIP. */
+int kq_mx4_moe_layer(int xtype, const void* x, int wtype, const void* router, const void* gate_codes,
+                     const void* gate_scales, const void* up_codes, const void* up_scales, const void* down_codes,
+                     const void* down_scales, float* y, int32_t* ids, float* weights, int64_t hidden, int64_t inter,
+                     int M, int top_k, int n_experts, int renorm, void* workspace, int64_t workspace_bytes,
+                     void* stream);
 
 /* ---- Shortlist: an exact argmax that scores only the rows that can win ----
  * Kinetic docs, "What makes it fast" (the Shortlist paragraph): choosing the
