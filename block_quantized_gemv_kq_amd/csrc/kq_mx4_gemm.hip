@@ -99,7 +99,10 @@ __global__ __launch_bounds__(64 * WN * WM) void k_mx4_gemm(const uint8_t* __rest
     for (int i = 0; i < TN; ++i) sw[i] = swn[i];
 #pragma unroll
     for (int j = 0; j < TM; ++j) sa[j] = san[j];
-    __syncthreads();   // this tile's copies have landed, and every wave has read the other buffer
+    // This tile's copies have landed (a barrier alone does not wait for them:
+    // they are loads to the compiler), and every wave has read the other buffer.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
     if (kt + 1 < nkt) {
       stage_codes<BN, THREADS>(rwc, nxt, kt + 1, nblk);
       stage_codes<BM, THREADS>(rac, nxt + BN * 128, kt + 1, nblk);
@@ -175,10 +178,6 @@ int gemm_cfg(const Mx4GemmArgs& a) {
   dispatch_log("k_mx4_gemm", -1, a.N, a.K, (int)a.M, grid, 1, 64 * WN * WM, lds, "type=%d tile=%dx%d", T, BN, BM);
   const bool al = a.K % 128 == 0;
   auto* k = al ? k_mx4_gemm<T, WN, WM, TN, TM, true> : k_mx4_gemm<T, WN, WM, TN, TM, false>;
-  if (lds > 65536) {
-    const int err = (int)hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (err) return err;
-  }
   hipLaunchKernelGGL(k, dim3(grid), dim3(64 * WN * WM), lds, a.stream, a.a_codes, a.a_scales, a.w_codes, a.w_scales,
                      a.y, a.M, a.N, (int)(a.K / 32), (uint32_t)tiles_m);
   return (int)hipGetLastError();
