@@ -156,10 +156,18 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_current_stream = None   # set on first use: torch's current stream of its current device, as an address
+
+
 def _stream(stream) -> int | None:
+    global _current_stream
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _current_stream is None:
+            import torch
+            torch.cuda.current_stream()   # initialises the device
+            raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+            _current_stream = lambda: raw(device())   # noqa: E731  (0.2 us; a Stream object takes 2.8 us)
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -126,12 +126,14 @@ __global__ __launch_bounds__(256) void k_mx4_dequantize(const uint8_t* __restric
 
 // y[m][n] for RT tiles of 16 weight rows and up to 16 CT columns. The waves of
 // a workgroup share the rows and split K; their partial sums meet in LDS and
-// are added in wave order. Dynamic LDS: waves * RT * CT KiB.
+// are added in wave order. Dynamic LDS: waves * region bytes, then (CT 1)
+// or in their place (CT > 1) waves * RT * CT KiB of partial sums.
 template <int XT, int CT, int RT, int U, bool AL>
 __global__ __launch_bounds__(1024) void k_mx4_gemv(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                                                    const void* __restrict__ x, float* __restrict__ y, int N, int K,
                                                    int M, int waves) {
-  extern __shared__ v4f red[];   // [wave][RT][CT][64]
+  extern __shared__ u32x4 lds4[];
+  uint8_t* lds = reinterpret_cast<uint8_t*>(lds4);
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int nblk = K / 32, nchunk = (nblk + 3) / 4;
   const int64_t row0 = (int64_t)blockIdx.x * (16 * RT);
@@ -144,19 +146,17 @@ __global__ __launch_bounds__(1024) void k_mx4_gemv(const uint8_t* __restrict__ c
   }
   const uint32_t xrow = (uint32_t)K * TypeSize<XT>::v;
   const rsrc_t rx = make_rsrc(x, (uint32_t)M * xrow);
-  uint32_t xoff[CT];
-#pragma unroll
-  for (int u = 0; u < CT; ++u) {
-    const int m = 16 * u + (lane & 15);
-    xoff[u] = m < M ? (uint32_t)m * xrow : OOB;
-  }
   v4f acc[RT][CT];
 #pragma unroll
   for (int t = 0; t < RT; ++t)
 #pragma unroll
     for (int u = 0; u < CT; ++u) acc[t][u] = v4f{0.f, 0.f, 0.f, 0.f};
-  const int c0 = (int)((int64_t)nchunk * wave / waves), c1 = (int)((int64_t)nchunk * (wave + 1) / waves);
-  mx4_tile<XT, CT, RT, U, AL>(rc, rs, rx, xoff, nblk, c0, c1, acc);
+  const int c0 = nchunk * wave / waves, c1 = nchunk * (wave + 1) / waves;
+  const int region = x_region_bytes<XT, U>(M);
+  mx4_tile<XT, CT, RT, U, AL>(rc, rs, rx, lds + wave * region, M, [=](int row) { return (uint32_t)row * xrow; }, nblk,
+                              c0, c1, acc);
+  v4f* red = reinterpret_cast<v4f*>(lds + (CT == 1 ? waves * region : 0));   // [wave][RT][CT][64]
+  if constexpr (CT > 1) __syncthreads();   // every wave has read its region
 #pragma unroll
   for (int t = 0; t < RT; ++t)
 #pragma unroll
@@ -242,15 +242,19 @@ int launch_mx4_dequantize(const void* codes, const void* scales, int type, void*
 
 namespace {
 
+constexpr int LDS_BYTES = 160 * 1024;   // of a compute unit
+
 template <int XT, int CT, int RT, int U>
 int gemv_cfg(const Mx4GemvArgs& a) {
   const int nchunk = (int)((a.K / 32 + 3) / 4);
+  const int region = x_region_bytes<XT, U>(a.M), sums = RT * CT * 1024;
+  const int per_wave = CT == 1 ? region + sums : region > sums ? region : sums;
   int waves = (nchunk + U - 1) / U;   // one batch of loads per wave
-  const int most = 64 / (RT * CT) < 16 ? 64 / (RT * CT) : 16;   // LDS: 64 KiB of partial sums
+  const int most = LDS_BYTES / per_wave < 16 ? LDS_BYTES / per_wave : 16;
   waves = waves < 1 ? 1 : waves > most ? most : waves;
   const unsigned grid = (unsigned)((a.N + 16 * RT - 1) / (16 * RT));
-  const size_t lds = (size_t)waves * RT * CT * 1024;
-  dispatch_log("k_mx4_gemv", -1, a.N, a.K, a.M, grid, 1, (unsigned)(64 * waves), lds, "type=%d ct=%d rt=%d", XT, CT, RT);
+  const size_t lds = (size_t)waves * per_wave;
+  dispatch_log("k_mx4_gemv", -1, a.N, a.K, a.M, grid, 1, (unsigned)(64 * waves), lds, "type=%d ct=%d rt=%d u=%d", XT, CT, RT, U);
   if (a.K % 128 == 0)
     hipLaunchKernelGGL((k_mx4_gemv<XT, CT, RT, U, true>), dim3(grid), dim3(64 * waves), lds, a.stream, a.codes,
                        a.scales, a.x, a.y, (int)a.N, (int)a.K, a.M, waves);
@@ -262,8 +266,10 @@ int gemv_cfg(const Mx4GemvArgs& a) {
 
 template <int XT>
 int gemv_type(const Mx4GemvArgs& a) {
-  if (a.M <= 16) return gemv_cfg<XT, 1, 1, XT == T_F32 ? 2 : 4>(a);
-  if (a.M <= 32) return gemv_cfg<XT, 2, 1, XT == T_F32 ? 1 : 2>(a);
+  if (a.M <= 8) return gemv_cfg<XT, 1, 1, XT == T_F32 ? 2 : 4>(a);
+  if (a.M <= 16) return gemv_cfg<XT, 1, 1, XT == T_F32 ? 1 : 2>(a);
+  if (a.M <= 32) return gemv_cfg<XT, 2, 1, 1>(a);
+  if (a.M <= 48) return gemv_cfg<XT, 3, 1, 1>(a);
   return gemv_cfg<XT, 4, 1, 1>(a);
 }
 

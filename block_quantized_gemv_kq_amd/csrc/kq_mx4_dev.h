@@ -98,29 +98,32 @@ __device__ __forceinline__ void transpose_groups(uint32_t& a, uint32_t& b, uint3
 // codes go in unscaled and the scale multiplies each block's fp32 result; for
 // that the codes are transposed among the lane groups first, and matrix
 // instruction s covers the 32 elements of block 4c + s.
-template <int XT, int CT>
-struct XChunk {
-  u32x4 v[CT][XT == T_F32 ? 8 : 4];
-};
+//
+// The columns of a wave's K range come through LDS, in a region of the wave's
+// own (no barrier): loads straight into the operand layout would take 16
+// instructions of 64 scattered 16-byte pieces per chunk and column tile, used
+// or not, against one instruction per KiB of real columns here. A row of the
+// region holds U chunks; its 16-byte piece p lies at p ^ (row & 7), so that
+// the operand reads of eight consecutive rows touch every bank. Lanes whose
+// column does not exist read an existing row: their results are never used.
+template <int XT> struct Pieces { static constexpr int v = 8 * TypeSize<XT>::v; };   // of a row's chunk: 16 or 32
 
-template <int XT, int CT>
-__device__ __forceinline__ void load_x_chunk(rsrc_t rx, const uint32_t (&xoff)[CT], int c, int nblk, int g,
-                                             XChunk<XT, CT>& x) {
-#pragma unroll
-  for (int t = 0; t < CT; ++t) {
-    if constexpr (XT == T_F16) {
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int b = 4 * c + s;
-        x.v[t][s] = ld128(rx, b < nblk ? xoff[t] + (uint32_t)b * 64u + (uint32_t)g * 16u : OOB);
-      }
-    } else {
-      constexpr uint32_t BLK = 32 * TypeSize<XT>::v;
-      const int b = 4 * c + g;
-      const uint32_t o = b < nblk ? xoff[t] + (uint32_t)b * BLK : OOB;
-#pragma unroll
-      for (int s = 0; s < (int)BLK / 16; ++s) x.v[t][s] = ld128(rx, o + 16u * s);
-    }
+// LDS bytes of a wave's region for `rows` columns, U chunks at a time.
+template <int XT, int U>
+__host__ __device__ constexpr int x_region_bytes(int rows) { return (rows * Pieces<XT>::v * U + 63) / 64 * 1024; }
+
+// Copy chunks c.. of `rows` columns into the region; off(row): byte offset of a
+// column in rx. Pieces from `end` (counted along a column) on read zero.
+template <int XT, int U, class Off>
+__device__ __forceinline__ void stage_x(rsrc_t rx, uint8_t* xl, int rows, Off off, int c, int end) {
+  constexpr int PR = Pieces<XT>::v * U;
+  const int lane = threadIdx.x & 63;
+  for (int first = 0; first < rows * PR; first += 64) {
+    const int slot = first + lane, row = slot / PR;
+    const int piece = c * Pieces<XT>::v + ((slot % PR) ^ (row & 7));
+    const uint32_t o = off(row < rows ? row : 0) + 16u * (uint32_t)piece;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void_t*)(xl + first * 16), 16,
+                                             row < rows && piece < end ? o : OOB, 0, 0, 0);
   }
 }
 
@@ -183,24 +186,31 @@ __device__ __forceinline__ void split3(const float (&x)[8], v8b& hi, v8b& mid, v
   lo = __builtin_bit_cast(v8b, l);
 }
 
-template <int XT, int CT, int RT>
-__device__ __forceinline__ void chunk_products(const XChunk<XT, CT>& x, WChunk<RT>& w, int g, v4f (&acc)[RT][CT]) {
+// acc += the products of chunk u of the region. xrow[t]: the region row of the
+// lane's column in column tile t; swz: its row & 7, the same for every t.
+template <int XT, int CT, int RT, int U>
+__device__ __forceinline__ void chunk_products(const uint8_t* (&xrow)[CT], int swz, int u, const WChunk<RT>& w, int g,
+                                               v4f (&acc)[RT][CT]) {
+  const int base = u * Pieces<XT>::v;
   if constexpr (XT == T_F16) {
+    v8h x[4][CT];
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int c = 0; c < CT; ++c) x[s][c] = *reinterpret_cast<const v8h*>(xrow[c] + (base + ((4 * s + g) ^ swz)) * 16);
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      uint32_t a = w.codes[t].x, b = w.codes[t].y, c = w.codes[t].z, d = w.codes[t].w;
-      transpose_groups(a, b, c, d);
-      const uint32_t e[4] = {a, b, c, d};
+      uint32_t e[4] = {w.codes[t].x, w.codes[t].y, w.codes[t].z, w.codes[t].w};
+      transpose_groups(e[0], e[1], e[2], e[3]);
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         const v8h wb = codes_f16(e[s]);
         const float sc = scale_value((w.scale[t] >> (8 * s)) & 255u);
 #pragma unroll
-        for (int u = 0; u < CT; ++u) {
-          const v4f p = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, x.v[u][s]), wb,
-                                                               v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+        for (int c = 0; c < CT; ++c) {
+          const v4f p = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[s][c], wb, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[t][u][i] = __builtin_fmaf(sc, p[i], acc[t][u][i]);
+          for (int i = 0; i < 4; ++i) acc[t][c][i] = __builtin_fmaf(sc, p[i], acc[t][c][i]);
         }
       }
     }
@@ -214,26 +224,22 @@ __device__ __forceinline__ void chunk_products(const XChunk<XT, CT>& x, WChunk<R
 #pragma unroll
       for (int t = 0; t < RT; ++t) wb[t] = codes_bf16(w.codes[t][s], sc[t]);
 #pragma unroll
-      for (int u = 0; u < CT; ++u) {
+      for (int c = 0; c < CT; ++c) {
         if constexpr (XT == T_BF16) {
-          const v8b xa = __builtin_bit_cast(v8b, x.v[u][s]);
+          const v8b x = *reinterpret_cast<const v8b*>(xrow[c] + (base + ((4 * g + s) ^ swz)) * 16);
 #pragma unroll
-          for (int t = 0; t < RT; ++t)
-            acc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa, wb[t], acc[t][u], 0, 0, 0);
+          for (int t = 0; t < RT; ++t) acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, wb[t], acc[t][c], 0, 0, 0);
         } else {
-          float f[8];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            f[j] = bits_f32(x.v[u][2 * s][j]);
-            f[4 + j] = bits_f32(x.v[u][2 * s + 1][j]);
-          }
+          const v4f a = *reinterpret_cast<const v4f*>(xrow[c] + (base + ((8 * g + 2 * s) ^ swz)) * 16);
+          const v4f b = *reinterpret_cast<const v4f*>(xrow[c] + (base + ((8 * g + 2 * s + 1) ^ swz)) * 16);
+          const float f[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
           v8b hi, mid, lo;
           split3(f, hi, mid, lo);
 #pragma unroll
           for (int t = 0; t < RT; ++t) {
-            acc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, wb[t], acc[t][u], 0, 0, 0);
-            acc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(mid, wb[t], acc[t][u], 0, 0, 0);
-            acc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, wb[t], acc[t][u], 0, 0, 0);
+            acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, wb[t], acc[t][c], 0, 0, 0);
+            acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(mid, wb[t], acc[t][c], 0, 0, 0);
+            acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, wb[t], acc[t][c], 0, 0, 0);
           }
         }
       }
@@ -241,23 +247,40 @@ __device__ __forceinline__ void chunk_products(const XChunk<XT, CT>& x, WChunk<R
   }
 }
 
-// acc += the products of chunks [c0, c1) (wave-uniform). rc[t], rs[t]: the
-// code and scale rows of tile t (rows past the matrix read zero); xoff: byte
-// offset of the lane's column in rx, OOB for none. U chunks are in flight.
-template <int XT, int CT, int RT, int U, bool AL>
-__device__ __forceinline__ void mx4_tile(const rsrc_t (&rc)[RT], const rsrc_t (&rs)[RT], rsrc_t rx,
-                                         const uint32_t (&xoff)[CT], int nblk, int c0, int c1, v4f (&acc)[RT][CT]) {
+// acc += the products of chunks [c0, c1) (wave-uniform) with `rows` columns
+// (1 to 16 CT). rc[t], rs[t]: the code and scale rows of tile t (rows past the
+// matrix read zero); xl: the wave's region; off: see stage_x. The weights of
+// the next U chunks are loaded before these are multiplied.
+template <int XT, int CT, int RT, int U, bool AL, class Off>
+__device__ __forceinline__ void mx4_tile(const rsrc_t (&rc)[RT], const rsrc_t (&rs)[RT], rsrc_t rx, uint8_t* xl,
+                                         int rows, Off off, int nblk, int c0, int c1, v4f (&acc)[RT][CT]) {
+  constexpr int PR = Pieces<XT>::v * U;
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const uint8_t* xrow[CT];
+  int swz = 0;
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    const int row = 16 * c + r, have = row < rows ? row : rows > 7 ? row & 7 : 0;
+    xrow[c] = xl + have * (PR * 16);
+    if (c == 0) swz = have & 7;
+  }
+  const int end = min(c1 * Pieces<XT>::v, nblk * (Pieces<XT>::v / 4));
+  WChunk<RT> next[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) load_w_chunk<XT, RT, AL>(rc, rs, c0 + u < c1 ? c0 + u : nblk, nblk, r, g, next[u]);
   for (int c = c0; c < c1; c += U) {
+    stage_x<XT, U>(rx, xl, rows, off, c, end);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the region is filled (and these weights are here)
     WChunk<RT> w[U];
-    XChunk<XT, CT> x[U];
-    // chunks past c1 read zero codes
 #pragma unroll
-    for (int u = 0; u < U; ++u) load_w_chunk<XT, RT, AL>(rc, rs, c + u < c1 ? c + u : nblk, nblk, r, g, w[u]);
+    for (int u = 0; u < U; ++u) w[u] = next[u];
+    if (c + U < c1) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) load_x_chunk<XT, CT>(rx, xoff, c + u < c1 ? c + u : nblk, nblk, g, x[u]);
+      for (int u = 0; u < U; ++u) load_w_chunk<XT, RT, AL>(rc, rs, c + U + u < c1 ? c + U + u : nblk, nblk, r, g, next[u]);
+    }
 #pragma unroll
-    for (int u = 0; u < U; ++u) chunk_products<XT, CT, RT>(x[u], w[u], g, acc);
+    for (int u = 0; u < U; ++u) chunk_products<XT, CT, RT, U>(xrow, swz, u, w[u], g, acc);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the region has been read
   }
 }
 

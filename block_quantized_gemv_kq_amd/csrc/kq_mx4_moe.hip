@@ -204,6 +204,8 @@ __global__ __launch_bounds__(64 * GU_WAVES) void k_mx4_gate_up(const uint8_t* __
                                                               uint16_t* __restrict__ h, int hidden, int inter, int M,
                                                               int top_k) {
   __shared__ v4f red[GU_WAVES][2][64];
+  constexpr int U = XT == T_F32 ? 1 : 2;
+  __shared__ u32x4 xl4[GU_WAVES][x_region_bytes<XT, U>(16) / 16];
   const int a = blockIdx.y;
   if (a >= *G.n_active) return;
   const int lane = threadIdx.x & 63, wave = wave_id();
@@ -219,10 +221,11 @@ __global__ __launch_bounds__(64 * GU_WAVES) void k_mx4_gate_up(const uint8_t* __
   const int64_t plane = (int64_t)M * top_k * inter;
   for (int t0 = 0; t0 < cnt; t0 += 16) {
     if (t0 > 0) __syncthreads();   // the previous pass has read red
-    const int t = t0 + (lane & 15);
-    const uint32_t xoff[1] = {t < cnt ? (uint32_t)(G.list[s0 + t] / top_k) * xrow : OOB};
+    const int t = t0 + (lane & 15), rows = min(16, cnt - t0);
+    const uint32_t xoff = t < cnt ? (uint32_t)(G.list[s0 + t] / top_k) * xrow : 0u;   // of column lane & 15
     v4f acc[2][1] = {{v4f{0.f, 0.f, 0.f, 0.f}}, {v4f{0.f, 0.f, 0.f, 0.f}}};
-    mx4_tile<XT, 1, 2, XT == T_F32 ? 2 : 4, AL>(rc, rs, rx, xoff, nblk, c0, c1, acc);
+    mx4_tile<XT, 1, 2, U, AL>(rc, rs, rx, reinterpret_cast<uint8_t*>(xl4[wave]), rows,
+                              [=](int row) { return (uint32_t)__shfl((int)xoff, row, 64); }, nblk, c0, c1, acc);
     red[wave][0][lane] = acc[0][0];
     red[wave][1][lane] = acc[1][0];
     __syncthreads();
@@ -259,6 +262,8 @@ __global__ __launch_bounds__(64 * DOWN_WAVES) void k_mx4_down(const uint8_t* __r
                                                              const float* __restrict__ weights, float* __restrict__ y,
                                                              int hidden, int inter, int M, int top_k) {
   extern __shared__ float lds_f[];   // [waves][M][16] sums, then [waves][16][16] scratch
+  constexpr int U = 2;
+  __shared__ u32x4 xl4[DOWN_WAVES][x_region_bytes<T_BF16, U>(3 * DOWN_SLOTS) / 16];
   const int lane = threadIdx.x & 63, wave = wave_id();
   float* ys = lds_f + wave * M * 16;
   float* scratch = lds_f + DOWN_WAVES * M * 16 + wave * 256;
@@ -267,30 +272,28 @@ __global__ __launch_bounds__(64 * DOWN_WAVES) void k_mx4_down(const uint8_t* __r
   const int nblk = inter / 32, nchunk = (nblk + 3) / 4;
   const uint32_t hrow = (uint32_t)inter * 2u;
   const rsrc_t rh = make_rsrc(h, 3u * (uint32_t)P * hrow);
-  const int r = lane & 15, piece = r / DOWN_SLOTS, col = r - piece * DOWN_SLOTS;
+  const int r = lane & 15;
   for (int a = wave; a < n_active; a += DOWN_WAVES) {
     const int e = __builtin_amdgcn_readfirstlane(G.expert[a]), s0 = __builtin_amdgcn_readfirstlane(G.start[a]);
     const int cnt = __builtin_amdgcn_readfirstlane(G.start[a + 1]) - s0;
     rsrc_t rc[1], rs[1];
     mx4_rows(dc, ds, (int64_t)e * hidden + blockIdx.x * 16, 16, nblk, rc[0], rs[0]);
     for (int t0 = 0; t0 < cnt; t0 += DOWN_SLOTS) {
-      const int t = t0 + col;
-      const bool on = piece < 3 && t < cnt;
-      const uint32_t xoff[1] = {on ? (uint32_t)(piece * P + G.list[s0 + t]) * hrow : OOB};
+      // column piece * n + m: that piece of h of slot m of this group
+      const int n = min(DOWN_SLOTS, cnt - t0), piece = r / n, m = r - piece * n;
+      const uint32_t xoff = piece < 3 ? (uint32_t)(piece * P + G.list[s0 + t0 + m]) * hrow : 0u;
       v4f acc[1][1] = {{v4f{0.f, 0.f, 0.f, 0.f}}};
-      mx4_tile<T_BF16, 1, 1, 4, AL>(rc, rs, rh, xoff, nblk, 0, nchunk, acc);
+      mx4_tile<T_BF16, 1, 1, U, AL>(rc, rs, rh, reinterpret_cast<uint8_t*>(xl4[wave]), 3 * n,
+                                    [=](int row) { return (uint32_t)__shfl((int)xoff, row, 64); }, nblk, 0, nchunk, acc);
 #pragma unroll
       for (int i = 0; i < 4; ++i) scratch[(4 * (lane >> 4) + i) * 16 + r] = acc[0][0][i];
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
-      for (int i = lane; i < DOWN_SLOTS * 16; i += 64) {
-        const int m = i >> 4, n = i & 15;
-        if (t0 + m < cnt) {
-          const int slot = G.list[s0 + t0 + m];
-          const float v = scratch[(2 * DOWN_SLOTS + m) * 16 + n] + scratch[(DOWN_SLOTS + m) * 16 + n] + scratch[m * 16 + n];
-          float* o = ys + (slot / top_k) * 16 + n;
-          *o = __builtin_fmaf(weights[slot], v, *o);
-        }
+      for (int i = lane; i < n * 16; i += 64) {
+        const int slot = G.list[s0 + t0 + (i >> 4)];
+        const float v = scratch[2 * n * 16 + i] + scratch[n * 16 + i] + scratch[i];
+        float* o = ys + (slot / top_k) * 16 + (i & 15);
+        *o = __builtin_fmaf(weights[slot], v, *o);
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
