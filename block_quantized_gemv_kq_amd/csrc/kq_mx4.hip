@@ -124,39 +124,23 @@ __global__ __launch_bounds__(256) void k_mx4_dequantize(const uint8_t* __restric
   }
 }
 
-// y[m][n] for RT tiles of 16 weight rows and up to 16 CT columns. The waves of
-// a workgroup share the rows and split K; their partial sums meet in LDS and
-// are added in wave order. Dynamic LDS: waves * region bytes, then (CT 1)
-// or in their place (CT > 1) waves * RT * CT KiB of partial sums.
-template <int XT, int CT, int RT, int U, bool AL>
-__global__ __launch_bounds__(1024) void k_mx4_gemv(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                                                   const void* __restrict__ x, float* __restrict__ y, int N, int K,
-                                                   int M, int waves) {
-  extern __shared__ u32x4 lds4[];
-  uint8_t* lds = reinterpret_cast<uint8_t*>(lds4);
-  const int lane = threadIdx.x & 63, wave = wave_id();
-  const int nblk = K / 32, nchunk = (nblk + 3) / 4;
-  const int64_t row0 = (int64_t)blockIdx.x * (16 * RT);
-  rsrc_t rc[RT], rs[RT];
+// Buffers of RT tiles of 16 weight rows from row0 on (rows past N read zero).
+template <int RT>
+__device__ __forceinline__ void mx4_tiles(const uint8_t* codes, const uint8_t* scales, int64_t row0, int N, int nblk,
+                                          rsrc_t (&rc)[RT], rsrc_t (&rs)[RT]) {
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     const int64_t left = (int64_t)N - row0 - 16 * t;
     const int rows = left < 0 ? 0 : left < 16 ? (int)left : 16;
     mx4_rows(codes, scales, rows ? row0 + 16 * t : 0, rows, nblk, rc[t], rs[t]);
   }
-  const uint32_t xrow = (uint32_t)K * TypeSize<XT>::v;
-  const rsrc_t rx = make_rsrc(x, (uint32_t)M * xrow);
-  v4f acc[RT][CT];
-#pragma unroll
-  for (int t = 0; t < RT; ++t)
-#pragma unroll
-    for (int u = 0; u < CT; ++u) acc[t][u] = v4f{0.f, 0.f, 0.f, 0.f};
-  const int c0 = nchunk * wave / waves, c1 = nchunk * (wave + 1) / waves;
-  const int region = x_region_bytes<XT, U>(M);
-  mx4_tile<XT, CT, RT, U, AL>(rc, rs, rx, lds + wave * region, M, [=](int row) { return (uint32_t)row * xrow; }, nblk,
-                              c0, c1, acc);
-  v4f* red = reinterpret_cast<v4f*>(lds + (CT == 1 ? waves * region : 0));   // [wave][RT][CT][64]
-  if constexpr (CT > 1) __syncthreads();   // every wave has read its region
+}
+
+// The waves' partial sums, added in wave order, to y.
+template <int RT, int CT>
+__device__ __forceinline__ void store_sums(const v4f (&acc)[RT][CT], v4f* red, int wave, int waves,
+                                           float* __restrict__ y, int64_t row0, int N, int M) {
+  const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int t = 0; t < RT; ++t)
 #pragma unroll
@@ -174,6 +158,32 @@ __global__ __launch_bounds__(1024) void k_mx4_gemv(const uint8_t* __restrict__ c
       if (m < M) y[(int64_t)m * N + n] = s[j];
     }
   }
+}
+
+// y[m][n] for RT tiles of 16 weight rows and up to 16 CT columns. The waves of
+// a workgroup share the rows and split K; their partial sums meet in LDS and
+// are added in wave order. Dynamic LDS: waves * region bytes, then (CT 1)
+// or in their place (CT > 1) waves * RT * CT KiB of partial sums.
+template <int XT, int CT, int RT, int U, bool AL>
+__global__ __launch_bounds__(1024) void k_mx4_gemv(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+                                                   const void* __restrict__ x, float* __restrict__ y, int N, int K,
+                                                   int M, int waves) {
+  extern __shared__ u32x4 lds4[];
+  uint8_t* lds = reinterpret_cast<uint8_t*>(lds4);
+  const int wave = wave_id();
+  const int nblk = K / 32, nchunk = (nblk + 3) / 4;
+  const int64_t row0 = (int64_t)blockIdx.x * (16 * RT);
+  rsrc_t rc[RT], rs[RT];
+  mx4_tiles<RT>(codes, scales, row0, N, nblk, rc, rs);
+  const uint32_t xrow = (uint32_t)K * TypeSize<XT>::v;
+  const rsrc_t rx = make_rsrc(x, (uint32_t)M * xrow);
+  v4f acc[RT][CT] = {};
+  const int c0 = nchunk * wave / waves, c1 = nchunk * (wave + 1) / waves;
+  const int region = x_region_bytes<XT, U>(M);
+  mx4_tile<XT, CT, RT, U, AL>(rc, rs, rx, lds + wave * region, M, [=](int row) { return (uint32_t)row * xrow; }, nblk,
+                              c0, c1, acc);
+  if constexpr (CT > 1) __syncthreads();   // every wave has read its region
+  store_sums<RT, CT>(acc, reinterpret_cast<v4f*>(lds + (CT == 1 ? waves * region : 0)), wave, waves, y, row0, N, M);
 }
 
 }  // namespace kqd
@@ -251,26 +261,33 @@ int gemv_cfg(const Mx4GemvArgs& a) {
   const int per_wave = CT == 1 ? region + sums : region > sums ? region : sums;
   int waves = (nchunk + U - 1) / U;   // one batch of loads per wave
   const int most = LDS_BYTES / per_wave < 16 ? LDS_BYTES / per_wave : 16;
-  waves = waves < 1 ? 1 : waves > most ? most : waves;
+  waves = waves > most ? most : waves;
   const unsigned grid = (unsigned)((a.N + 16 * RT - 1) / (16 * RT));
   const size_t lds = (size_t)waves * per_wave;
   dispatch_log("k_mx4_gemv", -1, a.N, a.K, a.M, grid, 1, (unsigned)(64 * waves), lds, "type=%d ct=%d rt=%d u=%d", XT, CT, RT, U);
-  if (a.K % 128 == 0)
-    hipLaunchKernelGGL((k_mx4_gemv<XT, CT, RT, U, true>), dim3(grid), dim3(64 * waves), lds, a.stream, a.codes,
-                       a.scales, a.x, a.y, (int)a.N, (int)a.K, a.M, waves);
-  else
-    hipLaunchKernelGGL((k_mx4_gemv<XT, CT, RT, U, false>), dim3(grid), dim3(64 * waves), lds, a.stream, a.codes,
-                       a.scales, a.x, a.y, (int)a.N, (int)a.K, a.M, waves);
+  auto* k = a.K % 128 == 0 ? k_mx4_gemv<XT, CT, RT, U, true> : k_mx4_gemv<XT, CT, RT, U, false>;
+  hipLaunchKernelGGL(k, dim3(grid), dim3(64 * waves), lds, a.stream, a.codes, a.scales, a.x, a.y, (int)a.N, (int)a.K,
+                     a.M, waves);
   return (int)hipGetLastError();
+}
+
+// More than 16 columns: the columns are most of what a workgroup reads, so two
+// row tiles share them where that leaves two workgroups per compute unit (19456
+// x 2560 at 48 columns: 24.6 us against 28.0 with one tile; 2560 x 9728, whose
+// grid it would halve below the compute units: 23.9 against 18.7).
+template <int XT, int CT>
+int gemv_wide(const Mx4GemvArgs& a) {
+  if (a.N >= 32 * 2 * 256) return gemv_cfg<XT, CT, 2, 1>(a);
+  return gemv_cfg<XT, CT, 1, 1>(a);
 }
 
 template <int XT>
 int gemv_type(const Mx4GemvArgs& a) {
   if (a.M <= 8) return gemv_cfg<XT, 1, 1, XT == T_F32 ? 2 : 4>(a);
   if (a.M <= 16) return gemv_cfg<XT, 1, 1, XT == T_F32 ? 1 : 2>(a);
-  if (a.M <= 32) return gemv_cfg<XT, 2, 1, 1>(a);
-  if (a.M <= 48) return gemv_cfg<XT, 3, 1, 1>(a);
-  return gemv_cfg<XT, 4, 1, 1>(a);
+  if (a.M <= 32) return gemv_wide<XT, 2>(a);
+  if (a.M <= 48) return gemv_wide<XT, 3>(a);
+  return gemv_wide<XT, 4>(a);
 }
 
 }  // namespace

@@ -355,7 +355,7 @@ int kq_mx4_gemv(const void* codes, const void* scales, int type, const void* x, 
  * shape; sums below 2^-126 in magnitude may be returned as zero.
  * M == 0 or N == 0 is a valid empty call; M, N <= KQ_MX4_MAX_ROWS.
  * Errors: as kq_mx4_gemv, and KQ_ERR_ARG where M * N is beyond the grid
- * (about 2^38). */
+ * (about 2^35). */
 int kq_mx4_gemm(const void* a_codes, const void* a_scales, const void* w_codes, const void* w_scales, int type,
                 void* y, int64_t M, int64_t N, int64_t K, void* stream);
 

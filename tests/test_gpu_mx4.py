@@ -281,7 +281,10 @@ def test_gemm(kind, M, N, K):
     check(got.reshape(M, N), ref, mags, K, kind, f"{kind} {M}x{N}x{K}")
 
 
-@pytest.mark.parametrize("M,N,K", [(4096, 2048, 96), (2049, 4000, 544), (300, 20001, 256), (20001, 300, 1280)])
+@pytest.mark.parametrize("M,N,K", [(4096, 2048, 96), (2049, 4000, 544), (300, 20001, 256), (20001, 300, 1280),   # 160 x 256 tiles
+                                   (2048, 2560, 160), (1900, 2561, 2592), (2000, 2500, 384),                  # 192 x 128
+                                   (4100, 12000, 96), (4099, 12001, 1184), (4096, 12032, 1280),               # 256 x 256
+                                   (300, 6143, 2592)])                                                        # 64 x 64
 def test_gemm_large(M, N, K):
     """Grids of the large tiles; every result bit for bit where the sums are exact in fp32."""
     t = U.torch_cuda()
