@@ -862,8 +862,8 @@ int kq_mx4_moe_layer(int xtype, const void* x, int wtype, const void* router, co
       return fail(KQ_ERR_ALIGN, "kq_mx4_moe_layer: codes must be 16-byte and scales 4-byte aligned");
   }
   if (!y || !ids || !weights) return fail(KQ_ERR_ARG, "kq_mx4_moe_layer: null pointer");
-  if (!aligned(y, 4) || !aligned(ids, 4) || !aligned(weights, 4))
-    return fail(KQ_ERR_ALIGN, "kq_mx4_moe_layer: y, ids and weights must be 4-byte aligned");
+  if (!aligned(y, 16) || !aligned(ids, 4) || !aligned(weights, 4))
+    return fail(KQ_ERR_ALIGN, "kq_mx4_moe_layer: y must be 16-byte, ids and weights 4-byte aligned");
   const int64_t need = kq::mx4_moe_workspace_bytes(hidden, inter, M, top_k, n_experts);
   if ((st = check_workspace("kq_mx4_moe_layer", workspace, workspace_bytes, need))) return st;
   kq::Mx4MoeArgs a;

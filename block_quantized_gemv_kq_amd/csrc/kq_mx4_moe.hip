@@ -34,7 +34,7 @@ __device__ __forceinline__ void to_f64(const u32x4 (&v)[T == T_F32 ? 2 : 1], dou
   }
 }
 
-constexpr int ROUTE_WAVES = 16, ROUTE_SPLITS = 8;
+constexpr int ROUTE_WAVES = 8, ROUTE_SPLITS = 8;
 
 template <int XT, int WT>
 __global__ __launch_bounds__(64 * ROUTE_WAVES) void k_route_logits(const void* __restrict__ x,
@@ -88,14 +88,32 @@ __device__ __forceinline__ uint64_t logit_key(double v) {
   return (uint64_t)b ^ ((uint64_t)(b >> 63) | 0x8000000000000000ull);
 }
 
-__global__ __launch_bounds__(1024) void k_route_select(const double* __restrict__ part, int splits, int M, int E,
-                                                       int top_k, int renorm, int32_t* __restrict__ ids,
-                                                       float* __restrict__ weights) {
-  __shared__ uint64_t s_key[1024];
-  __shared__ double s_raw[1024];
-  __shared__ int s_id[1024];
-  __shared__ double s_best[64], s_sum[16];
-  const int m = blockIdx.x, e = threadIdx.x, lane = threadIdx.x & 63, wave = wave_id(), waves = blockDim.x >> 6;
+// Scratch of a workgroup's choice, for `waves` waves.
+struct SelectLds {
+  uint64_t* key;    // [waves * top_k]
+  double* raw;      // [waves * top_k]
+  double* best;     // [64]
+  double* sum;      // [16]
+  int* id;          // [waves * top_k]
+  int* chosen;      // [64]
+  __device__ __forceinline__ SelectLds(void* lds, int waves, int top_k) {
+    key = static_cast<uint64_t*>(lds);
+    raw = reinterpret_cast<double*>(key + waves * top_k);
+    best = raw + waves * top_k;
+    sum = best + 64;
+    id = reinterpret_cast<int*>(sum + 16);
+    chosen = id + waves * top_k;
+  }
+};
+__host__ __device__ constexpr int select_lds_bytes(int waves, int top_k) { return waves * top_k * 20 + 64 * 8 + 16 * 8 + 64 * 4; }
+
+// The choice for token m by a workgroup of `waves` waves, at least a thread per
+// expert: S.chosen has it for every thread on return; ids and weights are
+// written where `write` is set.
+__device__ __forceinline__ void select_experts(const double* __restrict__ part, int splits, int m, int M, int E,
+                                               int top_k, int renorm, int waves, const SelectLds& S, bool write,
+                                               int32_t* __restrict__ ids, float* __restrict__ weights) {
+  const int e = threadIdx.x, lane = threadIdx.x & 63, wave = wave_id();
   double raw = 0.0;
   if (e < E) {
     double p[ROUTE_SPLITS];
@@ -108,54 +126,79 @@ __global__ __launch_bounds__(1024) void k_route_select(const double* __restrict_
   }
   const uint64_t key = e < E ? logit_key(raw) : 0ull;
   const uint32_t klo = (uint32_t)key, khi = (uint32_t)(key >> 32);
-  int rank = 0;
-#pragma unroll 8
+  // Upper halves first; whole keys where two of the wave's agree in them.
+  int rank = 0, same = 0;
+#pragma unroll 16
   for (int j = 0; j < 64; ++j) {
-    const uint64_t kj = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)klo, j) |
-                        (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)khi, j) << 32;
-    rank += kj > key || (kj == key && j < lane);
+    const uint32_t hj = (uint32_t)__builtin_amdgcn_readlane((int)khi, j);
+    rank += hj > khi;
+    same += hj == khi;
   }
+  if (__any(e < E && same > 1)) {
+    rank = 0;
+    for (int j = 0; j < 64; ++j) {
+      const uint64_t kj = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)klo, j) |
+                          (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)khi, j) << 32;
+      rank += kj > key || (kj == key && j < lane);
+    }
+  }
+  // lanes past the experts all have key 0 and the same rank: they come after
+  // the experts in lane order
+  if (e >= E && wave * 64 < E) rank = lane;
   if (rank < top_k) {
     const int at = wave * top_k + rank;
-    s_key[at] = key;
-    s_raw[at] = raw;
-    s_id[at] = e;
+    S.key[at] = key;
+    S.raw[at] = raw;
+    S.id[at] = e;
   }
   __syncthreads();
-  const int C = waves * top_k;
-  if (threadIdx.x < (unsigned)C) {
-    const uint64_t mine = s_key[threadIdx.x];
+  const int C = (E + 63) / 64 * top_k;   // waves past the experts have no candidates
+  if ((int)threadIdx.x < C) {
+    const uint64_t mine = S.key[threadIdx.x];
     int at = (int)threadIdx.x;
-    if (waves > 1) {
+    if (C > top_k) {
       at = 0;
+#pragma unroll 8
       for (int j = 0; j < C; ++j) {
-        const uint64_t kj = s_key[j];
+        const uint64_t kj = S.key[j];
         at += kj > mine || (kj == mine && j < (int)threadIdx.x);
       }
     }
     if (at < top_k) {
-      s_best[at] = s_raw[threadIdx.x];
-      ids[m * top_k + at] = s_id[threadIdx.x];
+      S.best[at] = S.raw[threadIdx.x];
+      S.chosen[at] = S.id[threadIdx.x];
     }
   }
   __syncthreads();
-  const double first = s_best[0];
+  if (!write) return;
+  const double first = S.best[0];
   if (!renorm) {
     double p = e < E ? exp(raw - first) : 0.0;
     for (int off = 32; off > 0; off >>= 1) p += __shfl_xor(p, off, 64);
-    if (lane == 0) s_sum[wave] = p;
+    if (lane == 0) S.sum[wave] = p;
     __syncthreads();
   }
   if (wave > 0) return;
-  const double mine = lane < top_k ? exp(s_best[lane] - first) : 0.0;
+  const double mine = lane < top_k ? exp(S.best[lane] - first) : 0.0;
   double sum = 0.0;
   if (renorm) {
     sum = mine;
     for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
   } else {
-    for (int w = 0; w < waves; ++w) sum += s_sum[w];
+    for (int w = 0; w < waves; ++w) sum += S.sum[w];
   }
-  if (lane < top_k) weights[m * top_k + lane] = (float)(mine / sum);
+  if (lane < top_k) {
+    ids[m * top_k + lane] = S.chosen[lane];
+    weights[m * top_k + lane] = (float)(mine / sum);
+  }
+}
+
+__global__ __launch_bounds__(1024) void k_route_select(const double* __restrict__ part, int splits, int M, int E,
+                                                       int top_k, int renorm, int32_t* __restrict__ ids,
+                                                       float* __restrict__ weights) {
+  extern __shared__ u32x4 lds4[];
+  const int waves = blockDim.x >> 6;
+  select_experts(part, splits, blockIdx.x, M, E, top_k, renorm, waves, SelectLds(lds4, waves, top_k), true, ids, weights);
 }
 
 // ---- Slots (token * top_k + rank) of one expert, found by a wave among the P
@@ -194,137 +237,240 @@ __device__ __forceinline__ void split3_one(float v, uint16_t& hi, uint16_t& mid,
 // ---- Gate and up rows of one expert for the tokens routed to it:
 // h[slot][n] = silu(gate_n . x) * (up_n . x), silu(z) = z / (1 + e^-z), kept
 // as three bf16 planes whose sum is the fp32 value (no rounding of h), ready
-// as operands of the down projection. Grid (inter / 16, min(E, P)): row y is
-// expert y, or, with fewer slots than experts, the expert of slot y unless an
-// earlier slot has it. The waves split K and meet in LDS in wave order.
-// Dynamic LDS: ids and list, P uint16 each.
-constexpr int GU_WAVES = 4;
+// as operands of the down projection. Grid (inter / 16 TILES, min(E, P)): row y
+// is expert y, or, with fewer slots than experts, the expert of slot y unless
+// an earlier slot has it. One token: its experts differ, and where a workgroup
+// has a thread per expert (splits > 0) each makes the choice itself, the first
+// one writing ids and weights, which saves a launch between two others.
+// The waves split K; each stages its part of the tokens once and walks TILES
+// tiles of 16 gate and 16 up rows, the next tile's weights in flight. The
+// partial sums meet in LDS in wave order, where the regions were.
+// Dynamic LDS: waves * PER_WAVE, then ids and list (P uint16 each).
+template <int XT> struct GuCols { static constexpr int v = XT == T_F32 ? 4 : 8; };   // columns in a pass
+constexpr int GU_CHUNKS = 4;   // of K in a wave's region
+template <int XT, int TILES>
+struct GateUp {
+  static constexpr int REGION = x_region_bytes<XT, GU_CHUNKS>(GuCols<XT>::v);
+  static constexpr int PER_WAVE = TILES * 2048 > REGION ? TILES * 2048 : REGION;
+  static constexpr int MAX_WAVES = 8;
+};
 
-template <int XT, bool AL>
-__global__ __launch_bounds__(64 * GU_WAVES) void k_mx4_gate_up(const uint8_t* __restrict__ gc, const uint8_t* __restrict__ gs,
-                                                              const uint8_t* __restrict__ uc, const uint8_t* __restrict__ us,
-                                                              const void* __restrict__ x, const int32_t* __restrict__ ids,
-                                                              uint16_t* __restrict__ h, int hidden, int inter, int M,
-                                                              int top_k, int E) {
-  constexpr int US = XT == T_F32 ? 2 : 4, UL = US / 2;   // chunks in flight with up to 8 and up to 16 columns
-  constexpr int REGION = x_region_bytes<XT, US>(8);
-  static_assert(REGION == x_region_bytes<XT, UL>(16), "one region for both");
-  extern __shared__ uint16_t s_ids[];
-  __shared__ v4f red[GU_WAVES][2][64];
-  __shared__ u32x4 xl4[GU_WAVES][REGION / 16];
+template <int XT, int TILES, bool AL>
+__global__ __launch_bounds__((GateUp<XT, TILES>::MAX_WAVES * 64)) void k_mx4_gate_up(const uint8_t* __restrict__ gc, const uint8_t* __restrict__ gs,
+                                                     const uint8_t* __restrict__ uc, const uint8_t* __restrict__ us,
+                                                     const void* __restrict__ x, int32_t* __restrict__ ids,
+                                                     uint16_t* __restrict__ h, int hidden, int inter, int M, int top_k,
+                                                     int E, int waves, const double* __restrict__ part, int splits,
+                                                     int renorm, float* __restrict__ weights) {
+  constexpr int COLS = GuCols<XT>::v, U = GU_CHUNKS, PER_WAVE = GateUp<XT, TILES>::PER_WAVE;
+  extern __shared__ u32x4 lds4[];
+  uint8_t* lds = reinterpret_cast<uint8_t*>(lds4);
+  uint16_t* s_ids = reinterpret_cast<uint16_t*>(lds + waves * PER_WAVE);
   const int P = M * top_k, y = blockIdx.y;
   uint16_t* list = s_ids + P;
-  const int lane = threadIdx.x & 63, wave = wave_id();
-  for (int p = threadIdx.x; p < P; p += 64 * GU_WAVES) s_ids[p] = (uint16_t)ids[p];
-  __syncthreads();
-  const int e = P <= E ? __builtin_amdgcn_readfirstlane(s_ids[y]) : y;
-  if (P <= E && earlier_slot(s_ids, y, e)) return;
-  const int cnt = gather_slots(s_ids, P, e, list);   // every wave writes the same list
-  if (cnt == 0) return;
-  const int nblk = hidden / 32, nchunk = (nblk + 3) / 4;
-  const int64_t row = (int64_t)e * inter + blockIdx.x * 16;
-  rsrc_t rc[2], rs[2];
-  mx4_rows(gc, gs, row, 16, nblk, rc[0], rs[0]);
-  mx4_rows(uc, us, row, 16, nblk, rc[1], rs[1]);
+  const int lane = threadIdx.x & 63, wave = wave_id(), r = lane & 15, g = lane >> 4;
+  int e, cnt;
+  if (M == 1) {
+    if (splits > 0) {
+      const SelectLds S(lds, waves, top_k);
+      select_experts(part, splits, 0, 1, E, top_k, renorm, waves, S, blockIdx.x == 0 && y == 0, ids, weights);
+      e = __builtin_amdgcn_readfirstlane(S.chosen[y]);
+      __syncthreads();   // read before the regions take its place
+    } else {
+      e = __builtin_amdgcn_readfirstlane(ids[y]);
+    }
+    cnt = 1;
+    if (lane == 0) list[0] = (uint16_t)y;   // every wave writes the same
+  } else {
+    for (int p = threadIdx.x; p < P; p += 64 * waves) s_ids[p] = (uint16_t)ids[p];
+    __syncthreads();
+    e = P <= E ? __builtin_amdgcn_readfirstlane(s_ids[y]) : y;
+    if (P <= E && earlier_slot(s_ids, y, e)) return;
+    cnt = gather_slots(s_ids, P, e, list);   // every wave writes the same list
+    if (cnt == 0) return;
+  }
+  const int nblk = hidden / 32, nchunk = (nblk + 3) / 4, tile0 = blockIdx.x * TILES;
   const uint32_t xrow = (uint32_t)hidden * TypeSize<XT>::v;
   const rsrc_t rx = make_rsrc(x, (uint32_t)M * xrow);
-  const int c0 = nchunk * wave / GU_WAVES, c1 = nchunk * (wave + 1) / GU_WAVES;
+  const int c0 = nchunk * wave / waves, c1 = nchunk * (wave + 1) / waves;
   const int64_t plane = (int64_t)P * inter;
-  uint8_t* xl = reinterpret_cast<uint8_t*>(xl4[wave]);
-  for (int t0 = 0; t0 < cnt; t0 += 16) {
-    if (t0 > 0) __syncthreads();   // the previous pass has read red
-    const int t = t0 + (lane & 15), rows = min(16, cnt - t0);
-    const uint32_t xoff = t < cnt ? (uint32_t)(list[t] / top_k) * xrow : 0u;   // of column lane & 15
+  uint8_t* xl = lds + wave * PER_WAVE;
+  for (int t0 = 0; t0 < cnt; t0 += COLS) {
+    if (t0 > 0) __syncthreads();   // the previous pass has read the sums
+    const int cols = min(COLS, cnt - t0);
+    const uint32_t xoff = lane < cols ? (uint32_t)(list[t0 + lane] / top_k) * xrow : 0u;   // of column `lane`
     const auto off = [=](int c) { return (uint32_t)__shfl((int)xoff, c, 64); };
-    v4f acc[2][1] = {{v4f{0.f, 0.f, 0.f, 0.f}}, {v4f{0.f, 0.f, 0.f, 0.f}}};
-    if (rows <= 8) mx4_tile<XT, 1, 2, US, AL>(rc, rs, rx, xl, rows, off, nblk, c0, c1, acc);
-    else mx4_tile<XT, 1, 2, UL, AL>(rc, rs, rx, xl, rows, off, nblk, c0, c1, acc);
-    red[wave][0][lane] = acc[0][0];
-    red[wave][1][lane] = acc[1][0];
+    const int have = r < cols ? r : 0;
+    const uint8_t* xr[1] = {xl + have * (Pieces<XT>::v * U * 16)};
+    v4f acc[TILES][2][1] = {};
+    for (int c = c0; c < c1; c += U) {   // once, unless K is longer than the waves' regions
+      rsrc_t rc[2], rs[2];
+      WChunk<2> next[U];
+#define KQ_LOAD_TILE(T)                                                                             \
+  {                                                                                                 \
+    const int rows = 16 * (tile0 + (T)) < inter ? 16 : 0;                                           \
+    const int64_t row = (int64_t)e * inter + (rows ? 16 * (tile0 + (T)) : 0);                       \
+    mx4_rows(gc, gs, row, rows, nblk, rc[0], rs[0]);                                                \
+    mx4_rows(uc, us, row, rows, nblk, rc[1], rs[1]);                                                \
+    _Pragma("unroll") for (int u = 0; u < U; ++u)                                                   \
+      load_w_chunk<XT, 2, AL>(rc, rs, c + u < c1 ? c + u : nblk, nblk, r, g, next[u]);              \
+  }
+      KQ_LOAD_TILE(0)
+      stage_x<XT, U>(rx, xl, cols, off, c, min(c1 * Pieces<XT>::v, nblk * (Pieces<XT>::v / 4)));
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the region is filled
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) {
+        WChunk<2> w[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) w[u] = next[u];
+        if (t + 1 < TILES) KQ_LOAD_TILE(t + 1)
+#pragma unroll
+        for (int u = 0; u < U; ++u) chunk_products<XT, 1, 2, U>(xr, have & 7, u, w[u], g, acc[t]);
+      }
+#undef KQ_LOAD_TILE
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the region has been read
+    }
+    __syncthreads();   // the sums take the regions' place
+    v4f* red = reinterpret_cast<v4f*>(lds);   // [wave][tile][gate, up][64]
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+      red[((wave * TILES + t) * 2 + 0) * 64 + lane] = acc[t][0][0];
+      red[((wave * TILES + t) * 2 + 1) * 64 + lane] = acc[t][1][0];
+    }
     __syncthreads();
-    // thread: result element i of lane l
-    const int l = threadIdx.x >> 2, i = threadIdx.x & 3;
-    float g = red[0][0][l][i], u = red[0][1][l][i];
-    for (int w = 1; w < GU_WAVES; ++w) g += red[w][0][l][i], u += red[w][1][l][i];
-    const int col = t0 + 4 * (l >> 4) + i;
-    if (col < cnt) {
-      uint16_t* o = h + (int64_t)list[col] * inter + blockIdx.x * 16 + (l & 15);
-      split3_one(g / (1.0f + expf(-g)) * u, o[0], o[plane], o[2 * plane]);
+    for (int j = threadIdx.x; j < TILES * 256; j += 64 * waves) {
+      // result element i of lane l of tile t: column 4 (l >> 4) + i, row l & 15
+      const int i = j & 3, l = (j >> 2) & 63, t = j >> 8, col = 4 * (l >> 4) + i;
+      const int n = 16 * (tile0 + t) + (l & 15);
+      if (col < cols && n < inter) {
+        float gv = 0.f, uv = 0.f;
+        for (int w = 0; w < waves; ++w) {
+          gv += red[((w * TILES + t) * 2 + 0) * 64 + l][i];
+          uv += red[((w * TILES + t) * 2 + 1) * 64 + l][i];
+        }
+        uint16_t* o = h + (int64_t)list[t0 + col] * inter + n;
+        split3_one(gv / (1.0f + expf(-gv)) * uv, o[0], o[plane], o[2 * plane]);
+      }
     }
   }
 }
 
 // ---- Down projection and weighted sum: y[m] = sum_j w[m][j] Down_e h[m][j].
 // A workgroup owns 16 rows of y for every token; its waves take the experts in
-// use in turn (wave w those first named by slots w, w + waves, ...), each into
-// sums of its own in LDS, and the waves' sums are added in wave order, so the
-// result does not depend on timing. Four slots at a time: the operand columns
-// are their three pieces of h (12 of 16).
+// use in turn (of all gridDim.y workgroups' waves, wave w those first named by
+// slots w, w + all waves, ...), each into sums of its own in LDS, and the waves'
+// sums are added in wave order, so the result does not depend on timing. With
+// more than one workgroup for the rows, out is theirs in turn and
+// k_mx4_down_sum adds them. SLOTS slots at a time: the operand columns are
+// their three pieces of h. The weights of the next U chunks, or of the wave's
+// next expert, are in flight while these are multiplied.
 // Dynamic LDS: per wave a region, then per wave M x 16 sums, then the route
 // weights (P fp32), ids (P uint16) and a list of slots per wave (P uint16).
-constexpr int DOWN_SLOTS = 4, DOWN_REGION = x_region_bytes<T_BF16, 2>(3 * DOWN_SLOTS);
-static_assert(DOWN_REGION >= x_region_bytes<T_BF16, 4>(6) && DOWN_REGION >= 1024, "the region serves both widths and the results");
-
-template <bool AL>
+template <int U, int SLOTS, bool AL>
 __global__ __launch_bounds__(1024) void k_mx4_down(const uint8_t* __restrict__ dc, const uint8_t* __restrict__ ds,
                                                   const uint16_t* __restrict__ h, const int32_t* __restrict__ ids,
-                                                  const float* __restrict__ weights, float* __restrict__ y, int hidden,
+                                                  const float* __restrict__ weights, float* __restrict__ out, int hidden,
                                                   int inter, int M, int top_k, int waves) {
+  constexpr int REGION = x_region_bytes<T_BF16, U>(3 * SLOTS), PR = Pieces<T_BF16>::v * U;
+  static_assert(REGION >= 1024, "the region serves the results too");
   extern __shared__ u32x4 lds4[];
-  const int lane = threadIdx.x & 63, wave = wave_id(), P = M * top_k;
-  uint8_t* xl = reinterpret_cast<uint8_t*>(lds4) + wave * DOWN_REGION;
-  float* sums = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(lds4) + waves * DOWN_REGION);
+  const int lane = threadIdx.x & 63, wave = wave_id(), P = M * top_k, r = lane & 15, g = lane >> 4;
+  uint8_t* xl = reinterpret_cast<uint8_t*>(lds4) + wave * REGION;
+  float* sums = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(lds4) + waves * REGION);
   float* ys = sums + wave * M * 16;
   float* s_w = sums + waves * M * 16;
   uint16_t* s_ids = reinterpret_cast<uint16_t*>(s_w + P);
   uint16_t* list = s_ids + P + wave * P;
-  for (int p = threadIdx.x; p < P; p += 64 * waves) {
-    s_ids[p] = (uint16_t)ids[p];
-    s_w[p] = weights[p];
-  }
-  for (int i = lane; i < M * 16; i += 64) ys[i] = 0.0f;
-  __syncthreads();
   const int nblk = inter / 32, nchunk = (nblk + 3) / 4;
   const uint32_t hrow = (uint32_t)inter * 2u;
   const rsrc_t rh = make_rsrc(h, 3u * (uint32_t)P * hrow);
-  const int r = lane & 15;
-  for (int p = wave; p < P; p += waves) {
-    const int e = __builtin_amdgcn_readfirstlane(s_ids[p]);
-    if (earlier_slot(s_ids, p, e)) continue;
+  WChunk<1> next[U];
+#define KQ_LOAD(EXPERT, C)                                                                             \
+  {                                                                                                    \
+    rsrc_t rc[1], rs[1];                                                                               \
+    mx4_rows(dc, ds, (int64_t)(EXPERT) * hidden + blockIdx.x * 16, 16, nblk, rc[0], rs[0]);            \
+    _Pragma("unroll") for (int u = 0; u < U; ++u)                                                      \
+      load_w_chunk<T_BF16, 1, AL>(rc, rs, (C) + u < nchunk ? (C) + u : nblk, nblk, r, g, next[u]);     \
+  }
+  const int all = waves * (int)gridDim.y;
+  int p = (int)blockIdx.y * waves + wave, e = p < P ? __builtin_amdgcn_readfirstlane(ids[p]) : 0;
+  if (M == 1 && p < P) KQ_LOAD(e, 0)
+  for (int i = threadIdx.x; i < P; i += 64 * waves) {
+    s_ids[i] = (uint16_t)ids[i];
+    s_w[i] = weights[i];
+  }
+  for (int i = lane; i < M * 16; i += 64) ys[i] = 0.0f;
+  __syncthreads();
+  if (M > 1) {   // (one token's experts differ)
+    while (p < P && earlier_slot(s_ids, p, e)) {
+      p += all;
+      e = p < P ? __builtin_amdgcn_readfirstlane(s_ids[p]) : 0;
+    }
+    if (p < P) KQ_LOAD(e, 0)
+  }
+  while (p < P) {
     const int cnt = gather_slots(s_ids, P, e, list);
-    rsrc_t rc[1], rs[1];
-    mx4_rows(dc, ds, (int64_t)e * hidden + blockIdx.x * 16, 16, nblk, rc[0], rs[0]);
-    for (int t0 = 0; t0 < cnt; t0 += DOWN_SLOTS) {
+    int pn = p + all, en = 0;
+    for (; pn < P; pn += all) {
+      en = __builtin_amdgcn_readfirstlane(s_ids[pn]);
+      if (!earlier_slot(s_ids, pn, en)) break;
+    }
+    for (int t0 = 0; t0 < cnt; t0 += SLOTS) {
       // column piece * n + m: that piece of h of slot m of this group
-      const int n = min(DOWN_SLOTS, cnt - t0), piece = r / n, m = r - piece * n;
+      const int n = min(SLOTS, cnt - t0), piece = r / n, m = r - piece * n;
       const uint32_t xoff = piece < 3 ? (uint32_t)(piece * P + list[t0 + m]) * hrow : 0u;
       const auto off = [=](int row) { return (uint32_t)__shfl((int)xoff, row, 64); };
-      v4f acc[1][1] = {{v4f{0.f, 0.f, 0.f, 0.f}}};
-      if (n <= 2) mx4_tile<T_BF16, 1, 1, 4, AL>(rc, rs, rh, xl, 3 * n, off, nblk, 0, nchunk, acc);
-      else mx4_tile<T_BF16, 1, 1, 2, AL>(rc, rs, rh, xl, 3 * n, off, nblk, 0, nchunk, acc);
-      // the results take the region's place, 16 rows (columns of h) of 16
-      float* out = reinterpret_cast<float*>(xl);
+      const int have = piece < 3 ? r : 0;
+      const uint8_t* xr[1] = {xl + have * (PR * 16)};
+      v4f acc[1][1] = {};
+      for (int c = 0; c < nchunk; c += U) {
+        stage_x<T_BF16, U>(rh, xl, 3 * n, off, c, nblk * (Pieces<T_BF16>::v / 4));
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the region is filled (and these weights are here)
+        WChunk<1> w[U];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) out[(4 * (lane >> 4) + i) * 16 + r] = acc[0][0][i];
+        for (int u = 0; u < U; ++u) w[u] = next[u];
+        const bool more = c + U < nchunk, again = t0 + SLOTS < cnt;
+        if (more || again || pn < P) KQ_LOAD(more || again ? e : en, more ? c + U : 0)
+#pragma unroll
+        for (int u = 0; u < U; ++u) chunk_products<T_BF16, 1, 1, U>(xr, have & 7, u, w[u], g, acc);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the region has been read
+      }
+      // the results take the region's place, 16 rows (columns of h) of 16
+      float* res = reinterpret_cast<float*>(xl);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) res[(4 * g + i) * 16 + r] = acc[0][0][i];
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
-      if (lane < n * 16) {
-        const int slot = list[t0 + (lane >> 4)];
-        const float v = out[2 * n * 16 + lane] + out[n * 16 + lane] + out[lane];
-        float* o = ys + (slot / top_k) * 16 + r;
+      for (int i = lane; i < n * 16; i += 64) {
+        const int slot = list[t0 + (i >> 4)];
+        const float v = res[2 * n * 16 + i] + res[n * 16 + i] + res[i];
+        float* o = ys + (slot / top_k) * 16 + (i & 15);
         *o = __builtin_fmaf(s_w[slot], v, *o);
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read before the next copies land there
     }
+    p = pn;
+    e = en;
   }
+#undef KQ_LOAD
   __syncthreads();
   for (int i = threadIdx.x; i < M * 16; i += 64 * waves) {
     float s = sums[i];
     for (int w = 1; w < waves; ++w) s += sums[w * M * 16 + i];
-    y[(int64_t)(i >> 4) * hidden + blockIdx.x * 16 + (i & 15)] = s;
+    out[((int64_t)blockIdx.y * M + (i >> 4)) * hidden + blockIdx.x * 16 + (i & 15)] = s;
   }
+}
+
+// y = the parts' sum in their order, four values a thread (hidden % 32 == 0).
+__global__ __launch_bounds__(256) void k_mx4_down_sum(const v4f* __restrict__ parts, v4f* __restrict__ y, int n4,
+                                                      int count) {
+  const int i = (int)blockIdx.x * 256 + (int)threadIdx.x;
+  if (i >= n4) return;
+  v4f s = parts[i];
+  for (int z = 1; z < count; ++z) s += parts[(int64_t)z * n4 + i];
+  y[i] = s;
 }
 
 }  // namespace kqd
@@ -361,14 +507,24 @@ int logits_x(const RouteArgs& a, double* part) {
 
 int64_t route_workspace_bytes(int M, int E) { return (int64_t)ROUTE_SPLITS * M * E * 8; }
 
+namespace {
+
+int launch_logits(const RouteArgs& a) {
+  double* part = static_cast<double*>(a.ws);
+  return a.xtype == KQ_F32 ? logits_x<T_F32>(a, part) : a.xtype == KQ_F16 ? logits_x<T_F16>(a, part) : logits_x<T_BF16>(a, part);
+}
+
+}  // namespace
+
 int launch_route(const RouteArgs& a) {
   double* part = static_cast<double*>(a.ws);
-  const int err = a.xtype == KQ_F32 ? logits_x<T_F32>(a, part) : a.xtype == KQ_F16 ? logits_x<T_F16>(a, part) : logits_x<T_BF16>(a, part);
+  const int err = launch_logits(a);
   if (err) return err;
   int threads = 64;   // a thread per expert, whole waves in a power of two
   while (threads < a.E) threads *= 2;
-  dispatch_log("k_route_select", -1, a.E, a.K, a.M, (unsigned)a.M, 1, (unsigned)threads, 0, "top_k=%d", a.top_k);
-  hipLaunchKernelGGL(k_route_select, dim3((unsigned)a.M), dim3((unsigned)threads), 0, a.stream, part, route_splits(a.K),
+  const size_t lds = (size_t)select_lds_bytes(threads / 64, a.top_k);
+  dispatch_log("k_route_select", -1, a.E, a.K, a.M, (unsigned)a.M, 1, (unsigned)threads, lds, "top_k=%d", a.top_k);
+  hipLaunchKernelGGL(k_route_select, dim3((unsigned)a.M), dim3((unsigned)threads), lds, a.stream, part, route_splits(a.K),
                      a.M, a.E, a.top_k, a.renorm, a.ids, a.weights);
   return (int)hipGetLastError();
 }
@@ -377,53 +533,91 @@ namespace {
 
 constexpr int MOE_LDS_BYTES = 160 * 1024;   // of a compute unit
 
+// One token's experts are chosen in the gate and up kernel where a workgroup of
+// up to 8 waves has a thread per expert.
+bool chooses_itself(const Mx4MoeArgs& a) {
+  return a.route.M == 1 && a.route.E <= 512 && (a.inter / 32) * a.route.top_k < 512;
+}
+
+template <int XT, int TILES>
+int gate_up_cfg(const Mx4MoeArgs& a, uint16_t* h) {
+  typedef GateUp<XT, TILES> G;
+  constexpr int U = GU_CHUNKS;
+  const RouteArgs& r = a.route;
+  const int P = r.M * r.top_k, nchunk = (int)((r.K / 32 + 3) / 4);
+  int waves = (nchunk + U - 1) / U;   // a wave's part of K in its region, while the waves last
+  waves = waves > G::MAX_WAVES ? G::MAX_WAVES : waves;
+  const int splits = chooses_itself(a) ? route_splits(r.K) : 0;
+  if (splits)   // a thread per expert, and the choice's scratch
+    while (waves * 64 < r.E || waves * G::PER_WAVE < select_lds_bytes(waves, r.top_k)) ++waves;
+  const dim3 grid((unsigned)((a.inter / 16 + TILES - 1) / TILES), (unsigned)(P < r.E ? P : r.E));
+  const size_t lds = (size_t)waves * G::PER_WAVE + (size_t)P * 4;
+  dispatch_log("k_mx4_gate_up", -1, a.inter, r.K, r.M, grid.x, grid.y, (unsigned)(64 * waves), lds, "type=%d tiles=%d chooses=%d", XT, TILES, splits > 0);
+  auto* k = r.K % 128 == 0 ? k_mx4_gate_up<XT, TILES, true> : k_mx4_gate_up<XT, TILES, false>;
+  hipLaunchKernelGGL(k, grid, dim3((unsigned)(64 * waves)), lds, r.stream, a.codes[0], a.scales[0], a.codes[1],
+                     a.scales[1], r.x, r.ids, h, (int)r.K, (int)a.inter, r.M, r.top_k, r.E, waves,
+                     static_cast<const double*>(r.ws), splits, r.renorm, r.weights);
+  return (int)hipGetLastError();
+}
+
+// Two tiles per workgroup spread what a workgroup does once over more rows
+// where the slots still fill the compute units (16 tokens, 128 experts of 768 x
+// 2048, top 8: 42.7 us against 48.2 with one and 50.5 with four).
 template <int XT>
 int gate_up_x(const Mx4MoeArgs& a, uint16_t* h) {
+  const int P = a.route.M * a.route.top_k;
+  return (a.inter / 32) * (P < a.route.E ? P : a.route.E) >= 512 ? gate_up_cfg<XT, 2>(a, h) : gate_up_cfg<XT, 1>(a, h);
+}
+
+// Workgroups that share the down projection's rows: with many slots one
+// workgroup per 16 rows leaves compute units idle and each reads all of h.
+constexpr int DOWN_PARTS = 4;
+int down_parts(int P) { return P >= 64 ? DOWN_PARTS : 1; }
+
+template <int U, int SLOTS>
+int down_cfg(const Mx4MoeArgs& a, const uint16_t* h, float* parts, int count) {
   const RouteArgs& r = a.route;
   const int P = r.M * r.top_k;
-  const dim3 grid((unsigned)(a.inter / 16), (unsigned)(P < r.E ? P : r.E));
-  const size_t lds = (size_t)P * 4;
-  dispatch_log("k_mx4_gate_up", -1, a.inter, r.K, r.M, grid.x, grid.y, 64 * GU_WAVES, lds, "type=%d", XT);
-#define KQ_LAUNCH(AL)                                                                                            \
-  hipLaunchKernelGGL((k_mx4_gate_up<XT, AL>), grid, dim3(64 * GU_WAVES), lds, r.stream, a.codes[0], a.scales[0], \
-                     a.codes[1], a.scales[1], r.x, r.ids, h, (int)r.K, (int)a.inter, r.M, r.top_k, r.E)
-  if (r.K % 128 == 0) KQ_LAUNCH(true);
-  else KQ_LAUNCH(false);
-#undef KQ_LAUNCH
+  // a wave per slot up to what LDS holds; two workgroups to a compute unit where there are parts
+  const int shared = P * 6, per_wave = x_region_bytes<T_BF16, U>(3 * SLOTS) + r.M * 64 + P * 2;
+  int waves = (MOE_LDS_BYTES / (count > 1 ? 2 : 1) - shared) / per_wave;
+  const int most = count > 1 ? 8 : 16;
+  waves = waves > most ? most : waves < 1 ? 1 : waves;
+  waves = waves > P ? P : waves;
+  const dim3 grid((unsigned)(r.K / 16), (unsigned)count);
+  const size_t lds = (size_t)(shared + waves * per_wave);
+  dispatch_log("k_mx4_down", -1, r.K, a.inter, r.M, grid.x, grid.y, (unsigned)(64 * waves), lds, "u=%d slots=%d", U, SLOTS);
+  auto* k = a.inter % 128 == 0 ? k_mx4_down<U, SLOTS, true> : k_mx4_down<U, SLOTS, false>;
+  hipLaunchKernelGGL(k, grid, dim3((unsigned)(64 * waves)), lds, r.stream, a.codes[2], a.scales[2], h, r.ids,
+                     r.weights, count > 1 ? parts : a.y, (int)r.K, (int)a.inter, r.M, r.top_k, waves);
+  int err = (int)hipGetLastError();
+  if (err || count == 1) return err;
+  const int n4 = (int)(r.M * r.K / 4);
+  dispatch_log("k_mx4_down_sum", -1, r.K, a.inter, r.M, (unsigned)((n4 + 255) / 256), 1, 256, 0, "parts=%d", count);
+  hipLaunchKernelGGL(k_mx4_down_sum, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, r.stream,
+                     reinterpret_cast<const v4f*>(parts), reinterpret_cast<v4f*>(a.y), n4, count);
   return (int)hipGetLastError();
 }
 
 }  // namespace
 
-// The logits' parts, then the three planes of h.
+// The logits' parts, the three planes of h, the parts of y (where there are any).
 int64_t mx4_moe_workspace_bytes(int64_t hidden, int64_t inter, int M, int top_k, int E) {
-  (void)hidden;
-  return up256(route_workspace_bytes(M, E)) + 3 * (int64_t)M * top_k * inter * 2;
+  const int64_t P = (int64_t)M * top_k, parts = down_parts((int)P);
+  return up256(route_workspace_bytes(M, E)) + up256(3 * P * inter * 2) + (parts > 1 ? parts * M * hidden * 4 : 0);
 }
 
 int launch_mx4_moe(const Mx4MoeArgs& a) {
   const RouteArgs& r = a.route;
-  uint16_t* h = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(r.ws) + up256(route_workspace_bytes(r.M, r.E)));
-  int err = launch_route(r);
+  const int P = r.M * r.top_k;
+  uint8_t* ws = static_cast<uint8_t*>(r.ws) + up256(route_workspace_bytes(r.M, r.E));
+  uint16_t* h = reinterpret_cast<uint16_t*>(ws);
+  float* parts = reinterpret_cast<float*>(ws + up256(3 * (int64_t)P * a.inter * 2));
+  int err = chooses_itself(a) ? launch_logits(r) : launch_route(r);
   if (err) return err;
   err = r.xtype == KQ_F32 ? gate_up_x<T_F32>(a, h) : r.xtype == KQ_F16 ? gate_up_x<T_F16>(a, h) : gate_up_x<T_BF16>(a, h);
   if (err) return err;
-  const int P = r.M * r.top_k;
-  // a wave per slot up to what LDS holds
-  const int shared = P * 6, per_wave = DOWN_REGION + r.M * 64 + P * 2;
-  int waves = (MOE_LDS_BYTES - shared) / per_wave;
-  waves = waves > 16 ? 16 : waves;
-  waves = waves > P ? P : waves;
-  const unsigned grid = (unsigned)(r.K / 16);
-  const size_t lds = (size_t)(shared + waves * per_wave);
-  dispatch_log("k_mx4_down", -1, r.K, a.inter, r.M, grid, 1, (unsigned)(64 * waves), lds, "top_k=%d", r.top_k);
-#define KQ_LAUNCH(AL)                                                                                            \
-  hipLaunchKernelGGL(k_mx4_down<AL>, dim3(grid), dim3((unsigned)(64 * waves)), lds, r.stream, a.codes[2],        \
-                     a.scales[2], h, r.ids, r.weights, a.y, (int)r.K, (int)a.inter, r.M, r.top_k, waves)
-  if (a.inter % 128 == 0) KQ_LAUNCH(true);
-  else KQ_LAUNCH(false);
-#undef KQ_LAUNCH
-  return (int)hipGetLastError();
+  return r.M == 1 ? down_cfg<6, 1>(a, h, parts, 1) : down_cfg<3, 3>(a, h, parts, down_parts(P));
 }
 
 }  // namespace kq

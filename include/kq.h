@@ -400,8 +400,8 @@ int64_t kq_mx4_moe_layer_workspace_bytes(int64_t hidden, int64_t inter, int M, i
  *   gate_*, up_*: planes of [n_experts][inter] rows of hidden elements; down_*:
  *   planes of [n_experts][hidden] rows of inter elements (experts back to back).
  *   router: device, [n_experts][hidden] of wtype. x: device, [M][hidden] of
- *   xtype. y: device, fp32 [M][hidden]. ids, weights: written as kq_moe_route
- *   does. hidden and inter: multiples of 32, at most KQ_MOE_MAX_DIM.
+ *   xtype. y: device, fp32 [M][hidden], 16-byte aligned. ids, weights: written
+ *   as kq_moe_route does. hidden and inter: multiples of 32, at most KQ_MOE_MAX_DIM.
  * h is not rounded below fp32. Sums are in an order fixed by the shape and the
  * routes, so results are deterministic. Alignment as kq_moe_route and
  * kq_mx4_gemv; workspace 16-byte aligned, scratch, not shared by calls that
