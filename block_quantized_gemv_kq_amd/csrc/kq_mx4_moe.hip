@@ -223,6 +223,17 @@ __device__ __forceinline__ bool earlier_slot(const uint16_t* ids, int p, int e) 
   return false;
 }
 
+// The down projection takes up to DOWN_SLOTS slots of an expert at a time. The
+// first of each group leads it: its entry of `groups` has the group's size in
+// the upper half, others 0; the lower half is the next slot with the expert.
+constexpr int DOWN_SLOTS = 3;
+__device__ __forceinline__ void write_groups(const uint16_t* list, int cnt, int32_t* __restrict__ groups) {
+  for (int t = threadIdx.x & 63; t < cnt; t += 64) {
+    const int size = t % DOWN_SLOTS == 0 ? min(DOWN_SLOTS, cnt - t) : 0;
+    groups[list[t]] = size << 16 | (t + 1 < cnt ? list[t + 1] : 0);
+  }
+}
+
 // Three bf16 pieces of an fp32 value (as split3).
 __device__ __forceinline__ void split3_one(float v, uint16_t& hi, uint16_t& mid, uint16_t& lo) {
   const uint32_t b0 = __builtin_bit_cast(uint32_t, v);
@@ -237,8 +248,8 @@ __device__ __forceinline__ void split3_one(float v, uint16_t& hi, uint16_t& mid,
 // ---- Gate and up rows of one expert for the tokens routed to it:
 // h[slot][n] = silu(gate_n . x) * (up_n . x), silu(z) = z / (1 + e^-z), kept
 // as three bf16 planes whose sum is the fp32 value (no rounding of h), ready
-// as operands of the down projection. Grid (inter / 16 TILES, min(E, P)): row y
-// is expert y, or, with fewer slots than experts, the expert of slot y unless
+// as operands of the down projection. Grid (inter / 16 TILES, min(E, P), Z):
+// workgroup z takes the expert's passes of columns z, z + Z, ...; row y is expert y, or, with fewer slots than experts, the expert of slot y unless
 // an earlier slot has it. One token: its experts differ, and where a workgroup
 // has a thread per expert (splits > 0) each makes the choice itself, the first
 // one writing ids and weights, which saves a launch between two others.
@@ -261,7 +272,8 @@ __global__ __launch_bounds__((GateUp<XT, TILES>::MAX_WAVES * 64)) void k_mx4_gat
                                                      const void* __restrict__ x, int32_t* __restrict__ ids,
                                                      uint16_t* __restrict__ h, int hidden, int inter, int M, int top_k,
                                                      int E, int waves, const double* __restrict__ part, int splits,
-                                                     int renorm, float* __restrict__ weights) {
+                                                     int renorm, float* __restrict__ weights,
+                                                     int32_t* __restrict__ groups) {
   constexpr int COLS = GuCols<XT>::v, U = GU_CHUNKS, PER_WAVE = GateUp<XT, TILES>::PER_WAVE;
   extern __shared__ u32x4 lds4[];
   uint8_t* lds = reinterpret_cast<uint8_t*>(lds4);
@@ -289,14 +301,15 @@ __global__ __launch_bounds__((GateUp<XT, TILES>::MAX_WAVES * 64)) void k_mx4_gat
     cnt = gather_slots(s_ids, P, e, list);   // every wave writes the same list
     if (cnt == 0) return;
   }
+  if (blockIdx.x == 0 && blockIdx.z == 0 && wave == 0) write_groups(list, cnt, groups);
   const int nblk = hidden / 32, nchunk = (nblk + 3) / 4, tile0 = blockIdx.x * TILES;
   const uint32_t xrow = (uint32_t)hidden * TypeSize<XT>::v;
   const rsrc_t rx = make_rsrc(x, (uint32_t)M * xrow);
   const int c0 = nchunk * wave / waves, c1 = nchunk * (wave + 1) / waves;
   const int64_t plane = (int64_t)P * inter;
   uint8_t* xl = lds + wave * PER_WAVE;
-  for (int t0 = 0; t0 < cnt; t0 += COLS) {
-    if (t0 > 0) __syncthreads();   // the previous pass has read the sums
+  for (int t0 = COLS * (int)blockIdx.z; t0 < cnt; t0 += COLS * (int)gridDim.z) {
+    if (t0 >= COLS * (int)gridDim.z) __syncthreads();   // the previous pass has read the sums
     const int cols = min(COLS, cnt - t0);
     const uint32_t xoff = lane < cols ? (uint32_t)(list[t0 + lane] / top_k) * xrow : 0u;   // of column `lane`
     const auto off = [=](int c) { return (uint32_t)__shfl((int)xoff, c, 64); };
@@ -357,20 +370,21 @@ __global__ __launch_bounds__((GateUp<XT, TILES>::MAX_WAVES * 64)) void k_mx4_gat
 
 // ---- Down projection and weighted sum: y[m] = sum_j w[m][j] Down_e h[m][j].
 // A workgroup owns 16 rows of y for every token; its waves take the experts in
-// use in turn (of all gridDim.y workgroups' waves, wave w those first named by
-// slots w, w + all waves, ...), each into sums of its own in LDS, and the waves'
-// sums are added in wave order, so the result does not depend on timing. With
-// more than one workgroup for the rows, out is theirs in turn and
-// k_mx4_down_sum adds them. SLOTS slots at a time: the operand columns are
-// their three pieces of h. The weights of the next U chunks, or of the wave's
-// next expert, are in flight while these are multiplied.
+// use in turn, up to SLOTS slots of one at a time (of all gridDim.y workgroups'
+// waves, wave w the groups led by slots w, w + all waves, ...), each into sums
+// of its own in LDS, and the waves' sums are added in wave order, so the result
+// does not depend on timing. With more than one workgroup for the rows, out is
+// theirs in turn and k_mx4_down_sum adds them. The operand columns are the
+// three pieces of h of a group's slots. The weights of the next U chunks, or of
+// the wave's next group, are in flight while these are multiplied.
 // Dynamic LDS: per wave a region, then per wave M x 16 sums, then the route
-// weights (P fp32), ids (P uint16) and a list of slots per wave (P uint16).
+// weights (P fp32), groups (P int32) and ids (P uint16).
 template <int U, int SLOTS, bool AL>
 __global__ __launch_bounds__(1024) void k_mx4_down(const uint8_t* __restrict__ dc, const uint8_t* __restrict__ ds,
                                                   const uint16_t* __restrict__ h, const int32_t* __restrict__ ids,
-                                                  const float* __restrict__ weights, float* __restrict__ out, int hidden,
-                                                  int inter, int M, int top_k, int waves) {
+                                                  const float* __restrict__ weights,
+                                                  const int32_t* __restrict__ groups, float* __restrict__ out,
+                                                  int hidden, int inter, int M, int top_k, int waves) {
   constexpr int REGION = x_region_bytes<T_BF16, U>(3 * SLOTS), PR = Pieces<T_BF16>::v * U;
   static_assert(REGION >= 1024, "the region serves the results too");
   extern __shared__ u32x4 lds4[];
@@ -379,8 +393,8 @@ __global__ __launch_bounds__(1024) void k_mx4_down(const uint8_t* __restrict__ d
   float* sums = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(lds4) + waves * REGION);
   float* ys = sums + wave * M * 16;
   float* s_w = sums + waves * M * 16;
-  uint16_t* s_ids = reinterpret_cast<uint16_t*>(s_w + P);
-  uint16_t* list = s_ids + P + wave * P;
+  int32_t* s_groups = reinterpret_cast<int32_t*>(s_w + P);
+  uint16_t* s_ids = reinterpret_cast<uint16_t*>(s_groups + P);
   const int nblk = inter / 32, nchunk = (nblk + 3) / 4;
   const uint32_t hrow = (uint32_t)inter * 2u;
   const rsrc_t rh = make_rsrc(h, 3u * (uint32_t)P * hrow);
@@ -394,31 +408,36 @@ __global__ __launch_bounds__(1024) void k_mx4_down(const uint8_t* __restrict__ d
   }
   const int all = waves * (int)gridDim.y;
   int p = (int)blockIdx.y * waves + wave, e = p < P ? __builtin_amdgcn_readfirstlane(ids[p]) : 0;
-  if (M == 1 && p < P) KQ_LOAD(e, 0)
+  if (M == 1 && p < P) KQ_LOAD(e, 0)   // one token's experts differ: every slot leads
   for (int i = threadIdx.x; i < P; i += 64 * waves) {
     s_ids[i] = (uint16_t)ids[i];
     s_w[i] = weights[i];
+    s_groups[i] = groups[i];
   }
   for (int i = lane; i < M * 16; i += 64) ys[i] = 0.0f;
   __syncthreads();
-  if (M > 1) {   // (one token's experts differ)
-    while (p < P && earlier_slot(s_ids, p, e)) {
-      p += all;
-      e = p < P ? __builtin_amdgcn_readfirstlane(s_ids[p]) : 0;
+  if (M > 1) {
+    while (p < P && s_groups[p] < 1 << 16) p += all;
+    if (p < P) {
+      e = __builtin_amdgcn_readfirstlane(s_ids[p]);
+      KQ_LOAD(e, 0)
     }
-    if (p < P) KQ_LOAD(e, 0)
   }
   while (p < P) {
-    const int cnt = gather_slots(s_ids, P, e, list);
-    int pn = p + all, en = 0;
-    for (; pn < P; pn += all) {
-      en = __builtin_amdgcn_readfirstlane(s_ids[pn]);
-      if (!earlier_slot(s_ids, pn, en)) break;
-    }
-    for (int t0 = 0; t0 < cnt; t0 += SLOTS) {
+    int pn = p + all;
+    while (pn < P && s_groups[pn] < 1 << 16) pn += all;
+    const int en = pn < P ? __builtin_amdgcn_readfirstlane(s_ids[pn]) : 0;
+    {
       // column piece * n + m: that piece of h of slot m of this group
-      const int n = min(SLOTS, cnt - t0), piece = r / n, m = r - piece * n;
-      const uint32_t xoff = piece < 3 ? (uint32_t)(piece * P + list[t0 + m]) * hrow : 0u;
+      const int n = __builtin_amdgcn_readfirstlane(s_groups[p] >> 16), piece = r / n, m = r - piece * n;
+      int slots[SLOTS];
+      slots[0] = p;
+#pragma unroll
+      for (int k = 1; k < SLOTS; ++k) slots[k] = k < n ? __builtin_amdgcn_readfirstlane(s_groups[slots[k - 1]] & 0xffff) : p;
+      int mine = p;   // slot of this lane's column
+#pragma unroll
+      for (int k = 1; k < SLOTS; ++k) mine = m == k ? slots[k] : mine;
+      const uint32_t xoff = piece < 3 ? (uint32_t)(piece * P + mine) * hrow : 0u;
       const auto off = [=](int row) { return (uint32_t)__shfl((int)xoff, row, 64); };
       const int have = piece < 3 ? r : 0;
       const uint8_t* xr[1] = {xl + have * (PR * 16)};
@@ -429,8 +448,8 @@ __global__ __launch_bounds__(1024) void k_mx4_down(const uint8_t* __restrict__ d
         WChunk<1> w[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) w[u] = next[u];
-        const bool more = c + U < nchunk, again = t0 + SLOTS < cnt;
-        if (more || again || pn < P) KQ_LOAD(more || again ? e : en, more ? c + U : 0)
+        const bool more = c + U < nchunk;
+        if (more || pn < P) KQ_LOAD(more ? e : en, more ? c + U : 0)
 #pragma unroll
         for (int u = 0; u < U; ++u) chunk_products<T_BF16, 1, 1, U>(xr, have & 7, u, w[u], g, acc);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the region has been read
@@ -442,7 +461,9 @@ __global__ __launch_bounds__(1024) void k_mx4_down(const uint8_t* __restrict__ d
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
       for (int i = lane; i < n * 16; i += 64) {
-        const int slot = list[t0 + (i >> 4)];
+        int slot = p;
+#pragma unroll
+        for (int k = 1; k < SLOTS; ++k) slot = (i >> 4) == k ? slots[k] : slot;
         const float v = res[2 * n * 16 + i] + res[n * 16 + i] + res[i];
         float* o = ys + (slot / top_k) * 16 + (i & 15);
         *o = __builtin_fmaf(s_w[slot], v, *o);
@@ -540,7 +561,7 @@ bool chooses_itself(const Mx4MoeArgs& a) {
 }
 
 template <int XT, int TILES>
-int gate_up_cfg(const Mx4MoeArgs& a, uint16_t* h) {
+int gate_up_cfg(const Mx4MoeArgs& a, uint16_t* h, int32_t* groups) {
   typedef GateUp<XT, TILES> G;
   constexpr int U = GU_CHUNKS;
   const RouteArgs& r = a.route;
@@ -550,13 +571,15 @@ int gate_up_cfg(const Mx4MoeArgs& a, uint16_t* h) {
   const int splits = chooses_itself(a) ? route_splits(r.K) : 0;
   if (splits)   // a thread per expert, and the choice's scratch
     while (waves * 64 < r.E || waves * G::PER_WAVE < select_lds_bytes(waves, r.top_k)) ++waves;
-  const dim3 grid((unsigned)((a.inter / 16 + TILES - 1) / TILES), (unsigned)(P < r.E ? P : r.E));
+  // passes of twice an expert's mean number of slots (54 tokens, 15 experts, top 11: PASSES us)
+  const int mean2 = (2 * P + r.E - 1) / r.E, z = (mean2 + GuCols<XT>::v - 1) / GuCols<XT>::v;
+  const dim3 grid((unsigned)((a.inter / 16 + TILES - 1) / TILES), (unsigned)(P < r.E ? P : r.E), (unsigned)(z > 8 ? 8 : z));
   const size_t lds = (size_t)waves * G::PER_WAVE + (size_t)P * 4;
   dispatch_log("k_mx4_gate_up", -1, a.inter, r.K, r.M, grid.x, grid.y, (unsigned)(64 * waves), lds, "type=%d tiles=%d chooses=%d", XT, TILES, splits > 0);
   auto* k = r.K % 128 == 0 ? k_mx4_gate_up<XT, TILES, true> : k_mx4_gate_up<XT, TILES, false>;
   hipLaunchKernelGGL(k, grid, dim3((unsigned)(64 * waves)), lds, r.stream, a.codes[0], a.scales[0], a.codes[1],
                      a.scales[1], r.x, r.ids, h, (int)r.K, (int)a.inter, r.M, r.top_k, r.E, waves,
-                     static_cast<const double*>(r.ws), splits, r.renorm, r.weights);
+                     static_cast<const double*>(r.ws), splits, r.renorm, r.weights, groups);
   return (int)hipGetLastError();
 }
 
@@ -564,22 +587,29 @@ int gate_up_cfg(const Mx4MoeArgs& a, uint16_t* h) {
 // where the slots still fill the compute units (16 tokens, 128 experts of 768 x
 // 2048, top 8: 42.7 us against 48.2 with one and 50.5 with four).
 template <int XT>
-int gate_up_x(const Mx4MoeArgs& a, uint16_t* h) {
+int gate_up_x(const Mx4MoeArgs& a, uint16_t* h, int32_t* groups) {
   const int P = a.route.M * a.route.top_k;
-  return (a.inter / 32) * (P < a.route.E ? P : a.route.E) >= 512 ? gate_up_cfg<XT, 2>(a, h) : gate_up_cfg<XT, 1>(a, h);
+  return (a.inter / 32) * (P < a.route.E ? P : a.route.E) >= 512 ? gate_up_cfg<XT, 2>(a, h, groups) : gate_up_cfg<XT, 1>(a, h, groups);
 }
 
-// Workgroups that share the down projection's rows: with many slots one
-// workgroup per 16 rows leaves compute units idle and each reads all of h.
-constexpr int DOWN_PARTS = 4;
-int down_parts(int P) { return P >= 64 ? DOWN_PARTS : 1; }
+// Workgroups that share the down projection's rows: with many slots, or few
+// rows, one workgroup per 16 rows leaves compute units idle (and each reads all
+// of h). Two per compute unit, four slots and more each; the sum of the parts
+// costs a launch (16 tokens, top 8, 2048 rows: 37.1 us with one, 25.4 + 4.8 with
+// four; 4 tokens 13.3 against 11.8 + 4.8).
+int down_parts(int64_t hidden, int P) {
+  if (P < 64 && hidden > 1024) return 1;
+  const int64_t fill = 512 / (hidden / 16), most = P / 4;
+  const int64_t n = fill < most ? fill : most;
+  return n < 2 ? 1 : n > 16 ? 16 : (int)n;
+}
 
 template <int U, int SLOTS>
-int down_cfg(const Mx4MoeArgs& a, const uint16_t* h, float* parts, int count) {
+int down_cfg(const Mx4MoeArgs& a, const uint16_t* h, const int32_t* groups, float* parts, int count) {
   const RouteArgs& r = a.route;
   const int P = r.M * r.top_k;
   // a wave per slot up to what LDS holds; two workgroups to a compute unit where there are parts
-  const int shared = P * 6, per_wave = x_region_bytes<T_BF16, U>(3 * SLOTS) + r.M * 64 + P * 2;
+  const int shared = P * 10, per_wave = x_region_bytes<T_BF16, U>(3 * SLOTS) + r.M * 64;
   int waves = (MOE_LDS_BYTES / (count > 1 ? 2 : 1) - shared) / per_wave;
   const int most = count > 1 ? 8 : 16;
   waves = waves > most ? most : waves < 1 ? 1 : waves;
@@ -589,7 +619,7 @@ int down_cfg(const Mx4MoeArgs& a, const uint16_t* h, float* parts, int count) {
   dispatch_log("k_mx4_down", -1, r.K, a.inter, r.M, grid.x, grid.y, (unsigned)(64 * waves), lds, "u=%d slots=%d", U, SLOTS);
   auto* k = a.inter % 128 == 0 ? k_mx4_down<U, SLOTS, true> : k_mx4_down<U, SLOTS, false>;
   hipLaunchKernelGGL(k, grid, dim3((unsigned)(64 * waves)), lds, r.stream, a.codes[2], a.scales[2], h, r.ids,
-                     r.weights, count > 1 ? parts : a.y, (int)r.K, (int)a.inter, r.M, r.top_k, waves);
+                     r.weights, groups, count > 1 ? parts : a.y, (int)r.K, (int)a.inter, r.M, r.top_k, waves);
   int err = (int)hipGetLastError();
   if (err || count == 1) return err;
   const int n4 = (int)(r.M * r.K / 4);
@@ -601,23 +631,43 @@ int down_cfg(const Mx4MoeArgs& a, const uint16_t* h, float* parts, int count) {
 
 }  // namespace
 
-// The logits' parts, the three planes of h, the parts of y (where there are any).
+namespace {
+
+// Byte offsets in the workspace, after the logits' parts.
+struct MoeLayout {
+  int64_t h, groups, parts, total;
+};
+MoeLayout moe_layout(int64_t hidden, int64_t inter, int M, int top_k, int E) {
+  const int64_t P = (int64_t)M * top_k, n = down_parts(hidden, (int)P);
+  MoeLayout L;
+  L.h = up256(route_workspace_bytes(M, E));
+  L.groups = L.h + up256(3 * P * inter * 2);
+  L.parts = L.groups + up256(P * 4);
+  L.total = L.parts + (n > 1 ? n * M * hidden * 4 : 0);
+  return L;
+}
+
+}  // namespace
+
 int64_t mx4_moe_workspace_bytes(int64_t hidden, int64_t inter, int M, int top_k, int E) {
-  const int64_t P = (int64_t)M * top_k, parts = down_parts((int)P);
-  return up256(route_workspace_bytes(M, E)) + up256(3 * P * inter * 2) + (parts > 1 ? parts * M * hidden * 4 : 0);
+  return moe_layout(hidden, inter, M, top_k, E).total;
 }
 
 int launch_mx4_moe(const Mx4MoeArgs& a) {
   const RouteArgs& r = a.route;
-  const int P = r.M * r.top_k;
-  uint8_t* ws = static_cast<uint8_t*>(r.ws) + up256(route_workspace_bytes(r.M, r.E));
-  uint16_t* h = reinterpret_cast<uint16_t*>(ws);
-  float* parts = reinterpret_cast<float*>(ws + up256(3 * (int64_t)P * a.inter * 2));
+  const MoeLayout L = moe_layout(r.K, a.inter, r.M, r.top_k, r.E);
+  uint8_t* ws = static_cast<uint8_t*>(r.ws);
+  uint16_t* h = reinterpret_cast<uint16_t*>(ws + L.h);
+  int32_t* groups = reinterpret_cast<int32_t*>(ws + L.groups);
+  float* parts = reinterpret_cast<float*>(ws + L.parts);
   int err = chooses_itself(a) ? launch_logits(r) : launch_route(r);
   if (err) return err;
-  err = r.xtype == KQ_F32 ? gate_up_x<T_F32>(a, h) : r.xtype == KQ_F16 ? gate_up_x<T_F16>(a, h) : gate_up_x<T_BF16>(a, h);
+  err = r.xtype == KQ_F32   ? gate_up_x<T_F32>(a, h, groups)
+        : r.xtype == KQ_F16 ? gate_up_x<T_F16>(a, h, groups)
+                            : gate_up_x<T_BF16>(a, h, groups);
   if (err) return err;
-  return r.M == 1 ? down_cfg<6, 1>(a, h, parts, 1) : down_cfg<3, 3>(a, h, parts, down_parts(P));
+  return r.M == 1 ? down_cfg<6, 1>(a, h, groups, parts, 1)
+                  : down_cfg<3, DOWN_SLOTS>(a, h, groups, parts, down_parts(r.K, r.M * r.top_k));
 }
 
 }  // namespace kq
