@@ -274,6 +274,77 @@ __global__ __launch_bounds__(64 * WN * WM) void k_mx4_gemm(const uint8_t* __rest
   }
 }
 
+// The product for few tiles: a workgroup computes 32 x 32, its waves split K and
+// take their operands straight from memory. Such loads (a lane's 16 bytes of a
+// row of its own) run at a quarter of the rate of whole lines, but nothing waits
+// for anything else until the waves' sums meet in LDS, where they are added in
+// wave order. A lane (r, h) takes blocks 4 h .. 4 h + 3 of each 8 of its wave's,
+// so that their scales are one dword.
+constexpr int SMALL_WAVES = 16;
+
+template <bool AL>
+struct SmallOperand {
+  u32x4 codes[4];
+  uint32_t scales;
+  __device__ __forceinline__ void load(rsrc_t rc, rsrc_t rs, int c, int nblk, int r, int h) {
+    const int b = c * GEMM_KB + 4 * h;
+    const uint32_t o = (uint32_t)r * (uint32_t)nblk + (uint32_t)b;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) codes[s] = ld128(rc, b + s < nblk ? (o + s) * 16u : OOB);
+    if constexpr (AL) {
+      scales = ld32(rs, b < nblk ? o : OOB);
+    } else {
+      scales = 0;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) scales |= ld8(rs, b + s < nblk ? o + s : OOB) << (8 * s);
+    }
+  }
+};
+
+template <int T, bool AL>
+__global__ __launch_bounds__(64 * SMALL_WAVES) void k_mx4_gemm_small(const uint8_t* __restrict__ ac, const uint8_t* __restrict__ as,
+                                                                    const uint8_t* __restrict__ wc, const uint8_t* __restrict__ ws,
+                                                                    void* __restrict__ y, int64_t M, int64_t N, int nblk,
+                                                                    uint32_t tiles_m, int waves) {
+  __shared__ v16f red[SMALL_WAVES][64];
+  const int lane = threadIdx.x & 63, wave = wave_id(), r = lane & 31, h = lane >> 5;
+  const uint32_t tn = blockIdx.x / tiles_m, tm = blockIdx.x - tn * tiles_m;
+  const int64_t n0 = (int64_t)tn * 32, m0 = (int64_t)tm * 32;
+  const int rows_n = __builtin_amdgcn_readfirstlane((int)min<int64_t>(32, N - n0));
+  const int rows_m = __builtin_amdgcn_readfirstlane((int)min<int64_t>(32, M - m0));
+  rsrc_t rwc, rws, rac, ras;
+  mx4_rows(wc, ws, n0, rows_n, nblk, rwc, rws);
+  mx4_rows(ac, as, m0, rows_m, nblk, rac, ras);
+  const int nc = (nblk + GEMM_KB - 1) / GEMM_KB, c0 = nc * wave / waves, c1 = nc * (wave + 1) / waves;
+  v16f acc = {};
+  SmallOperand<AL> w, a, wn, an;
+  wn.load(rwc, rws, c0 < c1 ? c0 : nc, nblk, r, h);
+  an.load(rac, ras, c0 < c1 ? c0 : nc, nblk, r, h);
+  for (int c = c0; c < c1; ++c) {
+    w = wn;
+    a = an;
+    wn.load(rwc, rws, c + 1 < c1 ? c + 1 : nc, nblk, r, h);
+    an.load(rac, ras, c + 1 < c1 ? c + 1 : nc, nblk, r, h);
+    acc = mfma_fp4<0>(w.codes[0], a.codes[0], acc, w.scales, a.scales);
+    acc = mfma_fp4<1>(w.codes[1], a.codes[1], acc, w.scales, a.scales);
+    acc = mfma_fp4<2>(w.codes[2], a.codes[2], acc, w.scales, a.scales);
+    acc = mfma_fp4<3>(w.codes[3], a.codes[3], acc, w.scales, a.scales);
+  }
+  red[wave][lane] = acc;
+  __syncthreads();
+  typedef typename OutT<T>::t out_t;
+  for (int t = threadIdx.x; t < 1024; t += 64 * waves) {
+    // weight row n is element 4 (n >> 3) + (n & 3) of lane m + 32 (n >> 2 & 1)
+    const int n = t & 31, m = t >> 5, i = 4 * (n >> 3) + (n & 3), l = m + 32 * (n >> 2 & 1);
+    if (n < rows_n && m < rows_m) {
+      const float* p = reinterpret_cast<const float*>(&red[0][l]) + i;
+      float v = p[0];
+      for (int k = 1; k < waves; ++k) v += p[k * 1024];
+      static_cast<out_t*>(y)[(m0 + m) * N + n0 + n] = (out_t)v;
+    }
+  }
+}
+
 }  // namespace kqd
 
 namespace kq {
@@ -302,9 +373,13 @@ int gemm_cfg(const Mx4GemmArgs& a) {
 //   4096 x 19456 x 2560: 256 x 256 157 us, 160 x 256 193
 //   2048 x 2560 x 9728: 192 x 128 (224 tiles) 40.9 us, 160 x 256 55.6
 //   300 x 6144 x 2560: 64 x 64 11.0 us, 192 x 128 14.5
-enum GemmShape { G256X256, G160X256, G192X128, G64X64 };
-GemmShape gemm_shape(int64_t M, int64_t N) {
+// Where 32 x 32 tiles do not outnumber the compute units and K is not short,
+// the direct kernel: 64 x 2560 x 9728 14.9 us (64 x 64: 20.2), 17 x 1570 x 5856
+// 8.8 (17.1), 3 x 520 x 14272 14.9 (33.8); with more, 128 x 2560 x 2560 9.5 (7.2).
+enum GemmShape { G256X256, G160X256, G192X128, G64X64, G32X32 };
+GemmShape gemm_shape(int64_t M, int64_t N, int64_t K) {
   const int64_t cus = device_cus();
+  if (K > 3 * 32 * GEMM_KB && ((M + 31) / 32) * ((N + 31) / 32) <= cus) return G32X32;
   const auto rounds = [&](int bn, int bm) {
     return (double)((((M + bm - 1) / bm) * ((N + bn - 1) / bn) + cus - 1) / cus);
   };
@@ -317,11 +392,24 @@ GemmShape gemm_shape(int64_t M, int64_t N) {
 }
 
 template <int T>
+int gemm_small(const Mx4GemmArgs& a) {
+  const int64_t tiles_m = (a.M + 31) / 32;
+  const unsigned grid = (unsigned)(tiles_m * ((a.N + 31) / 32));
+  const int nc = (int)((a.K / 32 + GEMM_KB - 1) / GEMM_KB), waves = nc < SMALL_WAVES ? nc : SMALL_WAVES;
+  dispatch_log("k_mx4_gemm_small", -1, a.N, a.K, (int)a.M, grid, 1, (unsigned)(64 * waves), SMALL_WAVES * 4096, "type=%d", T);
+  auto* k = a.K % 128 == 0 ? k_mx4_gemm_small<T, true> : k_mx4_gemm_small<T, false>;
+  hipLaunchKernelGGL(k, dim3(grid), dim3((unsigned)(64 * waves)), 0, a.stream, a.a_codes, a.a_scales, a.w_codes,
+                     a.w_scales, a.y, a.M, a.N, (int)(a.K / 32), (uint32_t)tiles_m, waves);
+  return (int)hipGetLastError();
+}
+
+template <int T>
 int gemm_type(const Mx4GemmArgs& a) {
-  switch (gemm_shape(a.M, a.N)) {
+  switch (gemm_shape(a.M, a.N, a.K)) {
     case G256X256: return gemm_cfg<T, 4, 2, 2, 4>(a);
     case G160X256: return gemm_cfg<T, 1, 4, 5, 2>(a);
     case G192X128: return gemm_cfg<T, 2, 2, 3, 2>(a);
+    case G32X32: return gemm_small<T>(a);
     default: return gemm_cfg<T, 2, 2, 1, 1>(a);
   }
 }

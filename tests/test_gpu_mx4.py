@@ -281,21 +281,24 @@ def test_gemm(kind, M, N, K):
     check(got.reshape(M, N), ref, mags, K, kind, f"{kind} {M}x{N}x{K}")
 
 
+@pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("M,N,K", [(4096, 2048, 96), (2049, 4000, 544), (300, 20001, 256), (20001, 300, 1280),   # 160 x 256 tiles
                                    (2048, 2560, 160), (1900, 2561, 2592), (2000, 2500, 384),                  # 192 x 128
                                    (4100, 12000, 96), (4099, 12001, 1184), (4096, 12032, 1280),               # 256 x 256
-                                   (300, 6143, 2592)])                                                        # 64 x 64
-def test_gemm_large(M, N, K):
-    """Grids of the large tiles; every result bit for bit where the sums are exact in fp32."""
+                                   (300, 6143, 2592), (300, 6144, 2560), (40, 300, 256), (513, 999, 96),      # 64 x 64
+                                   (64, 2560, 9728), (33, 1570, 5856), (512, 512, 3200)])                     # 32 x 32
+def test_gemm_tiles(kind, M, N, K):
+    """Every tile shape; every result bit for bit, as the sums are exact in fp32."""
     t = U.torch_cuda()
+    dtype = {"f32": t.float32, "f16": t.float16, "bf16": t.bfloat16}[kind]
     rng = np.random.default_rng((M, N))
     # magnitudes up to 6 and scales of 1: multiples of 1/4 up to 36 K < 2^24 / 4 are exact in any order
     a, w = random_planes(rng, M, K, 127, 128), random_planes(rng, N, K, 127, 128)
     pa, pw = upload(*a), upload(*w)
-    y = t.full((M, N), float("nan"), dtype=t.float32, device="cuda")
-    kq.kq_mx4_gemm(pa[0].ptr, pa[1].ptr, pw[0].ptr, pw[1].ptr, "f32", y, M, N, K)
-    av, wv = (t.from_numpy(X.dequantize(*p)).to("cuda") for p in (a, w))
-    assert t.equal(y.double(), av @ wv.T.contiguous())
+    y = t.full((M, N), float("nan"), dtype=dtype, device="cuda")
+    kq.kq_mx4_gemm(pa[0].ptr, pa[1].ptr, pw[0].ptr, pw[1].ptr, kind, y, M, N, K)
+    av, wv = (t.from_numpy(X.dequantize(*p).astype(np.float32)).to("cuda").double() for p in (a, w))
+    assert t.equal(y, (av @ wv.T.contiguous()).to(dtype))
 
 
 def test_gemm_nan_scales_stay_in_their_rows():
