@@ -162,8 +162,12 @@ __device__ __forceinline__ void store_sums(const v4f (&acc)[RT][CT], v4f* red, i
 
 // y[m][n] for RT tiles of 16 weight rows and up to 16 CT columns. The waves of
 // a workgroup share the rows and split K; their partial sums meet in LDS and
-// are added in wave order. Dynamic LDS: waves * region bytes, then (CT 1)
-// or in their place (CT > 1) waves * RT * CT KiB of partial sums.
+// are added in wave order. Grid y: groups of 16 CT columns. Dynamic LDS: waves *
+// (the columns' and the weights' regions), then (CT 1) or in their place (CT >
+// 1) waves * RT * CT KiB of partial sums. One column is bound by memory and the
+// launch (19456 x 2560, bf16: 26.5 MB in 6.8 us, 3.9 TB/s); many columns by what
+// each workgroup brings through LDS, a byte of it written and read once at 64
+// bytes a clock (2560 x 9728 at 48: 15 us).
 template <int XT, int CT, int RT, int U, bool AL>
 __global__ __launch_bounds__(1024) void k_mx4_gemv(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                                                    const void* __restrict__ x, float* __restrict__ y, int N, int K,
@@ -179,11 +183,13 @@ __global__ __launch_bounds__(1024) void k_mx4_gemv(const uint8_t* __restrict__ c
   const rsrc_t rx = make_rsrc(x, (uint32_t)M * xrow);
   v4f acc[RT][CT] = {};
   const int c0 = nchunk * wave / waves, c1 = nchunk * (wave + 1) / waves;
-  const int region = x_region_bytes<XT, U>(M);
-  mx4_tile<XT, CT, RT, U, AL>(rc, rs, rx, lds + wave * region, M, [=](int row) { return (uint32_t)row * xrow; }, nblk,
-                              c0, c1, acc);
+  const int m0 = (int)blockIdx.y * (16 * CT);
+  const int cols = min(M - m0, 16 * CT), xbytes = x_region_bytes<XT, U>(min(M, 16 * CT)), region = xbytes + w_region_bytes<RT, U>();
+  uint8_t* xl = lds + wave * region;
+  mx4_tile<XT, CT, RT, U, AL>(rc, rs, rx, xl, xl + xbytes, cols,
+                              [=](int row) { return (uint32_t)(m0 + row) * xrow; }, nblk, c0, c1, acc);
   if constexpr (CT > 1) __syncthreads();   // every wave has read its region
-  store_sums<RT, CT>(acc, reinterpret_cast<v4f*>(lds + (CT == 1 ? waves * region : 0)), wave, waves, y, row0, N, M);
+  store_sums<RT, CT>(acc, reinterpret_cast<v4f*>(lds + (CT == 1 ? waves * region : 0)), wave, waves, y + (int64_t)m0 * N, row0, N, cols);
 }
 
 }  // namespace kqd
@@ -257,43 +263,59 @@ constexpr int LDS_BYTES = 160 * 1024;   // of a compute unit
 template <int XT, int CT, int RT, int U>
 int gemv_cfg(const Mx4GemvArgs& a) {
   const int nchunk = (int)((a.K / 32 + 3) / 4);
-  const int region = x_region_bytes<XT, U>(a.M), sums = RT * CT * 1024;
+  const int region = x_region_bytes<XT, U>(a.M < 16 * CT ? a.M : 16 * CT) + w_region_bytes<RT, U>(), sums = RT * CT * 1024;
   const int per_wave = CT == 1 ? region + sums : region > sums ? region : sums;
   int waves = (nchunk + U - 1) / U;   // one batch of loads per wave
   const int most = LDS_BYTES / per_wave < 16 ? LDS_BYTES / per_wave : 16;
   waves = waves > most ? most : waves;
   const unsigned grid = (unsigned)((a.N + 16 * RT - 1) / (16 * RT));
+  const unsigned parts = (unsigned)((a.M + 16 * CT - 1) / (16 * CT));
   const size_t lds = (size_t)waves * per_wave;
-  dispatch_log("k_mx4_gemv", -1, a.N, a.K, a.M, grid, 1, (unsigned)(64 * waves), lds, "type=%d ct=%d rt=%d u=%d", XT, CT, RT, U);
+  dispatch_log("k_mx4_gemv", -1, a.N, a.K, a.M, grid, parts, (unsigned)(64 * waves), lds, "type=%d ct=%d rt=%d u=%d", XT, CT, RT, U);
   auto* k = a.K % 128 == 0 ? k_mx4_gemv<XT, CT, RT, U, true> : k_mx4_gemv<XT, CT, RT, U, false>;
-  hipLaunchKernelGGL(k, dim3(grid), dim3(64 * waves), lds, a.stream, a.codes, a.scales, a.x, a.y, (int)a.N, (int)a.K,
+  hipLaunchKernelGGL(k, dim3(grid, parts), dim3(64 * waves), lds, a.stream, a.codes, a.scales, a.x, a.y, (int)a.N, (int)a.K,
                      a.M, waves);
   return (int)hipGetLastError();
 }
 
-// More than 16 columns: the columns are most of what a workgroup reads, so two
-// row tiles share them where that leaves two workgroups per compute unit (19456
-// x 2560 at 48 columns: 24.6 us against 28.0 with one tile; 2560 x 9728, whose
-// grid it would halve below the compute units: 23.9 against 18.7).
+// bf16 and fp16 columns. More than 16 are most of what a workgroup reads, so a
+// workgroup takes them all, and two row tiles where that leaves a workgroup per
+// compute unit (19456 x 2560 at 48 bf16 columns: 21.6 us against 27.2 with one
+// tile and 41 with 16 columns each; 8192 x 4096 at 32: 9.8 against 12.9; 2560 x
+// 9728 at 48: 17.8 against 14.9). Where the row tiles are few, groups of columns
+// go to workgroups of their own as far as the compute units take them at once
+// (1000 x 14080 at 64 fp16 columns: 13.4 us against 31.5).
 template <int XT, int CT>
 int gemv_wide(const Mx4GemvArgs& a) {
-  if (a.N >= 32 * 2 * 256) return gemv_cfg<XT, CT, 2, 1>(a);
+  if (a.N >= 32 * 256) return gemv_cfg<XT, CT, 2, 1>(a);
   return gemv_cfg<XT, CT, 1, 1>(a);
 }
 
 template <int XT>
-int gemv_type(const Mx4GemvArgs& a) {
-  if (a.M <= 8) return gemv_cfg<XT, 1, 1, XT == T_F32 ? 2 : 4>(a);
-  if (a.M <= 16) return gemv_cfg<XT, 1, 1, XT == T_F32 ? 1 : 2>(a);
-  if (a.M <= 32) return gemv_wide<XT, 2>(a);
-  if (a.M <= 48) return gemv_wide<XT, 3>(a);
-  return gemv_wide<XT, 4>(a);
+int gemv_half(const Mx4GemvArgs& a) {
+  const int64_t tiles = (a.N + 15) / 16, parts = (a.M + 15) / 16;
+  if (a.M <= 8) return gemv_cfg<XT, 1, 1, 4>(a);
+  if (a.M <= 16 || tiles * parts <= 256) return gemv_cfg<XT, 1, 1, 2>(a);
+  if (a.M <= 32 || tiles * ((parts + 1) / 2) <= 256) return gemv_wide<XT, 2>(a);
+  return a.M <= 48 ? gemv_wide<XT, 3>(a) : gemv_wide<XT, 4>(a);
+}
+
+// fp32 columns. Splitting them into pieces is the work: row tiles share it, as
+// many as leave the compute units about one workgroup each, and columns past 16
+// go to other workgroups (11000 x 4096 at 64 columns: 45 us with four tiles, 91
+// with one, 122 with one of all columns; 2551 x 12000 at 36: 30 with two, 40, 43
+// and 55).
+int gemv_f32(const Mx4GemvArgs& a) {
+  const int64_t groups = (a.N + 15) / 16 * ((a.M + 15) / 16);
+  if (groups >= 4 * 192) return gemv_cfg<T_F32, 1, 4, 1>(a);
+  if (groups >= 2 * 192) return gemv_cfg<T_F32, 1, 2, 1>(a);
+  return gemv_cfg<T_F32, 1, 1, 1>(a);
 }
 
 }  // namespace
 
 int launch_mx4_gemv(const Mx4GemvArgs& a) {
-  return a.type == KQ_F32 ? gemv_type<T_F32>(a) : a.type == KQ_F16 ? gemv_type<T_F16>(a) : gemv_type<T_BF16>(a);
+  return a.type == KQ_F32 ? gemv_f32(a) : a.type == KQ_F16 ? gemv_half<T_F16>(a) : gemv_half<T_BF16>(a);
 }
 
 }  // namespace kq

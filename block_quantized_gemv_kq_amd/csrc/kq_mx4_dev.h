@@ -128,36 +128,38 @@ __device__ __forceinline__ void stage_x(rsrc_t rx, uint8_t* xl, int rows, Off of
   }
 }
 
-template <int RT>
-struct WChunk {
-  u32x4 codes[RT];
-  uint32_t scale[RT];   // fp16 columns: the four bytes of the chunk; others: the byte of the lane's block
-};
+// The weights come through LDS too, in the wave's region: a wave's lanes in
+// operand order are 16 rows, and loads of 16 bytes each by lanes of different
+// rows run at a quarter of the rate of loads whose neighbouring lanes take the
+// pieces of one row (19456 x 2560 at one bf16 column: 7.8 us against 6.8; gate and
+// up of 16 tokens of 128 experts: 40 against 31). Row
+// r of tile t holds U chunks, its piece p at p ^ r (its low bits for U < 4);
+// behind the codes, a dword of four scale bytes per row and chunk.
+template <int RT, int U>
+__host__ __device__ constexpr int w_region_bytes() { return RT * (U * 1024 + U * 64); }
 
-// AL: rows hold whole chunks (K a multiple of 128), so a chunk's four scale
-// bytes are one aligned dword; otherwise they are loaded one by one, blocks
-// past the row's end reading zero.
-template <int XT, int RT, bool AL>
-__device__ __forceinline__ void load_w_chunk(const rsrc_t (&rc)[RT], const rsrc_t (&rs)[RT], int c, int nblk, int r,
-                                             int g, WChunk<RT>& w) {
-  const int b = 4 * c + g;
-  const uint32_t co = b < nblk ? ((uint32_t)r * (uint32_t)nblk + (uint32_t)b) * 16u : OOB;
+// Chunks c .. c + U - 1 of a tile: codes to cl, scale bytes to sl. AL: rows hold
+// whole chunks (K a multiple of 128), so a chunk's scale bytes are one aligned
+// dword; otherwise it is put together from bytes. Blocks from `end` on read zero.
+template <int U, bool AL>
+__device__ __forceinline__ void stage_w(rsrc_t rc, rsrc_t rs, uint8_t* cl, uint8_t* sl, int c, int end, int nblk) {
+  const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int t = 0; t < RT; ++t) w.codes[t] = ld128(rc[t], co);
-  const uint32_t so = (uint32_t)r * (uint32_t)nblk + 4u * (uint32_t)c;
+  for (int i = 0; i < U; ++i) {
+    const int slot = i * 64 + lane, row = slot / (4 * U), b = 4 * c + ((slot % (4 * U)) ^ (row & (4 * U - 1)));
+    const uint32_t o = ((uint32_t)row * (uint32_t)nblk + (uint32_t)b) * 16u;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rc, (lds_void_t*)(cl + i * 1024), 16, b < end ? o : +OOB, 0, 0, 0);
+  }
+  const int row = lane / U, b = 4 * (c + lane % U);   // lanes past 16 U: rows past the tile
+  const uint32_t o = (uint32_t)row * (uint32_t)nblk + (uint32_t)b;
+  if constexpr (AL) {
+    if (lane < 16 * U)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)sl, 4, b < end ? o : +OOB, 0, 0, 0);
+  } else {
+    uint32_t d = 0;
 #pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    if constexpr (AL) {
-      const uint32_t d = ld32(rs[t], 4 * c < nblk ? so : OOB);
-      w.scale[t] = d;
-    } else if constexpr (XT == T_F16) {
-      uint32_t d = 0;
-#pragma unroll
-      for (int s = 0; s < 4; ++s) d |= ld8(rs[t], 4 * c + s < nblk ? so + s : OOB) << (8 * s);
-      w.scale[t] = d;
-    } else {
-      w.scale[t] = ld8(rs[t], b < nblk ? so + g : OOB) << (8 * g);
-    }
+    for (int k = 0; k < 4; ++k) d |= ld8(rs, lane < 16 * U && b + k < end ? o + k : +OOB) << (8 * k);
+    if (lane < 16 * U) reinterpret_cast<uint32_t*>(sl)[lane] = d;
   }
 }
 
@@ -187,12 +189,19 @@ __device__ __forceinline__ void split3(const float (&x)[8], v8b& hi, v8b& mid, v
   lo = __builtin_bit_cast(v8b, l);
 }
 
-// acc += the products of chunk u of the region. xrow[t]: the region row of the
+// acc += the products of chunk u of the regions. xrow[t]: the region row of the
 // lane's column in column tile t; swz: its row & 7, the same for every t.
 template <int XT, int CT, int RT, int U>
-__device__ __forceinline__ void chunk_products(const uint8_t* (&xrow)[CT], int swz, int u, const WChunk<RT>& w, int g,
+__device__ __forceinline__ void chunk_products(const uint8_t* (&xrow)[CT], int swz, int u, const uint8_t* wl, int r, int g,
                                                v4f (&acc)[RT][CT]) {
   const int base = u * Pieces<XT>::v;
+  u32x4 codes[RT];
+  uint32_t scale[RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    codes[t] = *reinterpret_cast<const u32x4*>(wl + t * U * 1024 + (r * (4 * U) + ((4 * u + g) ^ (r & (4 * U - 1)))) * 16);
+    scale[t] = *reinterpret_cast<const uint32_t*>(wl + RT * U * 1024 + t * U * 64 + (r * U + u) * 4);
+  }
   if constexpr (XT == T_F16) {
     v8h x[4][CT];
 #pragma unroll
@@ -201,12 +210,12 @@ __device__ __forceinline__ void chunk_products(const uint8_t* (&xrow)[CT], int s
       for (int c = 0; c < CT; ++c) x[s][c] = *reinterpret_cast<const v8h*>(xrow[c] + (base + ((4 * s + g) ^ swz)) * 16);
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      uint32_t e[4] = {w.codes[t].x, w.codes[t].y, w.codes[t].z, w.codes[t].w};
+      uint32_t e[4] = {codes[t].x, codes[t].y, codes[t].z, codes[t].w};
       transpose_groups(e[0], e[1], e[2], e[3]);
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         const v8h wb = codes_f16(e[s]);
-        const float sc = scale_value((w.scale[t] >> (8 * s)) & 255u);
+        const float sc = scale_value((scale[t] >> (8 * s)) & 255u);
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
           const v4f p = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[s][c], wb, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
@@ -218,12 +227,12 @@ __device__ __forceinline__ void chunk_products(const uint8_t* (&xrow)[CT], int s
   } else {
     float sc[RT];
 #pragma unroll
-    for (int t = 0; t < RT; ++t) sc[t] = scale_of((w.scale[t] >> (8 * g)) & 255u);
+    for (int t = 0; t < RT; ++t) sc[t] = scale_of((scale[t] >> (8 * g)) & 255u);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       v8b wb[RT];
 #pragma unroll
-      for (int t = 0; t < RT; ++t) wb[t] = codes_bf16(w.codes[t][s], sc[t]);
+      for (int t = 0; t < RT; ++t) wb[t] = codes_bf16(codes[t][s], sc[t]);
 #pragma unroll
       for (int c = 0; c < CT; ++c) {
         if constexpr (XT == T_BF16) {
@@ -248,13 +257,18 @@ __device__ __forceinline__ void chunk_products(const uint8_t* (&xrow)[CT], int s
   }
 }
 
+// Regions filled: this wave's copies have landed, and its LDS stores are done.
+__device__ __forceinline__ void regions_filled() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
+// Regions read: the next copies may take their place.
+__device__ __forceinline__ void regions_read() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
 // acc += the products of chunks [c0, c1) (wave-uniform) with `rows` columns
 // (1 to 16 CT). rc[t], rs[t]: the code and scale rows of tile t (rows past the
-// matrix read zero); xl: the wave's region; off: see stage_x. The weights of
-// the next U chunks are loaded before these are multiplied.
+// matrix read zero); xl, wl: the wave's regions; off: see stage_x.
 template <int XT, int CT, int RT, int U, bool AL, class Off>
 __device__ __forceinline__ void mx4_tile(const rsrc_t (&rc)[RT], const rsrc_t (&rs)[RT], rsrc_t rx, uint8_t* xl,
-                                         int rows, Off off, int nblk, int c0, int c1, v4f (&acc)[RT][CT]) {
+                                         uint8_t* wl, int rows, Off off, int nblk, int c0, int c1,
+                                         v4f (&acc)[RT][CT]) {
   constexpr int PR = Pieces<XT>::v * U;
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const uint8_t* xrow[CT];
@@ -266,22 +280,16 @@ __device__ __forceinline__ void mx4_tile(const rsrc_t (&rc)[RT], const rsrc_t (&
     if (c == 0) swz = have & 7;
   }
   const int end = min(c1 * Pieces<XT>::v, nblk * (Pieces<XT>::v / 4));
-  WChunk<RT> next[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) load_w_chunk<XT, RT, AL>(rc, rs, c0 + u < c1 ? c0 + u : nblk, nblk, r, g, next[u]);
   for (int c = c0; c < c1; c += U) {
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+      stage_w<U, AL>(rc[t], rs[t], wl + t * U * 1024, wl + RT * U * 1024 + t * U * 64, c, min(4 * c1, nblk), nblk);
     stage_x<XT, U>(rx, xl, rows, off, c, end);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the region is filled (and these weights are here)
-    WChunk<RT> w[U];
+    regions_filled();
 #pragma unroll
-    for (int u = 0; u < U; ++u) w[u] = next[u];
-    if (c + U < c1) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) load_w_chunk<XT, RT, AL>(rc, rs, c + U + u < c1 ? c + U + u : nblk, nblk, r, g, next[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) chunk_products<XT, CT, RT, U>(xrow, swz, u, w[u], g, acc);
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the region has been read
+    for (int u = 0; u < U; ++u)
+      if (c + u < c1) chunk_products<XT, CT, RT, U>(xrow, swz, u, wl, r, g, acc);
+    regions_read();
   }
 }
 

@@ -249,32 +249,33 @@ __device__ __forceinline__ void split3_one(float v, uint16_t& hi, uint16_t& mid,
 // h[slot][n] = silu(gate_n . x) * (up_n . x), silu(z) = z / (1 + e^-z), kept
 // as three bf16 planes whose sum is the fp32 value (no rounding of h), ready
 // as operands of the down projection. Grid (inter / 16 TILES, min(E, P), Z):
-// workgroup z takes the expert's passes of columns z, z + Z, ...; row y is expert y, or, with fewer slots than experts, the expert of slot y unless
-// an earlier slot has it. One token: its experts differ, and where a workgroup
+// workgroup z takes the expert's passes of columns z, z + Z, ...; row y is
+// expert y, or, with fewer slots than experts, the expert of slot y unless an
+// earlier slot has it. One token: its experts differ, and where a workgroup
 // has a thread per expert (splits > 0) each makes the choice itself, the first
 // one writing ids and weights, which saves a launch between two others.
 // The waves split K; each stages its part of the tokens once and walks TILES
-// tiles of 16 gate and 16 up rows, the next tile's weights in flight. The
-// partial sums meet in LDS in wave order, where the regions were.
+// tiles of 16 gate and 16 up rows. The partial sums meet in LDS in wave order,
+// where the regions were. Bound by memory: 16 tokens of 128 experts of 768 x
+// 2048, top 8, read 137 MB of weights of some 82 experts in 31 us, 4.4 TB/s; one
+// token 13.4 MB in 8.7 us, most of it the latency of the choice, the copies and
+// the launch.
 // Dynamic LDS: waves * PER_WAVE, then ids and list (P uint16 each).
-template <int XT> struct GuCols { static constexpr int v = XT == T_F32 ? 4 : 8; };   // columns in a pass
-constexpr int GU_CHUNKS = 4;   // of K in a wave's region
-template <int XT, int TILES>
+template <int XT, int TILES, int COLS>   // COLS: columns in a pass
 struct GateUp {
-  static constexpr int REGION = x_region_bytes<XT, GU_CHUNKS>(GuCols<XT>::v);
+  static constexpr int CHUNKS = XT == T_F32 ? 2 : 4;   // of K in a wave's region
+  static constexpr int X = x_region_bytes<XT, CHUNKS>(COLS), REGION = X + w_region_bytes<2, CHUNKS>();
   static constexpr int PER_WAVE = TILES * 2048 > REGION ? TILES * 2048 : REGION;
   static constexpr int MAX_WAVES = 8;
 };
 
-template <int XT, int TILES, bool AL>
-__global__ __launch_bounds__((GateUp<XT, TILES>::MAX_WAVES * 64)) void k_mx4_gate_up(const uint8_t* __restrict__ gc, const uint8_t* __restrict__ gs,
-                                                     const uint8_t* __restrict__ uc, const uint8_t* __restrict__ us,
-                                                     const void* __restrict__ x, int32_t* __restrict__ ids,
-                                                     uint16_t* __restrict__ h, int hidden, int inter, int M, int top_k,
-                                                     int E, int waves, const double* __restrict__ part, int splits,
-                                                     int renorm, float* __restrict__ weights,
-                                                     int32_t* __restrict__ groups) {
-  constexpr int COLS = GuCols<XT>::v, U = GU_CHUNKS, PER_WAVE = GateUp<XT, TILES>::PER_WAVE;
+template <int XT, int TILES, int COLS, bool AL>
+__global__ __launch_bounds__((GateUp<XT, TILES, COLS>::MAX_WAVES * 64)) void k_mx4_gate_up(
+    const uint8_t* __restrict__ gc, const uint8_t* __restrict__ gs, const uint8_t* __restrict__ uc,
+    const uint8_t* __restrict__ us, const void* __restrict__ x, int32_t* __restrict__ ids, uint16_t* __restrict__ h,
+    int hidden, int inter, int M, int top_k, int E, int waves, const double* __restrict__ part, int splits, int renorm,
+    float* __restrict__ weights, int32_t* __restrict__ groups) {
+  constexpr int U = GateUp<XT, TILES, COLS>::CHUNKS, PER_WAVE = GateUp<XT, TILES, COLS>::PER_WAVE;
   extern __shared__ u32x4 lds4[];
   uint8_t* lds = reinterpret_cast<uint8_t*>(lds4);
   uint16_t* s_ids = reinterpret_cast<uint16_t*>(lds + waves * PER_WAVE);
@@ -308,6 +309,7 @@ __global__ __launch_bounds__((GateUp<XT, TILES>::MAX_WAVES * 64)) void k_mx4_gat
   const int c0 = nchunk * wave / waves, c1 = nchunk * (wave + 1) / waves;
   const int64_t plane = (int64_t)P * inter;
   uint8_t* xl = lds + wave * PER_WAVE;
+  uint8_t* wl = xl + GateUp<XT, TILES, COLS>::X;
   for (int t0 = COLS * (int)blockIdx.z; t0 < cnt; t0 += COLS * (int)gridDim.z) {
     if (t0 >= COLS * (int)gridDim.z) __syncthreads();   // the previous pass has read the sums
     const int cols = min(COLS, cnt - t0);
@@ -317,31 +319,23 @@ __global__ __launch_bounds__((GateUp<XT, TILES>::MAX_WAVES * 64)) void k_mx4_gat
     const uint8_t* xr[1] = {xl + have * (Pieces<XT>::v * U * 16)};
     v4f acc[TILES][2][1] = {};
     for (int c = c0; c < c1; c += U) {   // once, unless K is longer than the waves' regions
-      rsrc_t rc[2], rs[2];
-      WChunk<2> next[U];
-#define KQ_LOAD_TILE(T)                                                                             \
-  {                                                                                                 \
-    const int rows = 16 * (tile0 + (T)) < inter ? 16 : 0;                                           \
-    const int64_t row = (int64_t)e * inter + (rows ? 16 * (tile0 + (T)) : 0);                       \
-    mx4_rows(gc, gs, row, rows, nblk, rc[0], rs[0]);                                                \
-    mx4_rows(uc, us, row, rows, nblk, rc[1], rs[1]);                                                \
-    _Pragma("unroll") for (int u = 0; u < U; ++u)                                                   \
-      load_w_chunk<XT, 2, AL>(rc, rs, c + u < c1 ? c + u : nblk, nblk, r, g, next[u]);              \
-  }
-      KQ_LOAD_TILE(0)
       stage_x<XT, U>(rx, xl, cols, off, c, min(c1 * Pieces<XT>::v, nblk * (Pieces<XT>::v / 4)));
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the region is filled
 #pragma unroll
       for (int t = 0; t < TILES; ++t) {
-        WChunk<2> w[U];
+        rsrc_t rc[2], rs[2];
+        const int rows = 16 * (tile0 + t) < inter ? 16 : 0;
+        const int64_t row = (int64_t)e * inter + (rows ? 16 * (tile0 + t) : 0);
+        mx4_rows(gc, gs, row, rows, nblk, rc[0], rs[0]);
+        mx4_rows(uc, us, row, rows, nblk, rc[1], rs[1]);
 #pragma unroll
-        for (int u = 0; u < U; ++u) w[u] = next[u];
-        if (t + 1 < TILES) KQ_LOAD_TILE(t + 1)
+        for (int i = 0; i < 2; ++i)
+          stage_w<U, AL>(rc[i], rs[i], wl + i * U * 1024, wl + 2 * U * 1024 + i * U * 64, c, min(4 * c1, nblk), nblk);
+        regions_filled();
 #pragma unroll
-        for (int u = 0; u < U; ++u) chunk_products<XT, 1, 2, U>(xr, have & 7, u, w[u], g, acc[t]);
+        for (int u = 0; u < U; ++u)
+          if (c + u < c1) chunk_products<XT, 1, 2, U>(xr, have & 7, u, wl, r, g, acc[t]);
+        regions_read();
       }
-#undef KQ_LOAD_TILE
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the region has been read
     }
     __syncthreads();   // the sums take the regions' place
     v4f* red = reinterpret_cast<v4f*>(lds);   // [wave][tile][gate, up][64]
@@ -375,8 +369,7 @@ __global__ __launch_bounds__((GateUp<XT, TILES>::MAX_WAVES * 64)) void k_mx4_gat
 // of its own in LDS, and the waves' sums are added in wave order, so the result
 // does not depend on timing. With more than one workgroup for the rows, out is
 // theirs in turn and k_mx4_down_sum adds them. The operand columns are the
-// three pieces of h of a group's slots. The weights of the next U chunks, or of
-// the wave's next group, are in flight while these are multiplied.
+// three pieces of h of a group's slots.
 // Dynamic LDS: per wave a region, then per wave M x 16 sums, then the route
 // weights (P fp32), groups (P int32) and ids (P uint16).
 template <int U, int SLOTS, bool AL>
@@ -385,11 +378,12 @@ __global__ __launch_bounds__(1024) void k_mx4_down(const uint8_t* __restrict__ d
                                                   const float* __restrict__ weights,
                                                   const int32_t* __restrict__ groups, float* __restrict__ out,
                                                   int hidden, int inter, int M, int top_k, int waves) {
-  constexpr int REGION = x_region_bytes<T_BF16, U>(3 * SLOTS), PR = Pieces<T_BF16>::v * U;
-  static_assert(REGION >= 1024, "the region serves the results too");
+  constexpr int X = x_region_bytes<T_BF16, U>(3 * SLOTS), REGION = X + w_region_bytes<1, U>(), PR = Pieces<T_BF16>::v * U;
+  static_assert(X >= 1024, "the region serves the results too");
   extern __shared__ u32x4 lds4[];
   const int lane = threadIdx.x & 63, wave = wave_id(), P = M * top_k, r = lane & 15, g = lane >> 4;
   uint8_t* xl = reinterpret_cast<uint8_t*>(lds4) + wave * REGION;
+  uint8_t* wl = xl + X;
   float* sums = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(lds4) + waves * REGION);
   float* ys = sums + wave * M * 16;
   float* s_w = sums + waves * M * 16;
@@ -398,17 +392,8 @@ __global__ __launch_bounds__(1024) void k_mx4_down(const uint8_t* __restrict__ d
   const int nblk = inter / 32, nchunk = (nblk + 3) / 4;
   const uint32_t hrow = (uint32_t)inter * 2u;
   const rsrc_t rh = make_rsrc(h, 3u * (uint32_t)P * hrow);
-  WChunk<1> next[U];
-#define KQ_LOAD(EXPERT, C)                                                                             \
-  {                                                                                                    \
-    rsrc_t rc[1], rs[1];                                                                               \
-    mx4_rows(dc, ds, (int64_t)(EXPERT) * hidden + blockIdx.x * 16, 16, nblk, rc[0], rs[0]);            \
-    _Pragma("unroll") for (int u = 0; u < U; ++u)                                                      \
-      load_w_chunk<T_BF16, 1, AL>(rc, rs, (C) + u < nchunk ? (C) + u : nblk, nblk, r, g, next[u]);     \
-  }
   const int all = waves * (int)gridDim.y;
   int p = (int)blockIdx.y * waves + wave, e = p < P ? __builtin_amdgcn_readfirstlane(ids[p]) : 0;
-  if (M == 1 && p < P) KQ_LOAD(e, 0)   // one token's experts differ: every slot leads
   for (int i = threadIdx.x; i < P; i += 64 * waves) {
     s_ids[i] = (uint16_t)ids[i];
     s_w[i] = weights[i];
@@ -418,10 +403,7 @@ __global__ __launch_bounds__(1024) void k_mx4_down(const uint8_t* __restrict__ d
   __syncthreads();
   if (M > 1) {
     while (p < P && s_groups[p] < 1 << 16) p += all;
-    if (p < P) {
-      e = __builtin_amdgcn_readfirstlane(s_ids[p]);
-      KQ_LOAD(e, 0)
-    }
+    if (p < P) e = __builtin_amdgcn_readfirstlane(s_ids[p]);
   }
   while (p < P) {
     int pn = p + all;
@@ -442,17 +424,16 @@ __global__ __launch_bounds__(1024) void k_mx4_down(const uint8_t* __restrict__ d
       const int have = piece < 3 ? r : 0;
       const uint8_t* xr[1] = {xl + have * (PR * 16)};
       v4f acc[1][1] = {};
+      rsrc_t rc[1], rs[1];
+      mx4_rows(dc, ds, (int64_t)e * hidden + blockIdx.x * 16, 16, nblk, rc[0], rs[0]);
       for (int c = 0; c < nchunk; c += U) {
+        stage_w<U, AL>(rc[0], rs[0], wl, wl + U * 1024, c, nblk, nblk);
         stage_x<T_BF16, U>(rh, xl, 3 * n, off, c, nblk * (Pieces<T_BF16>::v / 4));
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the region is filled (and these weights are here)
-        WChunk<1> w[U];
+        regions_filled();
 #pragma unroll
-        for (int u = 0; u < U; ++u) w[u] = next[u];
-        const bool more = c + U < nchunk;
-        if (more || pn < P) KQ_LOAD(more ? e : en, more ? c + U : 0)
-#pragma unroll
-        for (int u = 0; u < U; ++u) chunk_products<T_BF16, 1, 1, U>(xr, have & 7, u, w[u], g, acc);
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the region has been read
+        for (int u = 0; u < U; ++u)
+          if (c + u < nchunk) chunk_products<T_BF16, 1, 1, U>(xr, have & 7, u, wl, r, g, acc);
+        regions_read();
       }
       // the results take the region's place, 16 rows (columns of h) of 16
       float* res = reinterpret_cast<float*>(xl);
@@ -475,7 +456,6 @@ __global__ __launch_bounds__(1024) void k_mx4_down(const uint8_t* __restrict__ d
     p = pn;
     e = en;
   }
-#undef KQ_LOAD
   __syncthreads();
   for (int i = threadIdx.x; i < M * 16; i += 64 * waves) {
     float s = sums[i];
@@ -560,10 +540,10 @@ bool chooses_itself(const Mx4MoeArgs& a) {
   return a.route.M == 1 && a.route.E <= 512 && (a.inter / 32) * a.route.top_k < 512;
 }
 
-template <int XT, int TILES>
+template <int XT, int TILES, int COLS>
 int gate_up_cfg(const Mx4MoeArgs& a, uint16_t* h, int32_t* groups) {
-  typedef GateUp<XT, TILES> G;
-  constexpr int U = GU_CHUNKS;
+  typedef GateUp<XT, TILES, COLS> G;
+  constexpr int U = G::CHUNKS;
   const RouteArgs& r = a.route;
   const int P = r.M * r.top_k, nchunk = (int)((r.K / 32 + 3) / 4);
   int waves = (nchunk + U - 1) / U;   // a wave's part of K in its region, while the waves last
@@ -571,12 +551,13 @@ int gate_up_cfg(const Mx4MoeArgs& a, uint16_t* h, int32_t* groups) {
   const int splits = chooses_itself(a) ? route_splits(r.K) : 0;
   if (splits)   // a thread per expert, and the choice's scratch
     while (waves * 64 < r.E || waves * G::PER_WAVE < select_lds_bytes(waves, r.top_k)) ++waves;
-  // passes of twice an expert's mean number of slots (54 tokens, 15 experts, top 11: PASSES us)
-  const int mean2 = (2 * P + r.E - 1) / r.E, z = (mean2 + GuCols<XT>::v - 1) / GuCols<XT>::v;
+  // passes of twice an expert's mean number of slots (54 tokens, 15 experts of
+  // 480 x 896, top 11: 15.5 us against 56.5 with one workgroup walking all passes)
+  const int mean2 = (2 * P + r.E - 1) / r.E, z = (mean2 + COLS - 1) / COLS;
   const dim3 grid((unsigned)((a.inter / 16 + TILES - 1) / TILES), (unsigned)(P < r.E ? P : r.E), (unsigned)(z > 8 ? 8 : z));
   const size_t lds = (size_t)waves * G::PER_WAVE + (size_t)P * 4;
-  dispatch_log("k_mx4_gate_up", -1, a.inter, r.K, r.M, grid.x, grid.y, (unsigned)(64 * waves), lds, "type=%d tiles=%d chooses=%d", XT, TILES, splits > 0);
-  auto* k = r.K % 128 == 0 ? k_mx4_gate_up<XT, TILES, true> : k_mx4_gate_up<XT, TILES, false>;
+  dispatch_log("k_mx4_gate_up", -1, a.inter, r.K, r.M, grid.x, grid.y, (unsigned)(64 * waves), lds, "type=%d tiles=%d cols=%d chooses=%d", XT, TILES, COLS, splits > 0);
+  auto* k = r.K % 128 == 0 ? k_mx4_gate_up<XT, TILES, COLS, true> : k_mx4_gate_up<XT, TILES, COLS, false>;
   hipLaunchKernelGGL(k, grid, dim3((unsigned)(64 * waves)), lds, r.stream, a.codes[0], a.scales[0], a.codes[1],
                      a.scales[1], r.x, r.ids, h, (int)r.K, (int)a.inter, r.M, r.top_k, r.E, waves,
                      static_cast<const double*>(r.ws), splits, r.renorm, r.weights, groups);
@@ -585,11 +566,18 @@ int gate_up_cfg(const Mx4MoeArgs& a, uint16_t* h, int32_t* groups) {
 
 // Two tiles per workgroup spread what a workgroup does once over more rows
 // where the slots still fill the compute units (16 tokens, 128 experts of 768 x
-// 2048, top 8: 42.7 us against 48.2 with one and 50.5 with four).
+// 2048, top 8: 42.7 us against 48.2 with one and 50.5 with four). Passes of four
+// columns leave room for three workgroups per compute unit (those 16 tokens: 31
+// us against 35); experts with four slots and more on average take eight in
+// bf16 and fp16 (64 tokens, 16 experts of 1536 x 4096, top 4: layer 169 us
+// against 219).
 template <int XT>
 int gate_up_x(const Mx4MoeArgs& a, uint16_t* h, int32_t* groups) {
   const int P = a.route.M * a.route.top_k;
-  return (a.inter / 32) * (P < a.route.E ? P : a.route.E) >= 512 ? gate_up_cfg<XT, 2>(a, h, groups) : gate_up_cfg<XT, 1>(a, h, groups);
+  const bool two = (a.inter / 32) * (P < a.route.E ? P : a.route.E) >= 512;
+  if constexpr (XT != T_F32)
+    if (P >= 4 * a.route.E) return two ? gate_up_cfg<XT, 2, 8>(a, h, groups) : gate_up_cfg<XT, 1, 8>(a, h, groups);
+  return two ? gate_up_cfg<XT, 2, 4>(a, h, groups) : gate_up_cfg<XT, 1, 4>(a, h, groups);
 }
 
 // Workgroups that share the down projection's rows: with many slots, or few
@@ -609,7 +597,7 @@ int down_cfg(const Mx4MoeArgs& a, const uint16_t* h, const int32_t* groups, floa
   const RouteArgs& r = a.route;
   const int P = r.M * r.top_k;
   // a wave per slot up to what LDS holds; two workgroups to a compute unit where there are parts
-  const int shared = P * 10, per_wave = x_region_bytes<T_BF16, U>(3 * SLOTS) + r.M * 64;
+  const int shared = P * 10, per_wave = x_region_bytes<T_BF16, U>(3 * SLOTS) + w_region_bytes<1, U>() + r.M * 64;
   int waves = (MOE_LDS_BYTES / (count > 1 ? 2 : 1) - shared) / per_wave;
   const int most = count > 1 ? 8 : 16;
   waves = waves > most ? most : waves < 1 ? 1 : waves;
@@ -666,8 +654,8 @@ int launch_mx4_moe(const Mx4MoeArgs& a) {
         : r.xtype == KQ_F16 ? gate_up_x<T_F16>(a, h, groups)
                             : gate_up_x<T_BF16>(a, h, groups);
   if (err) return err;
-  return r.M == 1 ? down_cfg<6, 1>(a, h, groups, parts, 1)
-                  : down_cfg<3, DOWN_SLOTS>(a, h, groups, parts, down_parts(r.K, r.M * r.top_k));
+  return r.M == 1 ? down_cfg<4, 1>(a, h, groups, parts, 1)
+                  : down_cfg<2, DOWN_SLOTS>(a, h, groups, parts, down_parts(r.K, r.M * r.top_k));
 }
 
 }  // namespace kq
