@@ -555,3 +555,145 @@ def test_captured_and_on_another_stream():
             got = sets[k].outputs()
             assert all(t.equal(a, b) for a, b in zip(got, want[(i + k) % 5])), (i, k)
         _ = (xs[i].float() @ xs[i].float().T).sum().item()   # eager work and a synchronisation between replays
+
+
+# ------------------------------------------------------------------ ways the work is shared out
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("N,K,M", [(1000, 2080, 64),   # few row tiles: groups of 16 columns (16-bit types)
+                                   (1000, 2048, 50), (37, 13056, 33),
+                                   (1801, 160, 64), (1500, 544, 49),     # groups of 32
+                                   (8200, 160, 17), (8209, 256, 48), (8207, 96, 64),   # two row tiles
+                                   (1601, 160, 61), (3201, 288, 64), (12305, 128, 3), (12305, 160, 16)])   # fp32: two and four
+def test_gemv_shared_out(kind, N, K, M):
+    rng = np.random.default_rng((N, K, M, 3))
+    codes, scales = random_planes(rng, N, K)
+    pc, ps = upload(codes, scales)
+    x = as_type(activations(rng, M, K), kind)
+    y = Guarded(4 * M * N)
+    xd = dev(x)
+    kq.kq_mx4_gemv(pc.ptr, ps.ptr, kind, xd, y.ptr, N, K, M)
+    y.check(what=f"{kind} {N}x{K} M={M}")
+    got = U.to_host(y.buf)[GUARD:GUARD + 4 * M * N].view(np.float32).reshape(M, N)
+    check(got, *X.product(X.dequantize(codes, scales), X.widen(x)), K, what=f"{kind} {N}x{K} M={M}")
+
+
+@pytest.mark.parametrize("kind", TYPES)
+def test_longest_rows(kind):
+    """K at its limit: quantised, dequantised and multiplied in both products."""
+    K, M, N = 1 << 20, 5, 3
+    rng = np.random.default_rng(61)
+    x = as_type(activations(rng, M, K) * 0.01, kind)
+    codes, scales = random_planes(rng, N, K)
+    pw = upload(codes, scales)
+    w = X.dequantize(codes, scales)
+    c, s, y, yg = U.empty_dev((M, K // 2), "uint8"), U.empty_dev((M, K // 32), "uint8"), U.empty_dev((M, N)), U.empty_dev((M, N))
+    xd = dev(x)
+    kq.kq_mx4_quantize(kind, xd, K, c, s, M, K)
+    rc, rs = X.quantize(x)
+    pc, ps = X.planes(rc, rs)
+    assert np.array_equal(U.to_host(c), pc) and np.array_equal(U.to_host(s), ps)
+    kq.kq_mx4_gemv(pw[0].ptr, pw[1].ptr, kind, xd, y, N, K, M)
+    check(U.to_host(y), *X.product(w, X.widen(x)), K, what="gemv")
+    kq.kq_mx4_gemm(c, s, pw[0].ptr, pw[1].ptr, "f32", yg, M, N, K)
+    check(U.to_host(yg), *X.product(w, X.dequantize(rc, rs)), K, what="gemm")
+
+
+def test_many_rows_past_32_bit_offsets():
+    """A matrix whose code plane passes 4 GiB: the last rows are the last rows."""
+    t = U.torch_cuda()
+    K, N = 1024, (1 << 23) + 5
+    codes = t.zeros((N, K // 2), dtype=t.uint8, device="cuda")
+    scales = t.full((N, K // 32), 127, dtype=t.uint8, device="cuda")
+    rng = np.random.default_rng(62)
+    c, s = random_planes(rng, 40, K)
+    bc, bs = X.planes(c, s)
+    codes[-40:] = t.from_numpy(bc).to("cuda")
+    scales[-40:] = t.from_numpy(bs).to("cuda")
+    x = as_type(activations(rng, 2, K), "bf16")
+    y = U.empty_dev((2, N))
+    kq.kq_mx4_gemv(codes, scales, "bf16", dev(x), y, N, K, 2)
+    assert not bool(y[:, :-40].any())
+    check(y[:, -40:].cpu().numpy(), *X.product(X.dequantize(c, s), X.widen(x)), K)
+    ac, as_ = X.quantize(x)
+    pa = upload(ac, as_)
+    kq.kq_mx4_gemm(pa[0].ptr, pa[1].ptr, codes, scales, "f32", y, 2, N, K)
+    assert not bool(y[:, :-40].any())
+    check(y[:, -40:].cpu().numpy(), *X.product(X.dequantize(c, s), X.dequantize(ac, as_)), K)
+    v = t.empty((40, K), dtype=t.float32, device="cuda")
+    kq.kq_mx4_dequantize(codes[-40:], scales[-40:], "f32", v, K, 40, K)
+    kq.kq_mx4_quantize("f32", v, K, codes, scales, 40, K)   # into the first rows
+    back = t.empty((40, K), dtype=t.float32, device="cuda")
+    kq.kq_mx4_dequantize(codes, scales, "f32", back, K, 40, K)
+    assert t.equal(v, back)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("M,E,H,inter,top_k", [(1, 300, 160, 96, 7), (1, 512, 256, 64, 64), (1, 700, 96, 32, 5),     # one token: chosen in the experts' kernel, or not
+                                               (1, 1024, 64, 32, 64), (1, 9, 96, 2080, 8), (1, 3, 12320, 32, 2),
+                                               (64, 64, 32, 32, 64), (64, 80, 64, 32, 64),                             # every expert, 4096 slots
+                                               (64, 9, 160, 96, 3), (40, 5, 256, 544, 2), (33, 2, 64, 1056, 2),       # eight columns in a pass
+                                               (3, 7, 8352, 64, 3), (20, 3, 16384, 32, 1), (6, 4, 96, 8224, 2),       # long rows
+                                               (16, 8, 2048, 64, 4), (9, 8, 1056, 160, 8), (2, 40, 2080, 224, 33)])
+def test_layer_shared_out(kind, M, E, H, inter, top_k):
+    rng = np.random.default_rng((M, E, H, 5))
+    L = Layer(rng, E, H, inter)
+    x, W = as_type(activations(rng, M, H), kind), as_type(rng.standard_normal((E, H)) * H ** -0.5, kind)
+    y, ids, wts = L.run(x, kind, W, kind, top_k, False)
+    rid, rw, _ = X.route(X.widen(x), X.widen(W), top_k, False)
+    assert np.array_equal(ids, rid)
+    assert (np.abs(wts - rw) <= (2.0 ** -24 + 2.0 ** -30) * rw).all()
+    ref, bound = X.moe_layer(X.widen(x), *L.host, ids, wts.astype(np.float64))
+    err = np.abs(y - ref)
+    assert (err <= bound + 2.0 ** -120).all(), (err / bound).max()
+
+
+def test_one_token_captured_on_two_streams():
+    """Decode as it is captured: the one-token layer and the router, replayed on two streams at once, with workspaces of
+    their own that hold what other calls left there."""
+    t = U.torch_cuda()
+    rng = np.random.default_rng(63)
+    E, H, inter, top_k = 48, 512, 96, 6
+    L = Layer(rng, E, H, inter)
+    W = dev(as_type(rng.standard_normal((E, H)) * H ** -0.5, "f16"))
+    n = kq.kq_mx4_moe_layer_workspace_bytes(H, inter, 1, top_k, E)
+    nr = kq.kq_moe_route_workspace_bytes(1, E)
+
+    class Set:
+        def __init__(self):
+            self.x = t.zeros((1, H), dtype=t.float16, device="cuda")
+            self.y, self.ids, self.w = t.empty((1, H), device="cuda"), t.empty((1, top_k), dtype=t.int32, device="cuda"), t.empty((1, top_k), device="cuda")
+            self.ids2, self.w2 = t.empty_like(self.ids), t.empty_like(self.w)
+            self.ws = t.full((max(n, nr),), 0xFF, dtype=t.uint8, device="cuda")
+
+        def run(self):
+            kq.kq_mx4_moe_layer("f16", self.x, "f16", W, *[p.ptr for p in L.planes], self.y, self.ids, self.w, H, inter, 1,
+                                top_k, E, True, self.ws, n)
+            kq.kq_moe_route("f16", self.x, "f16", W, 1, H, E, top_k, True, self.ids2, self.w2, self.ws, nr)
+
+        def outputs(self):
+            return [a.clone() for a in (self.y, self.ids, self.w, self.ids2, self.w2)]
+
+    xs = [t.from_numpy(rng.standard_normal((1, H))).to("cuda", t.float16) for _ in range(6)]
+    sets, want = [Set(), Set()], []
+    for x in xs:
+        sets[0].x.copy_(x)
+        sets[0].run()
+        want.append(sets[0].outputs())
+        assert t.equal(want[-1][1], want[-1][3]) and t.equal(want[-1][2], want[-1][4])
+    graphs, streams = [], [t.cuda.Stream(), t.cuda.Stream()]
+    for s, st in zip(sets, streams):
+        st.wait_stream(t.cuda.current_stream())
+        g = t.cuda.CUDAGraph()
+        with t.cuda.graph(g, stream=st):
+            s.run()
+        graphs.append(g)
+    for i in range(6):
+        for k in (0, 1):
+            with t.cuda.stream(streams[k]):
+                sets[k].x.copy_(xs[(i + k) % 6])
+                graphs[k].replay()
+        t.cuda.synchronize()
+        for k in (0, 1):
+            assert all(t.equal(a, b) for a, b in zip(sets[k].outputs(), want[(i + k) % 6])), (i, k)
+        _ = (xs[i].float() ** 2).sum().item()
