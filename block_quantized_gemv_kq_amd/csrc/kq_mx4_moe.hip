@@ -19,6 +19,9 @@ namespace kqd {
 // 32 it + 8 g + j of expert row r and token row r to instruction j of step it.
 // A workgroup is one such tile and a part of K (blockIdx.z); its waves split that
 // and meet in LDS in wave order, and the choice adds the parts in their order.
+// Bound by one round trip to memory, which is why K is split over workgroups as
+// well: 128 experts of 2048 fp16 inputs 4.7 us (in one part 7), 512 experts of
+// 2048 bf16 inputs at 48 tokens 5.6.
 template <int T>
 __device__ __forceinline__ void to_f64(const u32x4 (&v)[T == T_F32 ? 2 : 1], double (&d)[8]) {
 #pragma unroll
@@ -80,7 +83,9 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void k_route_logits(const void* _
 // A wave ranks its 64 experts against each other (64 comparisons a lane, the
 // other keys through scalar registers) and passes on its top_k best in order;
 // these candidates are ranked against each other in the same way. Logits are
-// compared as integers that order like them; 0 is below every logit.
+// compared as integers that order like them; 0 is below every logit. Bound by
+// latency: 3.6 us for one token of 128 experts (picking them one at a time 8.6),
+// 7.3 for 48 tokens of 512 (15.2).
 __device__ __forceinline__ uint64_t logit_key(double v) {
   if (!(v == v)) v = -__builtin_inf();
   if (v == 0.0) v = 0.0;   // -0 and +0 are equal
@@ -369,7 +374,9 @@ __global__ __launch_bounds__((GateUp<XT, TILES, COLS>::MAX_WAVES * 64)) void k_m
 // of its own in LDS, and the waves' sums are added in wave order, so the result
 // does not depend on timing. With more than one workgroup for the rows, out is
 // theirs in turn and k_mx4_down_sum adds them. The operand columns are the
-// three pieces of h of a group's slots.
+// three pieces of h of a group's slots. Bound by memory and, at one token, by
+// latency: 16 tokens of 128 experts of 768 to 2048, top 8, 22.5 us and 4.8 for
+// the sum of the parts (68 MB of weights, 3.0 TB/s), one token 5.7.
 // Dynamic LDS: per wave a region, then per wave M x 16 sums, then the route
 // weights (P fp32), groups (P int32) and ids (P uint16).
 template <int U, int SLOTS, bool AL>

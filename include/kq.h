@@ -3,7 +3,9 @@
  *
  * A C ABI over hand-written HIP kernels for the memory-bound decode step of
  * LLM inference: dequantize-and-multiply of block-quantized weights against a
- * few activation columns, and the routed-expert (mixture-of-experts) variant.
+ * few activation columns, and the routed-expert (mixture-of-experts) variant;
+ * for microscaled 4-bit weights also the quantiser, the product of two such
+ * matrices, the router and the whole mixture-of-experts layer.
  *
  * Where the operation comes from (page title, section):
  *  - Kinetic docs, "What makes it fast": generating a token reads every weight
@@ -392,8 +394,8 @@ int64_t kq_mx4_moe_layer_workspace_bytes(int64_t hidden, int64_t inter, int M, i
 
 /* kq_mx4_moe_layer — a whole mixture-of-experts layer for a few tokens:
  * kq_moe_route, then the chosen experts' gated FFN with microscaled weights
- * and the weighted sum, with no host synchronisation (only the experts in use
- * are read, each once per call for all of its tokens):
+ * and the weighted sum, with no host synchronisation; only the experts in use
+ * are read:
  *   for token m, rank j, expert e = ids[m][j]:
  *     h = silu(Gate_e x_m) * (Up_e x_m), silu(z) = z / (1 + e^-z), in fp32
  *     y[m] = sum_j weights[m][j] * (Down_e h)
