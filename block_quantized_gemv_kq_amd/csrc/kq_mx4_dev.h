@@ -103,7 +103,7 @@ __device__ __forceinline__ void transpose_groups(uint32_t& a, uint32_t& b, uint3
 // own (no barrier): loads straight into the operand layout take four
 // instructions per chunk and column tile whether its columns exist or not, each
 // touching 16 rows (2560 x 9728 at 48 bf16 columns: 33 us, at any number of
-// waves, against 17), here one instruction per KiB of real columns. A row of the
+// waves, against 15), here one instruction per KiB of real columns. A row of the
 // region holds U chunks; its 16-byte piece p lies at p ^ (row & 7), so that
 // the operand reads of eight consecutive rows touch every bank. Lanes whose
 // column does not exist read an existing row: their results are never used.

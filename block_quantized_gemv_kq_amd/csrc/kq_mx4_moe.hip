@@ -572,8 +572,9 @@ int gate_up_cfg(const Mx4MoeArgs& a, uint16_t* h, int32_t* groups) {
 }
 
 // Two tiles per workgroup spread what a workgroup does once over more rows
-// where the slots still fill the compute units (16 tokens, 128 experts of 768 x
-// 2048, top 8: 42.7 us against 48.2 with one and 50.5 with four). Passes of four
+// where the slots still fill the compute units (16 fp32 tokens, 128 experts of
+// 768 x 2048, top 8: layer 88 us against 96 with one and 92 with four; bf16 66,
+// 66 and 70). Passes of four
 // columns leave room for three workgroups per compute unit (those 16 tokens: 31
 // us against 35); experts with four slots and more on average take eight in
 // bf16 and fp16 (64 tokens, 16 experts of 1536 x 4096, top 4: layer 169 us
@@ -590,8 +591,8 @@ int gate_up_x(const Mx4MoeArgs& a, uint16_t* h, int32_t* groups) {
 // Workgroups that share the down projection's rows: with many slots, or few
 // rows, one workgroup per 16 rows leaves compute units idle (and each reads all
 // of h). Two per compute unit, four slots and more each; the sum of the parts
-// costs a launch (16 tokens, top 8, 2048 rows: 37.1 us with one, 25.4 + 4.8 with
-// four; 4 tokens 13.3 against 11.8 + 4.8).
+// costs a launch of 4.8 us (16 tokens, top 8, 2048 rows: layer 72.5 us with one,
+// 66.3 with four; 4 tokens gain 1.5 us from parts, less than that launch).
 int down_parts(int64_t hidden, int P) {
   if (P < 64 && hidden > 1024) return 1;
   const int64_t fill = 512 / (hidden / 16), most = P / 4;
