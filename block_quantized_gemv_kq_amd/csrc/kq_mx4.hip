@@ -285,9 +285,12 @@ int gemv_cfg(const Mx4GemvArgs& a) {
 // workgroup takes them all, and two row tiles where that leaves a workgroup per
 // compute unit (19456 x 2560 at 48 bf16 columns: 21.6 us against 27.2 with one
 // tile and 41 with 16 columns each; 8192 x 4096 at 32: 9.8 against 12.9; 2560 x
-// 9728 at 48: 17.8 against 14.9). Where the row tiles are few, groups of columns
-// go to workgroups of their own as far as the compute units take them at once
-// (1000 x 14080 at 64 fp16 columns: 13.4 us against 31.5).
+// 9728 at 48: 17.8 against 14.9). Nine to 16 columns of rows that are not short
+// take two tiles from 384 tiles on (6144 x 2560 at 16 bf16 columns: 4.7 us
+// against 6.5, 19456 x 2560 12.5 against 15.5; 12000 x 1024 4.7 against 4.3).
+// Where the row tiles are few, groups of columns go to workgroups of their own
+// as far as the compute units take them at once (1000 x 14080 at 64 fp16
+// columns: 13.4 us against 31.5).
 template <int XT, int CT>
 int gemv_wide(const Mx4GemvArgs& a) {
   if (a.N >= 32 * 256) return gemv_cfg<XT, CT, 2, 1>(a);
@@ -298,6 +301,7 @@ template <int XT>
 int gemv_half(const Mx4GemvArgs& a) {
   const int64_t tiles = (a.N + 15) / 16, parts = (a.M + 15) / 16;
   if (a.M <= 8) return gemv_cfg<XT, 1, 1, 4>(a);
+  if (a.M <= 16 && tiles >= 384 && a.K >= 2048) return gemv_cfg<XT, 1, 2, 2>(a);
   if (a.M <= 16 || tiles * parts <= 256) return gemv_cfg<XT, 1, 1, 2>(a);
   if (a.M <= 32 || tiles * ((parts + 1) / 2) <= 256) return gemv_wide<XT, 2>(a);
   return a.M <= 48 ? gemv_wide<XT, 3>(a) : gemv_wide<XT, 4>(a);

@@ -697,3 +697,18 @@ def test_one_token_captured_on_two_streams():
         for k in (0, 1):
             assert all(t.equal(a, b) for a, b in zip(sets[k].outputs(), want[(i + k) % 6])), (i, k)
         _ = (xs[i].float() ** 2).sum().item()
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("N,K,M", [(6143, 2080, 9), (6161, 2048, 16), (6129, 2048, 13)])
+def test_gemv_two_row_tiles_of_up_to_16_columns(kind, N, K, M):
+    rng = np.random.default_rng((N, K, M, 4))
+    codes, scales = random_planes(rng, N, K)
+    pc, ps = upload(codes, scales)
+    x = as_type(activations(rng, M, K), kind)
+    y = Guarded(4 * M * N)
+    xd = dev(x)
+    kq.kq_mx4_gemv(pc.ptr, ps.ptr, kind, xd, y.ptr, N, K, M)
+    y.check(what=f"{kind} {N}x{K} M={M}")
+    got = U.to_host(y.buf)[GUARD:GUARD + 4 * M * N].view(np.float32).reshape(M, N)
+    check(got, *X.product(X.dequantize(codes, scales), X.widen(x)), K, what=f"{kind} {N}x{K} M={M}")
