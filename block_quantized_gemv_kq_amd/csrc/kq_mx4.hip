@@ -184,7 +184,7 @@ __global__ __launch_bounds__(1024) void k_mx4_gemv(const uint8_t* __restrict__ c
   mx4_tiles<RT>(codes, scales, row0, N, nblk, rc, rs);
   const uint32_t xrow = (uint32_t)K * TypeSize<XT>::v;
   const rsrc_t rx = make_rsrc(x, (uint32_t)M * xrow);
-  v4f acc[RT][CT] = {};
+  v4f acc[RT][CT];
   const int c0 = nchunk * wave / waves, c1 = nchunk * (wave + 1) / waves;
   const int m0 = (int)blockIdx.y * (16 * CT);
   const int cols = min(M - m0, 16 * CT), xbytes = x_region_bytes<XT, U>(min(M, 16 * CT)), region = xbytes + w_region_bytes<RT, U>();

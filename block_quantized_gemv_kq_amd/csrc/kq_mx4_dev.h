@@ -46,14 +46,30 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
   return one[0];
 }
 
-// Eight codes (one dword) times their scale as bf16: exact wherever bf16
-// reaches (every code and scale up to its largest finite value).
+// Eight codes (one dword) times their scale as bf16: exact as far as bf16
+// reaches (4 times 2^126 and 2 times 2^127, scale bytes 253 and 254, do not fit).
 __device__ __forceinline__ v8b codes_bf16(uint32_t d, float scale) {
   const v2b a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 0);
   const v2b b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 1);
   const v2b c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 2);
   const v2b e = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 3);
   return v8b{a[0], a[1], b[0], b[1], c[0], c[1], e[0], e[1]};
+}
+
+// Eight codes times a quarter of their scale as bf16: exact for every scale
+// byte (at most 1.5 * 2^127; the least, 2^-130, is a multiple of bf16's 2^-133).
+__device__ __forceinline__ v8b codes_quarter_bf16(uint32_t d, uint32_t byte) {
+  const float scale = scale_of(byte < 2u || byte == 255u ? byte : byte - 2u), rest = byte < 2u ? 0.25f : 1.0f;
+  const v2f a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, scale, 0);
+  const v2f b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, scale, 1);
+  const v2f c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, scale, 2);
+  const v2f e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, scale, 3);
+  const float f[8] = {a[0] * rest, a[1] * rest, b[0] * rest, b[1] * rest, c[0] * rest, c[1] * rest, e[0] * rest, e[1] * rest};
+  u32x4 h;   // the upper halves: a value has two significant bits
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    h[j] = perm(__builtin_bit_cast(uint32_t, f[2 * j + 1]), __builtin_bit_cast(uint32_t, f[2 * j]), 0x07060302u);
+  return __builtin_bit_cast(v8b, h);
 }
 
 // Eight codes as fp16, unscaled (exact).
@@ -92,6 +108,12 @@ __device__ __forceinline__ void transpose_groups(uint32_t& a, uint32_t& b, uint3
 // bf16 columns: the four matrix instructions of a chunk take dword s of every
 // lane, so lane group g contributes elements 8s..8s+7 of block 4c + g, and the
 // conversion applies each lane's own scale: the operand is the exact weight.
+// The largest scales pass bf16: a wave that has met a scale byte of 192 or more
+// (no weights in earnest have one) walks its chunks again, with a quarter of
+// every weight and four times each chunk's sum. Compiled into the ordinary way
+// it would take its registers (78 -> 128 for four column tiles). Looking for such
+// bytes takes two instructions per chunk and tile: 19456 x 2560 at 64 bf16
+// columns 25.7 and 25.3 us, at 64 fp32 columns 54.1 without and 55.5 with it.
 // fp32 columns: the same with the value split into three bf16 pieces of eight
 // bits each (24 in all: exact), three matrix instructions each.
 // fp16 columns: bf16 cannot hold them and fp16 cannot hold the scales, so the
@@ -189,11 +211,28 @@ __device__ __forceinline__ void split3(const float (&x)[8], v8b& hi, v8b& mid, v
   lo = __builtin_bit_cast(v8b, l);
 }
 
+// The bf16 pieces, the smallest first, of the eight bf16 or fp32 activations of
+// step s that a lane of group g takes from its region row at piece `base` on.
+template <int XT>
+__device__ __forceinline__ void x_pieces(const uint8_t* xrow, int base, int swz, int g, int s, v8b (&x)[XT == T_F32 ? 3 : 1]) {
+  if constexpr (XT == T_F32) {
+    const v4f a = *reinterpret_cast<const v4f*>(xrow + (base + ((8 * g + 2 * s) ^ swz)) * 16);
+    const v4f b = *reinterpret_cast<const v4f*>(xrow + (base + ((8 * g + 2 * s + 1) ^ swz)) * 16);
+    const float f[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    split3(f, x[2], x[1], x[0]);
+  } else {
+    x[0] = *reinterpret_cast<const v8b*>(xrow + (base + ((4 * g + s) ^ swz)) * 16);
+  }
+}
+
 // acc += the products of chunk u of the regions. xrow[t]: the region row of the
 // lane's column in column tile t; swz: its row & 7, the same for every t.
+// Bit 7 of a byte of `seen` is set where a scale byte has been 192 or more (bf16
+// and fp32 columns).
 template <int XT, int CT, int RT, int U>
 __device__ __forceinline__ void chunk_products(const uint8_t* (&xrow)[CT], int swz, int u, const uint8_t* wl, int r, int g,
-                                               v4f (&acc)[RT][CT]) {
+                                               v4f (&acc)[RT][CT], uint32_t& seen) {
+  constexpr int XP = XT == T_F32 ? 3 : 1;
   const int base = u * Pieces<XT>::v;
   u32x4 codes[RT];
   uint32_t scale[RT];
@@ -227,7 +266,10 @@ __device__ __forceinline__ void chunk_products(const uint8_t* (&xrow)[CT], int s
   } else {
     float sc[RT];
 #pragma unroll
-    for (int t = 0; t < RT; ++t) sc[t] = scale_of((scale[t] >> (8 * g)) & 255u);
+    for (int t = 0; t < RT; ++t) {
+      sc[t] = scale_of((scale[t] >> (8 * g)) & 255u);
+      seen |= scale[t] & (scale[t] << 1);
+    }
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       v8b wb[RT];
@@ -235,23 +277,12 @@ __device__ __forceinline__ void chunk_products(const uint8_t* (&xrow)[CT], int s
       for (int t = 0; t < RT; ++t) wb[t] = codes_bf16(codes[t][s], sc[t]);
 #pragma unroll
       for (int c = 0; c < CT; ++c) {
-        if constexpr (XT == T_BF16) {
-          const v8b x = *reinterpret_cast<const v8b*>(xrow[c] + (base + ((4 * g + s) ^ swz)) * 16);
+        v8b x[XP];
+        x_pieces<XT>(xrow[c], base, swz, g, s, x);
 #pragma unroll
-          for (int t = 0; t < RT; ++t) acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, wb[t], acc[t][c], 0, 0, 0);
-        } else {
-          const v4f a = *reinterpret_cast<const v4f*>(xrow[c] + (base + ((8 * g + 2 * s) ^ swz)) * 16);
-          const v4f b = *reinterpret_cast<const v4f*>(xrow[c] + (base + ((8 * g + 2 * s + 1) ^ swz)) * 16);
-          const float f[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-          v8b hi, mid, lo;
-          split3(f, hi, mid, lo);
+        for (int t = 0; t < RT; ++t)
 #pragma unroll
-          for (int t = 0; t < RT; ++t) {
-            acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, wb[t], acc[t][c], 0, 0, 0);
-            acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(mid, wb[t], acc[t][c], 0, 0, 0);
-            acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, wb[t], acc[t][c], 0, 0, 0);
-          }
-        }
+          for (int p = 0; p < XP; ++p) acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[p], wb[t], acc[t][c], 0, 0, 0);
       }
     }
   }
@@ -262,7 +293,57 @@ __device__ __forceinline__ void regions_filled() { asm volatile("s_waitcnt vmcnt
 // Regions read: the next copies may take their place.
 __device__ __forceinline__ void regions_read() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-// acc += the products of chunks [c0, c1) (wave-uniform) with `rows` columns
+// acc += the products of the first n chunks of the regions, the way that fits
+// every scale. Loops stay loops, one sum at a time, to take few registers.
+template <int XT, int CT, int RT, int U>
+__device__ __forceinline__ void large_products(const uint8_t* (&xrow)[CT], int swz, int n, const uint8_t* wl, int r, int g,
+                                               v4f (&acc)[RT][CT]) {
+  constexpr int XP = XT == T_F32 ? 3 : 1;
+#pragma unroll 1
+  for (int u = 0; u < n; ++u)
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const uint8_t* codes = wl + t * U * 1024 + (r * (4 * U) + ((4 * u + g) ^ (r & (4 * U - 1)))) * 16;
+      const uint32_t byte = wl[RT * U * 1024 + t * U * 64 + (r * U + u) * 4 + g];
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        v4f quarter = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          __builtin_amdgcn_sched_barrier(0);
+          const v8b wb = codes_quarter_bf16(*reinterpret_cast<const uint32_t*>(codes + 4 * s), byte);
+          v8b x[XP];
+          x_pieces<XT>(xrow[c], u * Pieces<XT>::v, swz, g, s, x);
+#pragma unroll
+          for (int p = 0; p < XP; ++p) quarter = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[p], wb, quarter, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][c][i] = __builtin_fmaf(4.0f, quarter[i], acc[t][c][i]);
+      }
+    }
+}
+
+// acc += the products of the first n (up to U) chunks of the filled regions.
+template <bool LARGE, int XT, int CT, int RT, int U>
+__device__ __forceinline__ void step_products(const uint8_t* (&xrow)[CT], int swz, int n, const uint8_t* wl, int r, int g,
+                                              v4f (&acc)[RT][CT], uint32_t& seen) {
+  if constexpr (LARGE && XT != T_F16) {
+    large_products<XT, CT, RT, U>(xrow, swz, min(n, U), wl, r, g, acc);
+  } else {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (u < n) chunk_products<XT, CT, RT, U>(xrow, swz, u, wl, r, g, acc, seen);
+  }
+}
+
+template <bool L> struct Large { static constexpr bool value = L; };
+// Whether the wave has to walk its chunks again (wave-uniform): see above.
+template <int XT>
+__device__ __forceinline__ bool again(uint32_t seen) {
+  return XT != T_F16 && __builtin_amdgcn_ballot_w64((seen & 0x80808080u) != 0) != 0;
+}
+
+// acc = the products of chunks [c0, c1) (wave-uniform) with `rows` columns
 // (1 to 16 CT). rc[t], rs[t]: the code and scale rows of tile t (rows past the
 // matrix read zero); xl, wl: the wave's regions; off: see stage_x.
 template <int XT, int CT, int RT, int U, bool AL, class Off>
@@ -280,17 +361,24 @@ __device__ __forceinline__ void mx4_tile(const rsrc_t (&rc)[RT], const rsrc_t (&
     if (c == 0) swz = have & 7;
   }
   const int end = min(c1 * Pieces<XT>::v, nblk * (Pieces<XT>::v / 4));
-  for (int c = c0; c < c1; c += U) {
+  const auto walk = [&](auto large) {
+    uint32_t seen = 0;
 #pragma unroll
     for (int t = 0; t < RT; ++t)
-      stage_w<U, AL>(rc[t], rs[t], wl + t * U * 1024, wl + RT * U * 1024 + t * U * 64, c, min(4 * c1, nblk), nblk);
-    stage_x<XT, U>(rx, xl, rows, off, c, end);
-    regions_filled();
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (c + u < c1) chunk_products<XT, CT, RT, U>(xrow, swz, u, wl, r, g, acc);
-    regions_read();
-  }
+      for (int u = 0; u < CT; ++u) acc[t][u] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int c = c0; c < c1; c += U) {
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+        stage_w<U, AL>(rc[t], rs[t], wl + t * U * 1024, wl + RT * U * 1024 + t * U * 64, c, min(4 * c1, nblk), nblk);
+      stage_x<XT, U>(rx, xl, rows, off, c, end);
+      regions_filled();
+      step_products<decltype(large)::value, XT, CT, RT, U>(xrow, swz, c1 - c, wl, r, g, acc, seen);
+      regions_read();
+    }
+    return seen;
+  };
+  if (again<XT>(walk(Large<false>()))) walk(Large<true>());
 }
 
 // Rows [row0, row0 + rows) of the planes of a matrix as buffers.

@@ -322,26 +322,31 @@ __global__ __launch_bounds__((GateUp<XT, TILES, COLS>::MAX_WAVES * 64)) void k_m
     const auto off = [=](int c) { return (uint32_t)__shfl((int)xoff, c, 64); };
     const int have = r < cols ? r : 0;
     const uint8_t* xr[1] = {xl + have * (Pieces<XT>::v * U * 16)};
-    v4f acc[TILES][2][1] = {};
-    for (int c = c0; c < c1; c += U) {   // once, unless K is longer than the waves' regions
-      stage_x<XT, U>(rx, xl, cols, off, c, min(c1 * Pieces<XT>::v, nblk * (Pieces<XT>::v / 4)));
+    v4f acc[TILES][2][1];
+    const auto walk = [&](auto large) {
+      uint32_t seen = 0;
 #pragma unroll
-      for (int t = 0; t < TILES; ++t) {
-        rsrc_t rc[2], rs[2];
-        const int rows = 16 * (tile0 + t) < inter ? 16 : 0;
-        const int64_t row = (int64_t)e * inter + (rows ? 16 * (tile0 + t) : 0);
-        mx4_rows(gc, gs, row, rows, nblk, rc[0], rs[0]);
-        mx4_rows(uc, us, row, rows, nblk, rc[1], rs[1]);
+      for (int t = 0; t < TILES; ++t) acc[t][0][0] = acc[t][1][0] = v4f{0.f, 0.f, 0.f, 0.f};
+      for (int c = c0; c < c1; c += U) {   // once, unless K is longer than the waves' regions
+        stage_x<XT, U>(rx, xl, cols, off, c, min(c1 * Pieces<XT>::v, nblk * (Pieces<XT>::v / 4)));
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          stage_w<U, AL>(rc[i], rs[i], wl + i * U * 1024, wl + 2 * U * 1024 + i * U * 64, c, min(4 * c1, nblk), nblk);
-        regions_filled();
+        for (int t = 0; t < TILES; ++t) {
+          rsrc_t rc[2], rs[2];
+          const int rows = 16 * (tile0 + t) < inter ? 16 : 0;
+          const int64_t row = (int64_t)e * inter + (rows ? 16 * (tile0 + t) : 0);
+          mx4_rows(gc, gs, row, rows, nblk, rc[0], rs[0]);
+          mx4_rows(uc, us, row, rows, nblk, rc[1], rs[1]);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (c + u < c1) chunk_products<XT, 1, 2, U>(xr, have & 7, u, wl, r, g, acc[t]);
-        regions_read();
+          for (int i = 0; i < 2; ++i)
+            stage_w<U, AL>(rc[i], rs[i], wl + i * U * 1024, wl + 2 * U * 1024 + i * U * 64, c, min(4 * c1, nblk), nblk);
+          regions_filled();
+          step_products<decltype(large)::value, XT, 1, 2, U>(xr, have & 7, c1 - c, wl, r, g, acc[t], seen);
+          regions_read();
+        }
       }
-    }
+      return seen;
+    };
+    if (again<XT>(walk(Large<false>()))) walk(Large<true>());
     __syncthreads();   // the sums take the regions' place
     v4f* red = reinterpret_cast<v4f*>(lds);   // [wave][tile][gate, up][64]
 #pragma unroll
@@ -400,7 +405,8 @@ __global__ __launch_bounds__(1024) void k_mx4_down(const uint8_t* __restrict__ d
   const uint32_t hrow = (uint32_t)inter * 2u;
   const rsrc_t rh = make_rsrc(h, 3u * (uint32_t)P * hrow);
   const int all = waves * (int)gridDim.y;
-  int p = (int)blockIdx.y * waves + wave, e = p < P ? __builtin_amdgcn_readfirstlane(ids[p]) : 0;
+  const int first = (int)blockIdx.y * waves + wave;
+  int e = first < P ? __builtin_amdgcn_readfirstlane(ids[first]) : 0;
   for (int i = threadIdx.x; i < P; i += 64 * waves) {
     s_ids[i] = (uint16_t)ids[i];
     s_w[i] = weights[i];
@@ -408,15 +414,13 @@ __global__ __launch_bounds__(1024) void k_mx4_down(const uint8_t* __restrict__ d
   }
   for (int i = lane; i < M * 16; i += 64) ys[i] = 0.0f;
   __syncthreads();
-  if (M > 1) {
-    while (p < P && s_groups[p] < 1 << 16) p += all;
-    if (p < P) e = __builtin_amdgcn_readfirstlane(s_ids[p]);
-  }
-  while (p < P) {
-    int pn = p + all;
-    while (pn < P && s_groups[pn] < 1 << 16) pn += all;
-    const int en = pn < P ? __builtin_amdgcn_readfirstlane(s_ids[pn]) : 0;
-    {
+  // e: the expert of the wave's first group
+  const auto walk = [&](auto large, int p, int e) {
+    uint32_t seen = 0;
+    while (p < P) {
+      int pn = p + all;
+      while (pn < P && s_groups[pn] < 1 << 16) pn += all;
+      const int en = pn < P ? __builtin_amdgcn_readfirstlane(s_ids[pn]) : 0;
       // column piece * n + m: that piece of h of slot m of this group
       const int n = __builtin_amdgcn_readfirstlane(s_groups[p] >> 16), piece = r / n, m = r - piece * n;
       int slots[SLOTS];
@@ -437,9 +441,7 @@ __global__ __launch_bounds__(1024) void k_mx4_down(const uint8_t* __restrict__ d
         stage_w<U, AL>(rc[0], rs[0], wl, wl + U * 1024, c, nblk, nblk);
         stage_x<T_BF16, U>(rh, xl, 3 * n, off, c, nblk * (Pieces<T_BF16>::v / 4));
         regions_filled();
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (c + u < nchunk) chunk_products<T_BF16, 1, 1, U>(xr, have & 7, u, wl, r, g, acc);
+        step_products<decltype(large)::value, T_BF16, 1, 1, U>(xr, have & 7, nchunk - c, wl, r, g, acc, seen);
         regions_read();
       }
       // the results take the region's place, 16 rows (columns of h) of 16
@@ -459,9 +461,19 @@ __global__ __launch_bounds__(1024) void k_mx4_down(const uint8_t* __restrict__ d
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read before the next copies land there
+      p = pn;
+      e = en;
     }
-    p = pn;
-    e = en;
+    return seen;
+  };
+  int p0 = first;
+  if (M > 1) {
+    while (p0 < P && s_groups[p0] < 1 << 16) p0 += all;
+    if (p0 < P) e = __builtin_amdgcn_readfirstlane(s_ids[p0]);
+  }
+  if (again<T_BF16>(walk(Large<false>(), p0, e))) {
+    for (int i = lane; i < M * 16; i += 64) ys[i] = 0.0f;
+    walk(Large<true>(), p0, e);
   }
   __syncthreads();
   for (int i = threadIdx.x; i < M * 16; i += 64 * waves) {

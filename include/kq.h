@@ -304,8 +304,10 @@ int kq_gemv_argmax_noalloc(int fmt, const void* W, const uint16_t* x, float* y,
  *   codes:  uint8 [R][K/2], element 2i of a row in the low nibble of its byte
  *           i and element 2i + 1 in the high nibble; 16-byte aligned.
  *   scales: uint8 [R][K/32]; 4-byte aligned.
- * A matrix has at most KQ_MX4_MAX_ROWS rows. Values whose magnitude reaches
- * 2^128 (scale byte 254 with codes of 2 and more) count as infinite.
+ * A matrix has at most KQ_MX4_MAX_ROWS rows. Values of 2^128 and more (scale
+ * byte 253 with magnitudes 4 and 6, 254 with 2 and more) do not fit fp32 and
+ * bf16: kq_mx4_dequantize returns infinities for them. The products take them as
+ * they are, whatever the activations' type: only a sum past fp32 is infinite.
  *
  * All matrices of these calls are in device memory. No buffer a call writes
  * may overlap one it reads. */
@@ -329,8 +331,9 @@ int kq_mx4_quantize(int type, const void* x, int64_t ldx, void* codes, void* sca
                     void* stream);
 
 /* kq_mx4_dequantize — the values of the planes as elements of type `type`,
- * row r at ldo * r elements after out. Exact in fp32 and bf16; rounded to
- * nearest even (infinite past the largest finite value) in fp16.
+ * row r at ldo * r elements after out. Exact in fp32 and bf16 below 2^128 and
+ * infinite from there on; rounded to nearest even (infinite past the largest
+ * finite value) in fp16.
  * Arguments otherwise and errors as kq_mx4_quantize. */
 int kq_mx4_dequantize(const void* codes, const void* scales, int type, void* out, int64_t ldo, int64_t R, int64_t K,
                       void* stream);

@@ -54,13 +54,17 @@ def planes(codes: np.ndarray, scales: np.ndarray):
     return (codes[:, 0::2] | (codes[:, 1::2] << 4)).astype(np.uint8), scales.astype(np.uint8)
 
 
-def dequantize(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
-    """fp64 values [R][K] (values of 2^128 and more are infinite, scale 255 NaN)."""
+def values(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
+    """fp64 values [R][K]: code times scale (up to 6 * 2^127; scale 255 NaN), as the products take them."""
     sign = np.where(codes & 8, -1.0, 1.0)
     s = np.repeat(scales.astype(np.int64), BLOCK, axis=1)
-    v = np.ldexp(MAGNITUDES[codes & 7], (s - 127).astype(np.int32))
-    v = np.where(v >= 2.0 ** 128, np.inf, v)
-    return np.where(s == 255, np.nan, sign * v)
+    return np.where(s == 255, np.nan, sign * np.ldexp(MAGNITUDES[codes & 7], (s - 127).astype(np.int32)))
+
+
+def dequantize(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
+    """The values as fp32 and bf16 hold them: infinite from 2^128 on."""
+    v = values(codes, scales)
+    return np.where(np.abs(v) >= 2.0 ** 128, np.copysign(np.inf, v), v)
 
 
 def product(w: np.ndarray, x: np.ndarray):

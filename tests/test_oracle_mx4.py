@@ -98,3 +98,14 @@ def test_layer_of_one_expert_is_its_ffn():
     z = x @ g[0].T
     assert np.allclose(y, (z / (1 + np.exp(-z)) * (x @ u[0].T)) @ d[0].T, rtol=1e-12)
     assert (bound > 0).all() and (bound < 1e-2 * np.abs(y).max()).all()
+
+
+def test_values_past_fp32():
+    """Code times scale up to 6 * 2^127; infinite only as fp32 or bf16 hold it."""
+    c, s = np.full((4, 32), 7, np.uint8), np.array([[252], [253], [254], [255]], np.uint8)
+    c[:, 1], c[:, 2] = 8 | 4, 2
+    v = X.values(c, s)
+    assert v[:3, :3].tolist() == [[6 * 2.0 ** (b - 127), -(2.0 ** (b - 126)), 2.0 ** (b - 127)] for b in (252, 253, 254)]
+    d = X.dequantize(c, s)
+    assert d[:3, :3].tolist() == [v[0, :3].tolist(), [np.inf, -(2.0 ** 127), 2.0 ** 126], [np.inf, -np.inf, 2.0 ** 127]]
+    assert np.isnan(v[3]).all() and np.isnan(d[3]).all()
