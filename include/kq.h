@@ -378,8 +378,9 @@ int64_t kq_moe_route_workspace_bytes(int M, int n_experts);
  *   ids[m]: the top_k experts of largest l, the largest first; the lower index
  *           first among equals; a NaN counts as minus infinity in this order.
  *   weights[m][j]: exp(l[ids[m][j]]) over the sum of exp(l) of the chosen
- *           (renorm 1) or of all experts (renorm 0); where a logit that enters
- *           the sum is NaN or infinite, the weights are NaN.
+ *           (renorm 1) or of all experts (renorm 0). A logit of minus infinity
+ *           has the weight 0; where a logit that enters the sum is NaN or plus
+ *           infinity, or all of them are minus infinity, the weights are NaN.
  * Both are as kq_moe_gemv, kq_moe_ffn take them. Logits and softmax are
  * computed in 64 bits: the choice is that of exact arithmetic unless two
  * logits agree to about 50 bits.
