@@ -717,7 +717,7 @@ int check_convert(const char* who, int type, const void* dense, int64_t ld, cons
   if (!aligned(dense, type_size(type))) return fail(KQ_ERR_ALIGN, "%s: elements must be aligned to their size", who);
   if (!aligned(codes, 16) || !aligned(scales, 4))
     return fail(KQ_ERR_ALIGN, "%s: codes must be 16-byte and scales 4-byte aligned", who);
-  if (!kq::mx4_walk_fits(R, K, ld)) return fail(KQ_ERR_ARG, "%s: too many strided rows", who);
+  if (!kq::mx4_walk_fits(R, K, ld)) return fail(KQ_ERR_ARG, "%s: more strided rows than a grid reaches", who);
   return KQ_OK;
 }
 

@@ -211,7 +211,7 @@ int copy_to_device(void* dst, const void* src, int64_t bytes, hipStream_t stream
 int read_from_device(void* dst, const void* src, int64_t bytes, hipStream_t stream);
 
 // ---- microscaled 4-bit matrices (kq_mx4*.hip)
-// Whether the quantise and dequantise grids reach this shape.
+// Whether the quantise and dequantise grids reach this shape (contiguous rows always).
 bool mx4_walk_fits(int64_t R, int64_t K, int64_t ld);
 int launch_mx4_quantize(int type, const void* x, int64_t ldx, void* codes, void* scales, int64_t R, int64_t K,
                         hipStream_t stream);

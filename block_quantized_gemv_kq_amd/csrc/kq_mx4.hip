@@ -206,57 +206,73 @@ namespace {
 // Rows as the kernels walk them: contiguous rows are one long row.
 struct Walk {
   int64_t rows, groups;
-  uint32_t chunks;
-  uint64_t blocks;
+  bool contiguous;
 };
-Walk walk_of(int64_t R, int64_t K, bool contiguous) {
-  Walk w;
-  w.rows = contiguous ? 1 : R;
-  w.groups = (contiguous ? R * K : K) / 8;
-  const int64_t chunks = (w.groups + 255) / 256;
-  w.chunks = (uint32_t)chunks;
-  w.blocks = (uint64_t)w.rows * (uint64_t)chunks;
-  return w;
+Walk walk_of(int64_t R, int64_t K, int64_t ld) {
+  return ld == K ? Walk{1, R * K / 8, true} : Walk{R, K / 8, false};
+}
+int64_t blocks_of(int64_t rows, int64_t groups) { return rows * ((groups + 255) / 256); }
+
+// A grid has less than 2^32 threads: contiguous rows of more than 2^34 elements
+// (8 a thread, half of what would fit) are several launches, one after another.
+constexpr int64_t PIECE_GROUPS = (int64_t)1 << 31;
+
+// launch(first group, groups, blocks) for each piece; the first error ends it.
+template <class Launch>
+int each_piece(const Walk& w, Launch launch) {
+  const int64_t step = w.contiguous ? PIECE_GROUPS : w.groups;
+  for (int64_t first = 0; first < w.groups; first += step) {
+    const int64_t groups = w.groups - first < step ? w.groups - first : step;
+    const int err = launch(first, groups, (unsigned)blocks_of(w.rows, groups));
+    if (err) return err;
+  }
+  return 0;
 }
 
 }  // namespace
 
 bool mx4_walk_fits(int64_t R, int64_t K, int64_t ld) {
-  return walk_of(R, K, ld == K).blocks <= 0xffffffffull / 256;   // a grid has less than 2^32 threads
+  const Walk w = walk_of(R, K, ld);
+  return w.contiguous || blocks_of(w.rows, w.groups) <= 0xffffffffll / 256;
 }
 
 int launch_mx4_quantize(int type, const void* x, int64_t ldx, void* codes, void* scales, int64_t R, int64_t K,
                         hipStream_t stream) {
-  const Walk w = walk_of(R, K, ldx == K);
+  const Walk w = walk_of(R, K, ldx);
   const int size = type == KQ_F32 ? 4 : 2;
   const bool vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (w.rows == 1 || ldx * size % 16 == 0);
-  dispatch_log("k_mx4_quantize", -1, R, K, 0, (unsigned)w.blocks, 1, 256, 0, "type=%d vec=%d", type, (int)vec);
+  return each_piece(w, [&](int64_t first, int64_t groups, unsigned blocks) {
+    dispatch_log("k_mx4_quantize", -1, R, K, 0, blocks, 1, 256, 0, "type=%d vec=%d", type, (int)vec);
 #define KQ_LAUNCH(T, V)                                                                                        \
-  hipLaunchKernelGGL((k_mx4_quantize<T, V>), dim3((unsigned)w.blocks), dim3(256), 0, stream,                   \
-                     static_cast<const uint8_t*>(x), ldx* size, static_cast<uint8_t*>(codes),                  \
-                     static_cast<uint8_t*>(scales), w.groups, w.chunks)
-  if (type == KQ_F32) { if (vec) KQ_LAUNCH(T_F32, true); else KQ_LAUNCH(T_F32, false); }
-  else if (type == KQ_F16) { if (vec) KQ_LAUNCH(T_F16, true); else KQ_LAUNCH(T_F16, false); }
-  else { if (vec) KQ_LAUNCH(T_BF16, true); else KQ_LAUNCH(T_BF16, false); }
+  hipLaunchKernelGGL((k_mx4_quantize<T, V>), dim3(blocks), dim3(256), 0, stream,                               \
+                     static_cast<const uint8_t*>(x) + first * 8 * size, ldx* size,                             \
+                     static_cast<uint8_t*>(codes) + first * 4, static_cast<uint8_t*>(scales) + first / 4, groups, \
+                     (uint32_t)((groups + 255) / 256))
+    if (type == KQ_F32) { if (vec) KQ_LAUNCH(T_F32, true); else KQ_LAUNCH(T_F32, false); }
+    else if (type == KQ_F16) { if (vec) KQ_LAUNCH(T_F16, true); else KQ_LAUNCH(T_F16, false); }
+    else { if (vec) KQ_LAUNCH(T_BF16, true); else KQ_LAUNCH(T_BF16, false); }
 #undef KQ_LAUNCH
-  return (int)hipGetLastError();
+    return (int)hipGetLastError();
+  });
 }
 
 int launch_mx4_dequantize(const void* codes, const void* scales, int type, void* out, int64_t ldo, int64_t R,
                           int64_t K, hipStream_t stream) {
-  const Walk w = walk_of(R, K, ldo == K);
+  const Walk w = walk_of(R, K, ldo);
   const int size = type == KQ_F32 ? 4 : 2;
   const bool vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0 && (w.rows == 1 || ldo * size % 16 == 0);
-  dispatch_log("k_mx4_dequantize", -1, R, K, 0, (unsigned)w.blocks, 1, 256, 0, "type=%d vec=%d", type, (int)vec);
+  return each_piece(w, [&](int64_t first, int64_t groups, unsigned blocks) {
+    dispatch_log("k_mx4_dequantize", -1, R, K, 0, blocks, 1, 256, 0, "type=%d vec=%d", type, (int)vec);
 #define KQ_LAUNCH(T, V)                                                                                        \
-  hipLaunchKernelGGL((k_mx4_dequantize<T, V>), dim3((unsigned)w.blocks), dim3(256), 0, stream,                 \
-                     static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales),                  \
-                     static_cast<uint8_t*>(out), ldo* size, w.groups, w.chunks)
-  if (type == KQ_F32) { if (vec) KQ_LAUNCH(T_F32, true); else KQ_LAUNCH(T_F32, false); }
-  else if (type == KQ_F16) { if (vec) KQ_LAUNCH(T_F16, true); else KQ_LAUNCH(T_F16, false); }
-  else { if (vec) KQ_LAUNCH(T_BF16, true); else KQ_LAUNCH(T_BF16, false); }
+  hipLaunchKernelGGL((k_mx4_dequantize<T, V>), dim3(blocks), dim3(256), 0, stream,                             \
+                     static_cast<const uint8_t*>(codes) + first * 4, static_cast<const uint8_t*>(scales) + first / 4, \
+                     static_cast<uint8_t*>(out) + first * 8 * size, ldo* size, groups, (uint32_t)((groups + 255) / 256))
+    if (type == KQ_F32) { if (vec) KQ_LAUNCH(T_F32, true); else KQ_LAUNCH(T_F32, false); }
+    else if (type == KQ_F16) { if (vec) KQ_LAUNCH(T_F16, true); else KQ_LAUNCH(T_F16, false); }
+    else { if (vec) KQ_LAUNCH(T_BF16, true); else KQ_LAUNCH(T_BF16, false); }
 #undef KQ_LAUNCH
-  return (int)hipGetLastError();
+    return (int)hipGetLastError();
+  });
 }
 
 namespace {

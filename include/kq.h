@@ -325,8 +325,9 @@ int kq_gemv_argmax_noalloc(int fmt, const void* W, const uint16_t* x, float* y,
  * planes do not depend on the kernel.
  *   x need only be aligned to its elements; rows aligned to 16 bytes are faster.
  * R == 0 is a valid empty call.
- * Errors: KQ_ERR_ARG (null, unknown type, R out of range, ldx < K or > 2^35, or
- * more strided rows than a grid reaches), KQ_ERR_SHAPE, KQ_ERR_ALIGN, KQ_ERR_HIP. */
+ * Errors: KQ_ERR_ARG (null, unknown type, R out of range, ldx < K or > 2^35, or,
+ * where ldx > K, more rows than a grid reaches: R times K / 2048 rounded up must
+ * be below 2^24), KQ_ERR_SHAPE, KQ_ERR_ALIGN, KQ_ERR_HIP. */
 int kq_mx4_quantize(int type, const void* x, int64_t ldx, void* codes, void* scales, int64_t R, int64_t K,
                     void* stream);
 
