@@ -279,17 +279,26 @@ namespace {
 
 constexpr int LDS_BYTES = 160 * 1024;   // of a compute unit
 
+// Waves of a workgroup, one batch of loads each while LDS lasts, and its LDS.
 template <int XT, int CT, int RT, int U>
-int gemv_cfg(const Mx4GemvArgs& a) {
+int gemv_waves(const Mx4GemvArgs& a, int* lds) {
   const int nchunk = (int)((a.K / 32 + 3) / 4);
   const int region = x_region_bytes<XT, U>(a.M < 16 * CT ? a.M : 16 * CT) + w_region_bytes<RT, U>(), sums = RT * CT * 1024;
   const int per_wave = CT == 1 ? region + sums : region > sums ? region : sums;
-  int waves = (nchunk + U - 1) / U;   // one batch of loads per wave
+  int waves = (nchunk + U - 1) / U;
   const int most = LDS_BYTES / per_wave < 16 ? LDS_BYTES / per_wave : 16;
   waves = waves > most ? most : waves;
+  *lds = waves * per_wave;
+  return waves;
+}
+
+template <int XT, int CT, int RT, int U>
+int gemv_cfg(const Mx4GemvArgs& a) {
+  int bytes;
+  const int waves = gemv_waves<XT, CT, RT, U>(a, &bytes);
   const unsigned grid = (unsigned)((a.N + 16 * RT - 1) / (16 * RT));
   const unsigned parts = (unsigned)((a.M + 16 * CT - 1) / (16 * CT));
-  const size_t lds = (size_t)waves * per_wave;
+  const size_t lds = (size_t)bytes;
   dispatch_log("k_mx4_gemv", -1, a.N, a.K, a.M, grid, parts, (unsigned)(64 * waves), lds, "type=%d ct=%d rt=%d u=%d", XT, CT, RT, U);
   auto* k = a.K % 128 == 0 ? k_mx4_gemv<XT, CT, RT, U, true> : k_mx4_gemv<XT, CT, RT, U, false>;
   hipLaunchKernelGGL(k, dim3(grid, parts), dim3(64 * waves), lds, a.stream, a.codes, a.scales, a.x, a.y, (int)a.N, (int)a.K,
@@ -301,9 +310,14 @@ int gemv_cfg(const Mx4GemvArgs& a) {
 // workgroup takes them all, and two row tiles where that leaves a workgroup per
 // compute unit (19456 x 2560 at 48 bf16 columns: 21.6 us against 27.2 with one
 // tile and 41 with 16 columns each; 8192 x 4096 at 32: 9.8 against 12.9; 2560 x
-// 9728 at 48: 17.8 against 14.9). Nine to 16 columns of rows that are not short
-// take two tiles from 384 tiles on (6144 x 2560 at 16 bf16 columns: 4.7 us
-// against 6.5, 19456 x 2560 12.5 against 15.5; 12000 x 1024 4.7 against 4.3).
+// 9728 at 48: 17.8 against 14.9; the rule's edge is late: 6144 x 2560 at 32, 48 and
+// 64 7.1, 8.0 and 9.8 with two, 10.4, 11.2 and 15.6 with one). Nine to 16 columns
+// take two tiles from 384 tiles on, unless a compute unit's LDS holds two
+// workgroups of one (6144 x 2560 at 16 bf16 columns: 4.7 us against 6.5, 19456 x
+// 2560 12.5 against 15.5; but 19456 x 2048 at nine, where it does, 11.0 against
+// 9.6, fp16 12.8 against 10.0, and 12288 x 1024 at 16 4.7 against 4.6). That is
+// less sure where the tiles fill the compute units just past a whole number of
+// times: 12288 x 4096 at nine fp16 columns 13.3 against 12.4.
 // Where the row tiles are few, groups of columns go to workgroups of their own
 // as far as the compute units take them at once (1000 x 14080 at 64 fp16
 // columns: 13.4 us against 31.5).
@@ -317,7 +331,11 @@ template <int XT>
 int gemv_half(const Mx4GemvArgs& a) {
   const int64_t tiles = (a.N + 15) / 16, parts = (a.M + 15) / 16;
   if (a.M <= 8) return gemv_cfg<XT, 1, 1, 4>(a);
-  if (a.M <= 16 && tiles >= 384 && a.K >= 2048) return gemv_cfg<XT, 1, 2, 2>(a);
+  if (a.M <= 16 && tiles >= 384) {
+    int one;   // LDS of a workgroup of one tile
+    gemv_waves<XT, 1, 1, 2>(a, &one);
+    if (2 * one > LDS_BYTES) return gemv_cfg<XT, 1, 2, 2>(a);
+  }
   if (a.M <= 16 || tiles * parts <= 256) return gemv_cfg<XT, 1, 1, 2>(a);
   if (a.M <= 32 || tiles * ((parts + 1) / 2) <= 256) return gemv_wide<XT, 2>(a);
   return a.M <= 48 ? gemv_wide<XT, 3>(a) : gemv_wide<XT, 4>(a);

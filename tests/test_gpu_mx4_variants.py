@@ -34,8 +34,9 @@ def launches(capfd, call):
 
 GEMV = [  # N, K, M, types, column tiles, row tiles, chunks
     (100, 160, 8, ("f16", "bf16"), 1, 1, 4), (100, 256, 1, ("f16", "bf16"), 1, 1, 4),
-    (6129, 2080, 9, ("f16", "bf16"), 1, 2, 2), (6144, 2048, 16, ("f16", "bf16"), 1, 2, 2),
-    (6128, 2048, 16, ("f16", "bf16"), 1, 1, 2), (6144, 2016, 9, ("f16", "bf16"), 1, 1, 2),
+    (6129, 2400, 9, ("f16", "bf16"), 1, 2, 2), (6144, 2048, 16, ("f16", "bf16"), 1, 2, 2),
+    (6144, 2048, 13, ("f16", "bf16"), 1, 2, 2), (6144, 2048, 12, ("f16", "bf16"), 1, 1, 2),   # two workgroups of one tile fit
+    (6128, 2048, 16, ("f16", "bf16"), 1, 1, 2), (6144, 2016, 9, ("f16", "bf16"), 1, 1, 2), (19456, 2048, 9, ("f16", "bf16"), 1, 1, 2),
     (1000, 160, 64, ("f16", "bf16"), 1, 1, 2),
     (1801, 160, 32, ("f16", "bf16"), 1, 1, 2), (2064, 160, 32, ("f16", "bf16"), 2, 1, 1), (1500, 256, 49, ("f16", "bf16"), 2, 1, 1),
     (8192, 160, 17, ("f16", "bf16"), 2, 2, 1), (8200, 128, 32, ("f16", "bf16"), 2, 2, 1),
