@@ -168,9 +168,11 @@ __device__ __forceinline__ void store_sums(const v4f (&acc)[RT][CT], v4f* red, i
 // are added in wave order. Grid y: groups of 16 CT columns. Dynamic LDS: waves *
 // (the columns' and the weights' regions), then (CT 1) or in their place (CT >
 // 1) waves * RT * CT KiB of partial sums. One column is bound by memory and the
-// launch (19456 x 2560, bf16: 26.5 MB in 6.8 us, 3.9 TB/s); many columns by what
-// each workgroup brings through LDS, a byte of it written and read once at 64
-// bytes a clock (2560 x 9728 at 48: 15 us).
+// launch (19456 x 2560, bf16: 26.5 MB in 6.9 us, 7.3 where none of it is in the last
+// cache; a kernel that only reads it takes 5.3); many columns by what each
+// workgroup brings through LDS, a byte of it written and read once at 64 bytes a
+// clock (2560 x 9728 at 48: 15 us, 33000 clocks, of which reads and writes take
+// 16000 each).
 template <int XT, int CT, int RT, int U, bool AL>
 __global__ __launch_bounds__(1024) void k_mx4_gemv(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                                                    const void* __restrict__ x, float* __restrict__ y, int N, int K,

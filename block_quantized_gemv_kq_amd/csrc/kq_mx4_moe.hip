@@ -261,10 +261,13 @@ __device__ __forceinline__ void split3_one(float v, uint16_t& hi, uint16_t& mid,
 // one writing ids and weights, which saves a launch between two others.
 // The waves split K; each stages its part of the tokens once and walks TILES
 // tiles of 16 gate and 16 up rows. The partial sums meet in LDS in wave order,
-// where the regions were. Bound by memory: 16 tokens of 128 experts of 768 x
-// 2048, top 8, read 137 MB of weights of some 82 experts in 31 us, 4.4 TB/s; one
-// token 13.4 MB in 8.7 us, most of it the latency of the choice, the copies and
-// the launch.
+// where the regions were. 16 tokens of 128 experts of 768 x 2048, top 8, read 137
+// MB of weights of some 82 experts in 31 us, 4.4 TB/s, where a kernel that only
+// reads them takes 22: a wave's region is filled, waited for and then multiplied,
+// with the other waves' copies in flight meanwhile. One token takes 8.7 us for
+// 13.4 MB, most of it the latency of the choice, the copies and the launch. An
+// expert's weights come again for each pass of its slots: 64 tokens of 16
+// experts of 1536 x 4096, top 4, are far from their bytes (layer 153 us, 26).
 // Dynamic LDS: waves * PER_WAVE, then ids and list (P uint16 each).
 template <int XT, int TILES, int COLS>   // COLS: columns in a pass
 struct GateUp {
@@ -379,9 +382,10 @@ __global__ __launch_bounds__((GateUp<XT, TILES, COLS>::MAX_WAVES * 64)) void k_m
 // of its own in LDS, and the waves' sums are added in wave order, so the result
 // does not depend on timing. With more than one workgroup for the rows, out is
 // theirs in turn and k_mx4_down_sum adds them. The operand columns are the
-// three pieces of h of a group's slots. Bound by memory and, at one token, by
-// latency: 16 tokens of 128 experts of 768 to 2048, top 8, 22.5 us and 4.8 for
-// the sum of the parts (68 MB of weights, 3.0 TB/s), one token 5.7.
+// three pieces of h of a group's slots. Bound by a wave's own copies, which it
+// waits for with nothing else in flight, three times per group at 768 inputs: 16
+// tokens of 128 experts of 768 to 2048, top 8, 22.4 us and 4.8 for the sum of the
+// parts (68 MB of weights, 3.0 TB/s; reading them alone takes 11.8), one token 5.7.
 // Dynamic LDS: per wave a region, then per wave M x 16 sums, then the route
 // weights (P fp32), groups (P int32) and ids (P uint16).
 template <int U, int SLOTS, bool AL>
@@ -603,8 +607,11 @@ int gate_up_x(const Mx4MoeArgs& a, uint16_t* h, int32_t* groups) {
 // Workgroups that share the down projection's rows: with many slots, or few
 // rows, one workgroup per 16 rows leaves compute units idle (and each reads all
 // of h). Two per compute unit, four slots and more each; the sum of the parts
-// costs a launch of 4.8 us (16 tokens, top 8, 2048 rows: layer 72.5 us with one,
-// 66.3 with four; 4 tokens gain 1.5 us from parts, less than that launch).
+// costs a launch of 4.8 us. Layers of 128 experts with 768 inner values, top 8, in
+// us with one part, two, four and eight: 2048 rows, 4 tokens 30.9, 31.5, 30.0,
+// 31.4; 8 tokens 48.5, 47.7, 43.0, 46.4; 16 tokens 68.9, 68.6, 61.8, 65.1; 1024
+// rows, 4 tokens 26.1, 25.9, 24.0, 25.4; 16 tokens 55.8, 52.5, 43.8, 40.6; 4096
+// rows, 16 tokens 118, 121, 124, 130 (the rule's two cost 2 % there).
 int down_parts(int64_t hidden, int P) {
   if (P < 64 && hidden > 1024) return 1;
   const int64_t fill = 512 / (hidden / 16), most = P / 4;
