@@ -154,3 +154,43 @@ def test_layer(kind, M, E, H, inter, top_k, which):
     ref, bound = X.moe_layer(X.widen(x), *L.host, ids, wts.astype(np.float64))
     err = np.abs(y - ref)
     assert (err <= bound).all(), (kind, (err / bound).max())
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("N,K,M", [(37, 13056, 33), (20, 16416, 1), (50, 9728, 64), (33, 20000, 9)])
+def test_gemv_long_rows(kind, N, K, M):
+    """Rows that a wave walks in several steps, the large scales in some of them."""
+    rng = np.random.default_rng((N, K, M, 14))
+    codes, scales = ends_planes(rng, N, K, np.array([100, 127, 128], np.uint8))
+    scales[::2, K // 64] = 254
+    scales[1::3, K // 32 - 1] = 253
+    pc, ps = upload(codes, scales)
+    x = rng.standard_normal((M, K))
+    x[:, K // 64 * 32:K // 64 * 32 + 32] *= 2.0 ** -14
+    x[:, -32:] *= 2.0 ** -13
+    xt = as_type(x, kind)
+    y = U.empty_dev((M, N))
+    kq.kq_mx4_gemv(pc.ptr, ps.ptr, kind, dev(xt), y, N, K, M)
+    check(U.to_host(y), *X.product(X.values(codes, scales), X.widen(xt)), K, what=f"{kind} M={M}")
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("M,E,H,inter,top_k", [(3, 5, 8352, 64, 3), (20, 3, 16384, 32, 1), (1, 3, 12320, 32, 2), (6, 4, 96, 8224, 2)])
+def test_layer_long_rows(kind, M, E, H, inter, top_k):
+    """The same in the layer: up rows with a block at 2^126 or 2^127, down rows with a large scale on codes of zero."""
+    rng = np.random.default_rng((M, E, H, 15))
+    L = Layer(rng, E, H, inter)
+    # up rows about 2^-86, a block of some at 2^126 or 2^127: u up to about 2^120, h to 2^107; down weights about 2^-79
+    c, s = ends_planes(rng, E * inter, H, np.array([40, 41], np.uint8))
+    s[::5, H // 64], s[2::5, H // 32 - 1] = 254, 253
+    L.host[1], L.planes[2:4] = X.values(c, s).reshape(E, inter, H), [Plane(p) for p in X.planes(c, s)]
+    c, s = ends_planes(rng, E * H, inter, np.array([47, 48, 49], np.uint8))
+    s[::7, inter // 64] = 200   # met by the down projection's waves, on weights of zero
+    c[::7, inter // 64 * 32:inter // 64 * 32 + 32] = 0
+    L.host[2], L.planes[4:6] = X.values(c, s).reshape(E, H, inter), [Plane(p) for p in X.planes(c, s)]
+    x = as_type(np.clip(rng.standard_normal((M, H)), -3, 3) * 2.0 ** -14, kind)
+    W = as_type(rng.standard_normal((E, H)), kind)
+    y, ids, wts = L.run(x, kind, W, kind, top_k, True)
+    assert np.isfinite(y).all()
+    ref, bound = X.moe_layer(X.widen(x), *L.host, ids, wts.astype(np.float64))
+    assert (np.abs(y - ref) <= bound).all()
