@@ -30,9 +30,21 @@ KQ_MAX_N = 0x7FFFFFFF   # output rows per call
 KQ_MX4_MAX_ROWS = 1 << 25
 KQ_MOE_MAX_EXPERTS = 1024
 KQ_MOE_MAX_DIM = 65536
+KQ_KV_PAGE = 32          # positions per page of a key-value cache
+KQ_MAX_HEAD_DIM = 256
+KQ_MAX_HEADS = 1024
+KQ_MAX_TOKENS = 1 << 20
+KQ_MAX_SEQS = 4096
+KQ_MAX_WINDOW = 1 << 30
+KQ_ROPE_HALF, KQ_ROPE_INTERLEAVED = 0, 1
+KQ_ROPE_NONE, KQ_ROPE_LINEAR, KQ_ROPE_NTK, KQ_ROPE_YARN = 0, 1, 2, 3
+ROPE_SCALINGS = {"none": KQ_ROPE_NONE, "linear": KQ_ROPE_LINEAR, "ntk": KQ_ROPE_NTK, "yarn": KQ_ROPE_YARN}
+KQ_KV_F16, KQ_KV_BF16, KQ_KV_Q8_0 = 1, 2, 8
+KV_TYPES = {"f16": KQ_KV_F16, "bf16": KQ_KV_BF16, "q8_0": KQ_KV_Q8_0}
 
 # Every symbol include/kq.h declares, with (restype, argtypes).
 _I64, _I32, _P = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p
+_F32, _F64 = ctypes.c_float, ctypes.c_double
 SIGNATURES = {
     "kq_version": (_I32, []),
     "kq_status_string": (ctypes.c_char_p, [_I32]),
@@ -65,6 +77,15 @@ SIGNATURES = {
     "kq_mx4_moe_layer_workspace_bytes": (_I64, [_I64, _I64, _I32, _I32, _I32]),
     "kq_mx4_moe_layer": (_I32, [_I32, _P, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I32, _I32, _I32,
                                 _I32, _P, _I64, _P]),
+    "kq_rope_freqs": (_I32, [_I32, _I32, _F64, _F64, _I64, _F64, _F64, _P, _P]),
+    "kq_rope": (_I32, [_P, _I32, _P, _I64, _I32, _P, _I64, _I32, _I32, _I32, _P]),
+    "kq_kv_page_bytes": (_I64, [_I32, _I32, _I32]),
+    "kq_kv_append": (_I32, [_P, _P, _P, _I32, _P, _I64, _P, _I64, _P, _I64, _I32, _P, _I64, _I32, _P]),
+    "kq_kv_read": (_I32, [_P, _P, _I32, _P, _I64, _P, _I64, _P]),
+    "kq_attn_decode_workspace_bytes": (_I64, [_P, _P, _I32]),
+    "kq_attn_prompt_workspace_bytes": (_I64, [_P, _P, _I32]),
+    "kq_attn_decode": (_I32, [_I32, _P, _I64, _P, _P, _P, _I64, _I32, _F32, _I32, _P, _P, _I64, _P]),
+    "kq_attn_prompt": (_I32, [_I32, _P, _I64, _P, _P, _P, _I64, _I32, _F32, _I32, _P, _I64, _P]),
     "kq_argmax_workspace_bytes": (_I64, [_I64, _I32]),
     "kq_argmax": (_I32, [_P, _I64, _I32, _P, _P, _I64, _P]),
     "kq_f32_to_f16": (_I32, [_P, _P, _I64]),
@@ -86,6 +107,39 @@ class kq_stage(ctypes.Structure):
 class kq_stack_info(ctypes.Structure):
     _fields_ = [("n_stages", ctypes.c_int32), ("fmt_mask", ctypes.c_int32), ("k_max", ctypes.c_int32),
                 ("workgroups", ctypes.c_int32)]
+
+
+class kq_rope_spec(ctypes.Structure):
+    """Mirror of the C struct kq_rope_spec: freqs float64 [rot_dim / 2] and
+    positions int32 [tokens] (or None, kq_kv_append only), device."""
+    _fields_ = [("freqs", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("mscale", ctypes.c_double),
+                ("rot_dim", ctypes.c_int32), ("pairs", ctypes.c_int32)]
+
+    def __init__(self, freqs, rot_dim: int, pairs: int = KQ_ROPE_HALF, mscale: float = 1.0, positions=None):
+        super().__init__(_ptr(freqs), _ptr(positions), mscale, rot_dim, pairs)
+        self._buffers = (freqs, positions)
+
+
+class kq_kv_cache(ctypes.Structure):
+    """Mirror of the C struct kq_kv_cache: k and v are device buffers of
+    n_pages * kq_kv_page_bytes(type, kv_heads, head_dim) bytes each."""
+    _fields_ = [("type", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("n_pages", ctypes.c_int64), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p)]
+
+    def __init__(self, type, k, v, n_pages: int, kv_heads: int, head_dim: int):
+        super().__init__(_kv_type(type), kv_heads, head_dim, 0, n_pages, _ptr(k), _ptr(v))
+        self._buffers = (k, v)
+
+
+class kq_kv_batch(ctypes.Structure):
+    """Mirror of the C struct kq_kv_batch: page_table int32 [n_seqs][table_width],
+    q_start int32 [n_seqs + 1] and lens int32 [n_seqs], device."""
+    _fields_ = [("page_table", ctypes.c_void_p), ("table_width", ctypes.c_int64), ("q_start", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("n_seqs", ctypes.c_int32), ("n_tokens", ctypes.c_int32)]
+
+    def __init__(self, page_table, table_width: int, q_start, lens, n_seqs: int, n_tokens: int):
+        super().__init__(_ptr(page_table), table_width, _ptr(q_start), _ptr(lens), n_seqs, n_tokens)
+        self._buffers = (page_table, q_start, lens)
 
 
 class KQError(RuntimeError):
@@ -143,6 +197,17 @@ def _type(t) -> int:
     if isinstance(t, str):
         return TYPES[t]
     return int(t)
+
+
+def _kv_type(t) -> int:
+    if isinstance(t, str):
+        return KV_TYPES[t]
+    return int(t)
+
+
+def _struct(s) -> int | None:
+    """Address of a struct, or None."""
+    return None if s is None else ctypes.addressof(s)
 
 
 def _ptr(t) -> int | None:
@@ -355,6 +420,64 @@ def kq_mx4_moe_layer(xtype, x, wtype, router, gate_codes, gate_scales, up_codes,
                                   _ptr(down_scales), _ptr(y), _ptr(ids), _ptr(weights), hidden, inter, M, top_k,
                                   n_experts, int(renorm), _ptr(workspace), workspace_bytes, _stream(stream)),
            "kq_mx4_moe_layer")
+
+
+def kq_rope_freqs(scaling, rot_dim: int, base: float, factor: float = 1.0, original_length: int = 0,
+                  beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(freqs, mscale): float64 [rot_dim / 2] radians per position (host), and the factor on cos and sin."""
+    freqs, mscale = np.empty(max(rot_dim // 2, 1), np.float64), ctypes.c_double(0.0)
+    scaling = ROPE_SCALINGS[scaling] if isinstance(scaling, str) else int(scaling)
+    _check(lib().kq_rope_freqs(scaling, rot_dim, base, factor, original_length, beta_fast, beta_slow, freqs.ctypes.data,
+                               ctypes.addressof(mscale)), "kq_rope_freqs")
+    return freqs, mscale.value
+
+
+def kq_rope(rope: kq_rope_spec, xtype, x, ldx: int, otype, out, ldo: int, T: int, heads: int, head_dim: int,
+            stream=None) -> None:
+    """out[t] = x[t] with every head rotated by positions[t]; rows of heads * head_dim elements, ldx and ldo apart."""
+    _check(lib().kq_rope(_struct(rope), _type(xtype), _ptr(x), ldx, _type(otype), _ptr(out), ldo, T, heads, head_dim,
+                         _stream(stream)), "kq_rope")
+
+
+def kq_kv_page_bytes(type, kv_heads: int, head_dim: int) -> int:
+    return _check(lib().kq_kv_page_bytes(_kv_type(type), kv_heads, head_dim), "kq_kv_page_bytes")
+
+
+def kq_kv_append(cache: kq_kv_cache, batch: kq_kv_batch, rope: kq_rope_spec | None, xtype, k, ldk: int, v, ldv: int,
+                 q=None, ldq: int = 0, otype=KQ_F16, q_out=None, ldo: int = 0, heads: int = 0, stream=None) -> None:
+    """The new tokens' k (rotated) and v into their pages; q rotated into q_out where it is given."""
+    _check(lib().kq_kv_append(_struct(cache), _struct(batch), _struct(rope), _type(xtype), _ptr(k), ldk, _ptr(v), ldv,
+                              _ptr(q), ldq, _type(otype), _ptr(q_out), ldo, heads, _stream(stream)), "kq_kv_append")
+
+
+def kq_kv_read(cache: kq_kv_cache, batch: kq_kv_batch, otype, k, ldk: int, v, ldv: int, stream=None) -> None:
+    """The k and v rows of the batch's tokens as the cache holds them."""
+    _check(lib().kq_kv_read(_struct(cache), _struct(batch), _type(otype), _ptr(k), ldk, _ptr(v), ldv, _stream(stream)),
+           "kq_kv_read")
+
+
+def kq_attn_decode_workspace_bytes(cache: kq_kv_cache, batch: kq_kv_batch, heads: int) -> int:
+    return _check(lib().kq_attn_decode_workspace_bytes(_struct(cache), _struct(batch), heads),
+                  "kq_attn_decode_workspace_bytes")
+
+
+def kq_attn_prompt_workspace_bytes(cache: kq_kv_cache, batch: kq_kv_batch, heads: int) -> int:
+    return _check(lib().kq_attn_prompt_workspace_bytes(_struct(cache), _struct(batch), heads),
+                  "kq_attn_prompt_workspace_bytes")
+
+
+def kq_attn_decode(type, q, ldq: int, cache: kq_kv_cache, batch: kq_kv_batch, out, ldo: int, heads: int, scale: float,
+                   window: int = 0, tree=None, workspace=None, workspace_bytes: int = 0, stream=None) -> None:
+    """out = attention of a few new tokens per sequence over the paged cache (tree: int64/uint64 bit masks per row)."""
+    _check(lib().kq_attn_decode(_type(type), _ptr(q), ldq, _struct(cache), _struct(batch), _ptr(out), ldo, heads, scale,
+                                window, _ptr(tree), _ptr(workspace), workspace_bytes, _stream(stream)), "kq_attn_decode")
+
+
+def kq_attn_prompt(type, q, ldq: int, cache: kq_kv_cache, batch: kq_kv_batch, out, ldo: int, heads: int, scale: float,
+                   window: int = 0, workspace=None, workspace_bytes: int = 0, stream=None) -> None:
+    """out = causal attention of packed prompts (or the next parts of prompts) over the paged cache."""
+    _check(lib().kq_attn_prompt(_type(type), _ptr(q), ldq, _struct(cache), _struct(batch), _ptr(out), ldo, heads, scale,
+                                window, _ptr(workspace), workspace_bytes, _stream(stream)), "kq_attn_prompt")
 
 
 def kq_shortlist_copy_bytes(N: int, K: int) -> int:

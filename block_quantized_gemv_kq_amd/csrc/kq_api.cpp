@@ -1,5 +1,6 @@
 // kq_api.cpp — the C ABI: argument checks (all on the host, before any HIP
 // call), thread-local error messages, and dispatch to the kernel launchers.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <stdlib.h>
@@ -873,6 +874,240 @@ int kq_mx4_moe_layer(int xtype, const void* x, int wtype, const void* router, co
   a.y = y;
   a.inter = inter;
   return hip_status(kq::launch_mx4_moe(a), "kq_mx4_moe_layer");
+}
+
+// ---- rotary positions, the paged key-value cache, attention
+
+namespace {
+
+int check_head_dim(int64_t D) {
+  if (D <= 0 || D % 32 != 0 || D > KQ_MAX_HEAD_DIM)
+    return fail(KQ_ERR_SHAPE, "head_dim=%lld must be a positive multiple of 32 and <= %d", (long long)D, KQ_MAX_HEAD_DIM);
+  return KQ_OK;
+}
+
+int check_heads(const char* who, const char* what, int64_t heads) {
+  if (heads < 1 || heads > KQ_MAX_HEADS)
+    return fail(KQ_ERR_ARG, "%s: %s=%lld must be in [1, %d]", who, what, (long long)heads, KQ_MAX_HEADS);
+  return KQ_OK;
+}
+
+// Rows of `width` elements `ld` apart.
+int check_rows(const char* who, const char* what, const void* p, int type, int64_t ld, int64_t width) {
+  if (!p) return fail(KQ_ERR_ARG, "%s: %s is null", who, what);
+  if (ld < width || ld > (int64_t)1 << 35)
+    return fail(KQ_ERR_ARG, "%s: row stride %lld of %s must be in [%lld, 2^35]", who, (long long)ld, what, (long long)width);
+  if (!aligned(p, (uintptr_t)type_size(type))) return fail(KQ_ERR_ALIGN, "%s: %s must be aligned to its elements", who, what);
+  return KQ_OK;
+}
+
+int check_rope(const char* who, const kq_rope_spec* r, int head_dim) {
+  if (!r->freqs) return fail(KQ_ERR_ARG, "%s: freqs is null", who);
+  if (r->rot_dim < 2 || r->rot_dim % 2 != 0 || r->rot_dim > head_dim)
+    return fail(KQ_ERR_SHAPE, "%s: rot_dim=%d must be even and in [2, head_dim]", who, r->rot_dim);
+  if (r->pairs != KQ_ROPE_HALF && r->pairs != KQ_ROPE_INTERLEAVED) return fail(KQ_ERR_ARG, "%s: unknown pairs %d", who, r->pairs);
+  if (!isfinite(r->mscale)) return fail(KQ_ERR_ARG, "%s: mscale must be finite", who);
+  if (!aligned(r->freqs, 8) || !aligned(r->positions, 4))
+    return fail(KQ_ERR_ALIGN, "%s: freqs must be 8-byte and positions 4-byte aligned", who);
+  return KQ_OK;
+}
+
+int check_cache_shape(const char* who, int type, int64_t kv_heads, int64_t head_dim) {
+  if (type != KQ_KV_F16 && type != KQ_KV_BF16 && type != KQ_KV_Q8_0) return fail(KQ_ERR_ARG, "%s: unknown cache type %d", who, type);
+  const int st = check_heads(who, "kv_heads", kv_heads);
+  return st ? st : check_head_dim(head_dim);
+}
+
+// The sizes of a cache and a batch; *empty where there are no tokens or sequences.
+int check_kv_shape(const char* who, const kq_kv_cache* c, const kq_kv_batch* b, bool* empty) {
+  *empty = false;
+  if (!c || !b) return fail(KQ_ERR_ARG, "%s: null cache or batch", who);
+  int st = check_cache_shape(who, c->type, c->kv_heads, c->head_dim);
+  if (st) return st;
+  if (c->reserved != 0) return fail(KQ_ERR_ARG, "%s: reserved must be 0", who);
+  if (c->n_pages < 1 || c->n_pages > 0x7fffffff) return fail(KQ_ERR_ARG, "%s: n_pages=%lld out of range", who, (long long)c->n_pages);
+  if (b->n_seqs < 0 || b->n_seqs > KQ_MAX_SEQS) return fail(KQ_ERR_ARG, "%s: n_seqs=%d must be in [0, %d]", who, b->n_seqs, KQ_MAX_SEQS);
+  if (b->n_tokens < 0 || b->n_tokens > KQ_MAX_TOKENS)
+    return fail(KQ_ERR_ARG, "%s: n_tokens=%d must be in [0, %d]", who, b->n_tokens, KQ_MAX_TOKENS);
+  if (b->table_width < 1 || b->table_width >= 1 << 26)
+    return fail(KQ_ERR_ARG, "%s: table_width=%lld must be in [1, 2^26)", who, (long long)b->table_width);
+  *empty = b->n_seqs == 0 || b->n_tokens == 0;
+  return KQ_OK;
+}
+
+int check_kv_pointers(const char* who, const kq_kv_cache* c, const kq_kv_batch* b) {
+  if (!c->k || !c->v || !b->page_table || !b->q_start || !b->lens) return fail(KQ_ERR_ARG, "%s: null pointer in the cache or batch", who);
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(b->page_table, 4) || !aligned(b->q_start, 4) || !aligned(b->lens, 4))
+    return fail(KQ_ERR_ALIGN, "%s: k and v must be 16-byte, the batch's arrays 4-byte aligned", who);
+  return KQ_OK;
+}
+
+int check_attn_shape(const char* who, const kq_kv_cache* c, const kq_kv_batch* b, int heads, bool decode, bool* empty) {
+  int st = check_kv_shape(who, c, b, empty);
+  if (st) return st;
+  if ((st = check_heads(who, "heads", heads))) return st;
+  if (heads % c->kv_heads != 0) return fail(KQ_ERR_SHAPE, "%s: heads=%d must be a multiple of kv_heads=%d", who, heads, c->kv_heads);
+  if (decode && (b->n_tokens > KQ_MAX_M || b->n_seqs > KQ_MAX_M))
+    return fail(KQ_ERR_ARG, "%s: n_tokens=%d and n_seqs=%d must be at most %d", who, b->n_tokens, b->n_seqs, KQ_MAX_M);
+  return KQ_OK;
+}
+
+int check_attn(const char* who, const kq::AttnCall& a, int64_t need, int64_t given) {
+  const kq_kv_cache& c = *a.cache;
+  const int64_t width = (int64_t)a.heads * c.head_dim;
+  int st = check_kv_pointers(who, a.cache, a.batch);
+  if (st) return st;
+  if ((st = check_rows(who, "q", a.q, a.type, a.ldq, width))) return st;
+  if ((st = check_rows(who, "out", a.out, a.type, a.ldo, width))) return st;
+  if (!aligned(a.tree, 8)) return fail(KQ_ERR_ALIGN, "%s: tree must be 8-byte aligned", who);
+  if (need > 0 && (st = check_workspace(who, a.ws, given, need))) return st;
+  return KQ_OK;
+}
+
+int check_attn_values(const char* who, const kq::AttnCall& a) {
+  if (a.type != KQ_F16 && a.type != KQ_BF16) return fail(KQ_ERR_ARG, "%s: type must be KQ_F16 or KQ_BF16", who);
+  if (a.cache->type != KQ_KV_Q8_0 && a.cache->type != (a.type == KQ_F16 ? KQ_KV_F16 : KQ_KV_BF16))
+    return fail(KQ_ERR_ARG, "%s: the cache must hold the type of q, or Q8_0", who);
+  if (!(a.scale > 0.0f) || !isfinite(a.scale)) return fail(KQ_ERR_ARG, "%s: scale must be positive and finite", who);
+  if (a.window < 0 || a.window > KQ_MAX_WINDOW) return fail(KQ_ERR_ARG, "%s: window=%d must be in [0, 2^30]", who, a.window);
+  return KQ_OK;
+}
+
+}  // namespace
+
+int kq_rope_freqs(int scaling, int rot_dim, double base, double factor, int64_t original_length, double beta_fast,
+                  double beta_slow, double* freqs, double* mscale) {
+  if (rot_dim < 2 || rot_dim % 2 != 0 || rot_dim > KQ_MAX_HEAD_DIM)
+    return fail(KQ_ERR_SHAPE, "kq_rope_freqs: rot_dim=%d must be even and in [2, %d]", rot_dim, KQ_MAX_HEAD_DIM);
+  if (scaling < KQ_ROPE_NONE || scaling > KQ_ROPE_YARN) return fail(KQ_ERR_ARG, "kq_rope_freqs: unknown scaling %d", scaling);
+  if (!freqs || !mscale) return fail(KQ_ERR_ARG, "kq_rope_freqs: null pointer");
+  if (!(base > 0) || !isfinite(base) || !(factor > 0) || !isfinite(factor))
+    return fail(KQ_ERR_ARG, "kq_rope_freqs: base and factor must be positive and finite");
+  if (scaling == KQ_ROPE_YARN && (original_length <= 0 || !isfinite(beta_fast) || !isfinite(beta_slow) || !(beta_fast > beta_slow)))
+    return fail(KQ_ERR_ARG, "kq_rope_freqs: YARN needs original_length > 0 and beta_fast > beta_slow");
+  if (scaling == KQ_ROPE_NTK && rot_dim > 2) base *= pow(factor, (double)rot_dim / (rot_dim - 2));
+  *mscale = scaling == KQ_ROPE_YARN && factor > 1 ? 0.1 * log(factor) + 1 : 1.0;
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    const double f = pow(base, -2.0 * i / rot_dim);
+    freqs[i] = f;
+    if (scaling == KQ_ROPE_LINEAR) freqs[i] = f / factor;
+    if (scaling == KQ_ROPE_YARN) {
+      const double turns = (double)original_length * f / 6.283185307179586;
+      const double g = fmin(1.0, fmax(0.0, (turns - beta_slow) / (beta_fast - beta_slow)));
+      freqs[i] = g * f + (1 - g) * f / factor;
+    }
+  }
+  return ok();
+}
+
+int kq_rope(const kq_rope_spec* rope, int xtype, const void* x, int64_t ldx, int otype, void* out, int64_t ldo, int T,
+            int heads, int head_dim, void* stream) {
+  int st = check_head_dim(head_dim);
+  if (st) return st;
+  if ((st = check_heads("kq_rope", "heads", heads))) return st;
+  if (!valid_type(xtype) || !valid_type(otype)) return fail(KQ_ERR_ARG, "kq_rope: unknown type");
+  if (T < 0 || T > KQ_MAX_TOKENS) return fail(KQ_ERR_ARG, "kq_rope: T=%d must be in [0, %d]", T, KQ_MAX_TOKENS);
+  if (!rope) return fail(KQ_ERR_ARG, "kq_rope: rope is null");
+  if ((st = check_rope("kq_rope", rope, head_dim))) return st;
+  if (T == 0) return ok();
+  if (!rope->positions) return fail(KQ_ERR_ARG, "kq_rope: positions is null");
+  const int64_t width = (int64_t)heads * head_dim;
+  if ((st = check_rows("kq_rope", "x", x, xtype, ldx, width))) return st;
+  if ((st = check_rows("kq_rope", "out", out, otype, ldo, width))) return st;
+  if (x == out && (xtype != otype || ldx != ldo)) return fail(KQ_ERR_ARG, "kq_rope: in place needs one type and row stride");
+  return hip_status(kq::launch_rope(rope, xtype, x, ldx, otype, out, ldo, T, heads, head_dim, static_cast<hipStream_t>(stream)),
+                    "kq_rope");
+}
+
+int64_t kq_kv_page_bytes(int type, int kv_heads, int head_dim) {
+  const int st = check_cache_shape("kq_kv_page_bytes", type, kv_heads, head_dim);
+  if (st) return st;
+  return (int64_t)kv_heads * head_dim * (type == KQ_KV_Q8_0 ? 34 : 64);
+}
+
+int kq_kv_append(const kq_kv_cache* cache, const kq_kv_batch* batch, const kq_rope_spec* rope, int xtype, const void* k,
+                 int64_t ldk, const void* v, int64_t ldv, const void* q, int64_t ldq, int otype, void* q_out, int64_t ldo,
+                 int heads, void* stream) {
+  const char* who = "kq_kv_append";
+  bool empty;
+  int st = check_kv_shape(who, cache, batch, &empty);
+  if (st) return st;
+  if (!valid_type(xtype)) return fail(KQ_ERR_ARG, "%s: unknown type %d", who, xtype);
+  if (rope && (st = check_rope(who, rope, cache->head_dim))) return st;
+  if (q) {
+    if (!valid_type(otype)) return fail(KQ_ERR_ARG, "%s: unknown type %d", who, otype);
+    if ((st = check_heads(who, "heads", heads))) return st;
+  }
+  if (empty) return ok();
+  if ((st = check_kv_pointers(who, cache, batch))) return st;
+  const int64_t width = (int64_t)cache->kv_heads * cache->head_dim;
+  if ((st = check_rows(who, "k", k, xtype, ldk, width))) return st;
+  if ((st = check_rows(who, "v", v, xtype, ldv, width))) return st;
+  if (q) {
+    if ((st = check_rows(who, "q", q, xtype, ldq, (int64_t)heads * cache->head_dim))) return st;
+    if ((st = check_rows(who, "q_out", q_out, otype, ldo, (int64_t)heads * cache->head_dim))) return st;
+    if (q == q_out && (xtype != otype || ldq != ldo)) return fail(KQ_ERR_ARG, "%s: in place needs one type and row stride", who);
+  }
+  const kq::KvAppendArgs a{cache, batch, rope, xtype, k, ldk, v, ldv, q, ldq, otype, q_out, ldo, heads, static_cast<hipStream_t>(stream)};
+  return hip_status(kq::launch_kv_append(a), who);
+}
+
+int kq_kv_read(const kq_kv_cache* cache, const kq_kv_batch* batch, int otype, void* k, int64_t ldk, void* v, int64_t ldv,
+               void* stream) {
+  const char* who = "kq_kv_read";
+  bool empty;
+  int st = check_kv_shape(who, cache, batch, &empty);
+  if (st) return st;
+  if (!valid_type(otype)) return fail(KQ_ERR_ARG, "%s: unknown type %d", who, otype);
+  if (empty) return ok();
+  if ((st = check_kv_pointers(who, cache, batch))) return st;
+  const int64_t width = (int64_t)cache->kv_heads * cache->head_dim;
+  if ((st = check_rows(who, "k", k, otype, ldk, width))) return st;
+  if ((st = check_rows(who, "v", v, otype, ldv, width))) return st;
+  return hip_status(kq::launch_kv_read(*cache, *batch, otype, k, ldk, v, ldv, static_cast<hipStream_t>(stream)), who);
+}
+
+int64_t kq_attn_decode_workspace_bytes(const kq_kv_cache* cache, const kq_kv_batch* batch, int heads) {
+  bool empty;
+  const int st = check_attn_shape("kq_attn_decode_workspace_bytes", cache, batch, heads, true, &empty);
+  if (st) return st;
+  return empty ? 0 : kq::decode_plan(*cache, *batch, heads).bytes;
+}
+
+int64_t kq_attn_prompt_workspace_bytes(const kq_kv_cache* cache, const kq_kv_batch* batch, int heads) {
+  bool empty;
+  const int st = check_attn_shape("kq_attn_prompt_workspace_bytes", cache, batch, heads, false, &empty);
+  if (st) return st;
+  return empty ? 0 : kq::prompt_plan(*cache, *batch, heads).bytes;
+}
+
+int kq_attn_decode(int type, const void* q, int64_t ldq, const kq_kv_cache* cache, const kq_kv_batch* batch, void* out,
+                   int64_t ldo, int heads, float scale, int window, const uint64_t* tree, void* workspace,
+                   int64_t workspace_bytes, void* stream) {
+  const char* who = "kq_attn_decode";
+  bool empty;
+  int st = check_attn_shape(who, cache, batch, heads, true, &empty);
+  if (st) return st;
+  const kq::AttnCall a{type, q, ldq, cache, batch, out, ldo, heads, scale, window, tree, workspace, static_cast<hipStream_t>(stream)};
+  if ((st = check_attn_values(who, a))) return st;
+  if (empty) return ok();
+  if ((st = check_attn(who, a, kq::decode_plan(*cache, *batch, heads).bytes, workspace_bytes))) return st;
+  return hip_status(kq::launch_attn_decode(a), who);
+}
+
+int kq_attn_prompt(int type, const void* q, int64_t ldq, const kq_kv_cache* cache, const kq_kv_batch* batch, void* out,
+                   int64_t ldo, int heads, float scale, int window, void* workspace, int64_t workspace_bytes, void* stream) {
+  const char* who = "kq_attn_prompt";
+  bool empty;
+  int st = check_attn_shape(who, cache, batch, heads, false, &empty);
+  if (st) return st;
+  const kq::AttnCall a{type, q, ldq, cache, batch, out, ldo, heads, scale, window, nullptr, workspace, static_cast<hipStream_t>(stream)};
+  if ((st = check_attn_values(who, a))) return st;
+  if (empty) return ok();
+  const kq::AttnPlan plan = kq::prompt_plan(*cache, *batch, heads);
+  if (plan.grid > 0x7fffff) return fail(KQ_ERR_ARG, "%s: %lld tiles are beyond the grid", who, (long long)plan.grid);
+  if ((st = check_attn(who, a, plan.bytes, workspace_bytes))) return st;
+  return hip_status(kq::launch_attn_prompt(a), who);
 }
 
 }  // extern "C"

@@ -1,0 +1,429 @@
+// kq_attn.hip — attention of a few new tokens per sequence over the paged
+// cache (decode and verify passes), and the join of partial results.
+//
+// A wave takes a page (32 keys) at a time, straight from memory to registers:
+// S^T = K Q^T on matrix instructions, 16 keys by 16 columns (the queries of one
+// key-value head, token by token); the scores of a lane are 8 consecutive keys
+// of one column, which is the operand of O^T += V^T P^T as it stands.
+// Every byte of K and V is read once per column tile.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kq_attn_dev.h"
+
+namespace kqd {
+
+constexpr int DEC_WAVES = 4;
+
+// Column tiles of 16 that a workgroup's waves carry.
+template <bool Q8, int DB>
+struct Page {
+  u32x4 k[Q8 ? DB : 2 * DB];
+  u32x4 v[Q8 ? DB : 2 * DB];
+  u32x4 ks[Q8 ? DB : 1];   // scales of the lane's 8 keys, per block of 32 channels
+  u32x4 vs[Q8 ? DB : 1];
+};
+
+template <bool Q8, int DB>
+__device__ __forceinline__ void load_page(Page<Q8, DB>& p, const Cache& c, int32_t id, int head) {
+  const int lane = threadIdx.x & 63;
+  const int64_t at = ((int64_t)(id < 0 ? 0 : id) * c.kv_heads + head) * region_bytes(Q8, 32 * DB);
+  const u32x4* k = reinterpret_cast<const u32x4*>(c.k + at);
+  const u32x4* v = reinterpret_cast<const u32x4*>(c.v + at);
+  constexpr int N = Q8 ? DB : 2 * DB;
+#pragma unroll
+  for (int i = 0; i < N; ++i) p.k[i] = k[i * 64 + lane];
+  if constexpr (Q8) {
+#pragma unroll
+    for (int i = 0; i < DB; ++i) p.ks[i] = k[64 * DB + 4 * i + (lane >> 4)];
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) p.v[i] = v[i * 64 + lane];
+  if constexpr (Q8) {
+#pragma unroll
+    for (int i = 0; i < DB; ++i) p.vs[i] = v[64 * DB + 4 * i + (lane >> 4)];
+  }
+}
+
+template <int QT, bool Q8, int DB, int CT>
+__global__ __launch_bounds__(64 * DEC_WAVES) void k_attn_decode(AttnArgs a) {
+  constexpr int D = 32 * DB, DT = 2 * DB, VT = Q8 ? A_BF16 : QT;
+  // d-tiles per round of the sum over the waves: 64 KB of LDS
+  constexpr int ROUND = DT * CT * DEC_WAVES <= 64 ? DT : 64 / (CT * DEC_WAVES);
+  __shared__ v4f sum[DEC_WAVES * ROUND * CT * 64];
+  __shared__ float s_m[DEC_WAVES][CT * 16], s_l[DEC_WAVES][CT * 16];
+
+  const Part p = part_of(a.b, a.w, blockIdx.x);
+  if (p.s < 0) return;
+  const int lane = threadIdx.x & 63, wave = wave_id(), r = lane & 15, g = lane >> 4;
+  const int G = a.w.G, cols = p.seq.n * G, col0 = p.tile * (16 * CT);
+
+  // this lane's columns: token, position, what of the newest tokens it sees
+  u32x4 qf[CT][DB];
+  int at[CT];            // position, or -1: no column
+  uint64_t tree[CT];
+  const bool qwide = wide_rows(a.q, a.ldq);
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    const int col = col0 + 16 * ct + r;
+    const bool have = col < cols;
+    const int i = have ? col / G : 0, h = p.head * G + (have ? col - i * G : 0);
+    at[ct] = have ? p.seq.len - p.seq.n + i : -1;
+    tree[ct] = a.tree != nullptr && have ? a.tree[p.seq.begin + i] : ~0ull;
+    const uint16_t* q = a.q + (int64_t)(p.seq.begin + i) * a.ldq + (int64_t)h * D + 8 * g;
+#pragma unroll
+    for (int c = 0; c < DB; ++c) {
+      qf[ct][c] = row_piece(q + 32 * c, qwide);
+      if (!have) qf[ct][c] = u32x4{0u, 0u, 0u, 0u};
+    }
+  }
+  // a page that every column sees whole needs no mask
+  const int newest = p.seq.len - p.seq.n;   // position of the first new token
+  const int whole_to = a.tree != nullptr ? newest : newest + 1;   // keys below are seen by every query
+  const int whole_from = a.w.window > 0 ? p.seq.len - a.w.window : 0;
+
+  v4f o[CT][DT];
+  float m[CT], l[CT];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    m[ct] = -__builtin_inff();
+    l[ct] = 0.0f;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) o[ct][dt] = v4f{0.f, 0.f, 0.f, 0.f};
+  }
+
+  // the chunk's pages, one in DEC_WAVES for this wave
+  const int base = p.np / p.chunks, rest = p.np % p.chunks;
+  const int p0 = p.first + p.chunk * base + min(p.chunk, rest);
+  const int p1 = p0 + base + (p.chunk < rest ? 1 : 0);
+  const int steps = (p1 - p0 - wave + DEC_WAVES - 1) / DEC_WAVES;
+
+  const auto step = [&](const Page<Q8, DB>& pg, int32_t id, int page) {
+    const int key0 = page * PAGE + 8 * g;    // this lane's keys: key0 + j
+    const bool masked = page * PAGE + PAGE > whole_to || page * PAGE < whole_from || id < 0;
+    u32x4 ph[CT][Q8 ? DB : 1], pl[CT][Q8 ? DB : 1], seen1[CT];
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      float t[8];
+      v4f s[2] = {v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int c = 0; c < DB; ++c) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if constexpr (Q8) {
+            const u32x4 kf = codes16<QT>(pg.k[c][2 * h], pg.k[c][2 * h + 1]);
+            const v4f d = mfma16<QT>(kf, qf[ct][c], v4f{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t w = pg.ks[c][2 * h + i / 2];
+              s[h][i] = __builtin_fmaf(h2f(i & 1 ? w >> 16 : w), d[i], s[h][i]);
+            }
+          } else {
+            s[h] = mfma16<QT>(pg.k[2 * c + h], qf[ct][c], s[h]);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[j] = s[j >> 2][j & 3] * a.scale;
+      uint32_t seen = 0xff;
+      if (masked) {
+        seen = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int key = key0 + j, among = key - newest;
+          bool ok = key <= at[ct] && (a.w.window <= 0 || key > at[ct] - a.w.window);
+          if (a.tree != nullptr && among >= 0) ok &= among < 64 && (tree[ct] >> (among & 63) & 1) != 0;
+          if (id == -2) ok = true;
+          seen |= (ok ? 1u : 0u) << j;
+          t[j] = !ok ? -__builtin_inff() : id < 0 ? __builtin_nanf("") : t[j];
+        }
+      }
+      float top = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
+      top = fmaxf(top, __shfl_xor(top, 16, 64));
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      if (__any(top > m[ct])) {
+        const float now = fmaxf(m[ct], top), by = m[ct] == now ? 1.0f : exp2_fast(m[ct] - now);
+        m[ct] = now;
+        l[ct] *= by;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) o[ct][dt] *= by;
+      }
+      const float sub = m[ct] == -__builtin_inff() ? 0.0f : m[ct];   // nothing seen yet: weights 0
+      float e[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        e[j] = exp2_fast(t[j] - sub);
+        l[ct] += e[j];
+      }
+      if constexpr (Q8) {
+        // the scale of V's block goes to the weight: the codes stay whole numbers
+#pragma unroll
+        for (int c = 0; c < DB; ++c)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t w = pg.vs[c][j];
+            const float e0 = seen >> (2 * j) & 1 ? e[2 * j] * h2f(w) : 0.0f;
+            const float e1 = seen >> (2 * j + 1) & 1 ? e[2 * j + 1] * h2f(w >> 16) : 0.0f;
+            uint32_t hi, lo;
+            split2<A_BF16>(e0, e1, hi, lo);
+            ph[ct][c][j] = hi;
+            pl[ct][c][j] = lo;
+          }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t hi, lo;
+          split2<VT>(e[2 * j], e[2 * j + 1], hi, lo);
+          ph[ct][0][j] = hi;
+          pl[ct][0][j] = lo;
+          const uint32_t one = VT == A_F16 ? 0x3c00u : 0x3f80u;
+          seen1[ct][j] = (seen >> (2 * j) & 1 ? one : 0u) | (seen >> (2 * j + 1) & 1 ? one << 16 : 0u);
+        }
+      }
+    }
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) {
+      if constexpr (Q8) {
+        const u32x4 vf = codes16<VT>(pg.v[dt / 2][2 * (dt & 1)], pg.v[dt / 2][2 * (dt & 1) + 1]);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          o[ct][dt] = mfma16<VT>(vf, ph[ct][dt / 2], o[ct][dt]);
+          o[ct][dt] = mfma16<VT>(vf, pl[ct][dt / 2], o[ct][dt]);
+        }
+      } else {
+        u32x4 vf = pg.v[dt];
+        if (__any(any_not_finite<VT>(vf))) {
+          // Infinities and NaN of V must not reach columns that do not see
+          // them (0 times them is NaN): the finite part is multiplied, and what
+          // a column sees of the rest is counted and added as it is.
+          u32x4 plus, minus;
+          vf = take_finite<VT>(vf, plus, minus);
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) {
+            const v4f up = mfma16<VT>(plus, seen1[ct], v4f{0.f, 0.f, 0.f, 0.f});
+            const v4f down = mfma16<VT>(minus, seen1[ct], v4f{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              o[ct][dt][i] += (up[i] > 0.0f ? __builtin_inff() : 0.0f) + (down[i] > 0.0f ? -__builtin_inff() : 0.0f);
+          }
+        }
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          o[ct][dt] = mfma16<VT>(vf, ph[ct][0], o[ct][dt]);
+          o[ct][dt] = mfma16<VT>(vf, pl[ct][0], o[ct][dt]);
+        }
+      }
+    }
+  };
+
+  if (steps > 0) {
+    Page<Q8, DB> now, next;
+    int32_t id = scalar(page_id(a.b, a.c.n_pages, p.s, p0 + wave));
+    load_page<Q8, DB>(now, a.c, id, p.head);
+    for (int i = 0; i < steps; ++i) {
+      const int page = p0 + wave + i * DEC_WAVES;
+      const int32_t id_next = i + 1 < steps ? scalar(page_id(a.b, a.c.n_pages, p.s, page + DEC_WAVES)) : 0;
+      if (i + 1 < steps) load_page<Q8, DB>(next, a.c, id_next, p.head);
+      step(now, id, page);
+      now = next;
+      id = id_next;
+    }
+  }
+
+  // join the waves
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    l[ct] += __shfl_xor(l[ct], 16, 64);
+    l[ct] += __shfl_xor(l[ct], 32, 64);
+    if (g == 0) {
+      s_m[wave][16 * ct + r] = m[ct];
+      s_l[wave][16 * ct + r] = l[ct];
+    }
+  }
+  __syncthreads();
+  float by[CT];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int w = 0; w < DEC_WAVES; ++w) top = fmaxf(top, s_m[w][16 * ct + r]);
+    by[ct] = m[ct] == -__builtin_inff() ? (l[ct] == 0.0f ? 0.0f : 1.0f) : exp2_fast(m[ct] - top);
+  }
+  const bool owide = wide_rows(a.out, a.ldo);
+#pragma unroll
+  for (int d0 = 0; d0 < DT; d0 += ROUND) {
+    if (d0 > 0) __syncthreads();
+#pragma unroll
+    for (int dt = d0; dt < d0 + ROUND && dt < DT; ++dt)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) sum[((wave * ROUND + dt - d0) * CT + ct) * 64 + lane] = o[ct][dt] * by[ct];
+    __syncthreads();
+    const int here = DT - d0 < ROUND ? DT - d0 : ROUND;
+    for (int i = wave; i < here * CT; i += DEC_WAVES) {
+      const int dt = d0 + i / CT, ct = i % CT;
+      v4f v = sum[i * 64 + lane];
+#pragma unroll
+      for (int w = 1; w < DEC_WAVES; ++w) v += sum[(w * ROUND * CT + i) * 64 + lane];
+      const int col = col0 + 16 * ct + r;
+      if (col >= cols) continue;
+      float top = -__builtin_inff(), total = 0.0f;
+#pragma unroll
+      for (int w = 0; w < DEC_WAVES; ++w) top = fmaxf(top, s_m[w][16 * ct + r]);
+#pragma unroll
+      for (int w = 0; w < DEC_WAVES; ++w) {
+        const float mw = s_m[w][16 * ct + r], lw = s_l[w][16 * ct + r];
+        total += mw == -__builtin_inff() ? lw : exp2_fast(mw - top) * lw;   // NaN scores leave m, and l is NaN
+      }
+      if (p.chunks > 1) {
+        const int64_t row = (int64_t)p.slot * (16 * CT) + 16 * ct + r;
+        *reinterpret_cast<v4f*>(a.part + row * D + 16 * dt + 4 * g) = v;
+        if (dt == 0 && g == 0) a.ml[row] = float2{top, total};
+      } else {
+        const int tok = col / G, h = p.head * G + col % G;
+        v = total == 0.0f ? v4f{0.f, 0.f, 0.f, 0.f} : v / total;
+        put_4<QT>(a.out + (int64_t)(p.seq.begin + tok) * a.ldo + (int64_t)h * D + 16 * dt + 4 * g, owide, v);
+      }
+    }
+  }
+}
+
+// ---- The join of split tiles: a wave per output row (token, head), lanes over
+// its channels in fours and, where these are fewer than 64 lanes, over chunks.
+template <int QT>
+__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int D) {
+  const int token = blockIdx.x, lane = threadIdx.x & 63;
+  const int s = seq_at(a.b, token);
+  if (s >= a.b.n_seqs) return;
+  const Seq q = seq_of(a.b, s);
+  if (token < q.begin || token >= q.begin + q.n) return;
+  int slot0, chunks;
+  slots_of(a.b, a.w, s, slot0, chunks);
+  const int mine = a.w.kv_heads * chunks * tiles_of(a.w, q.n);
+  if (chunks == 1 || slot0 + mine > a.w.slots) return;   // the latter for starts that do not ascend
+  const int G = a.w.G, Hk = a.w.kv_heads, quads = D / 4;
+  const int per = quads <= 8 ? 8 : quads <= 16 ? 16 : quads <= 32 ? 32 : 64;   // lanes of a row's channels
+  const int lanes = 64 / per, part = lane / per, quad = lane % per;
+  const bool wide = wide_rows(a.out, a.ldo);
+  for (int h = blockIdx.y * 4 + wave_id(); h < G * Hk; h += 4 * gridDim.y) {
+    const int col = (token - q.begin) * G + h % G, head = h / G, tile = col / a.w.tile;
+    // slot of chunk c: slot0 + (tile * chunks + c) * kv_heads + head
+    const int64_t row0 = ((int64_t)slot0 + (int64_t)tile * chunks * Hk + head) * a.w.tile + col % a.w.tile;
+    const int64_t step = (int64_t)Hk * a.w.tile;
+    float top = -__builtin_inff();
+    for (int c = lane; c < chunks; c += 64) top = fmaxf(top, a.ml[row0 + c * step].x);
+    for (int o = 32; o > 0; o /= 2) top = fmaxf(top, __shfl_xor(top, o, 64));
+    float total = 0.0f;
+    v4f v = {0.f, 0.f, 0.f, 0.f};
+    for (int c = part; c < chunks; c += lanes) {
+      const float2 ml = a.ml[row0 + c * step];
+      const float by = ml.x == -__builtin_inff() ? (ml.y == 0.0f ? 0.0f : 1.0f) : exp2_fast(ml.x - top);
+      total += by * ml.y;
+      if (quad < quads) v += by * *reinterpret_cast<const v4f*>(a.part + (row0 + c * step) * D + 4 * quad);
+    }
+    for (int o = per; o < 64; o *= 2) {
+      total += __shfl_xor(total, o, 64);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += __shfl_xor(v[i], o, 64);
+    }
+    if (part == 0 && quad < quads) {
+      v = total == 0.0f ? v4f{0.f, 0.f, 0.f, 0.f} : v / total;
+      put_4<QT>(a.out + (int64_t)token * a.ldo + (int64_t)h * D + 4 * quad, wide, v);
+    }
+  }
+}
+
+}  // namespace kqd
+
+namespace kq {
+using namespace kqd;
+
+int launch_attn_join(const AttnArgs& a, int type, int D, hipStream_t stream) {
+  const unsigned heads = (unsigned)((a.w.G * a.w.kv_heads + 3) / 4);
+  const dim3 grid((unsigned)a.b.n_tokens, heads);
+  dispatch_log("k_attn_join", -1, a.w.G * a.w.kv_heads, D, a.b.n_tokens, grid.x, grid.y, 256, 0, "-");
+  if (type == KQ_F16) hipLaunchKernelGGL(k_attn_join<A_F16>, grid, dim3(256), 0, stream, a, D);
+  else hipLaunchKernelGGL(k_attn_join<A_BF16>, grid, dim3(256), 0, stream, a, D);
+  return (int)hipGetLastError();
+}
+
+AttnArgs attn_args(const AttnCall& p, const AttnPlan& w) {
+  AttnArgs a;
+  const kq_kv_batch& b = *p.batch;
+  const kq_kv_cache& c = *p.cache;
+  a.b = Batch{b.page_table, b.table_width, b.q_start, b.lens, b.n_seqs, b.n_tokens};
+  a.c = Cache{static_cast<uint8_t*>(c.k), static_cast<uint8_t*>(c.v), c.n_pages, c.kv_heads};
+  a.w = Split{p.heads / c.kv_heads, c.kv_heads, w.tile, p.window, w.target, w.least, (int)w.slots};
+  a.q = static_cast<const uint16_t*>(p.q);
+  a.out = static_cast<uint16_t*>(p.out);
+  a.tree = p.tree;
+  a.part = static_cast<float*>(p.ws);
+  a.ml = reinterpret_cast<float2*>(a.part + w.slots * w.tile * c.head_dim);
+  a.ldq = p.ldq;
+  a.ldo = p.ldo;
+  a.scale = p.scale * 1.4426950408889634f;
+  return a;
+}
+
+namespace {
+
+template <int QT, bool Q8, int DB, int CT>
+int decode_launch(const AttnCall& p, const AttnPlan& w) {
+  const AttnArgs a = attn_args(p, w);
+  dispatch_log("k_attn_decode", -1, p.heads, 32 * DB, p.batch->n_tokens, (unsigned)w.grid, 1, 64 * DEC_WAVES, 0,
+               "cache=%d tile=%d slots=%lld", p.cache->type, w.tile, (long long)w.slots);
+  hipLaunchKernelGGL((k_attn_decode<QT, Q8, DB, CT>), dim3((unsigned)w.grid), dim3(64 * DEC_WAVES), 0, p.stream, a);
+  int err = (int)hipGetLastError();
+  if (err || w.slots == 0) return err;
+  return launch_attn_join(a, p.type, 32 * DB, p.stream);
+}
+template <int QT, bool Q8, int DB>
+int decode_cols(const AttnCall& p, const AttnPlan& w) {
+  constexpr int MOST = DB <= 4 ? 4 : 2;
+  return w.tile == 16 ? decode_launch<QT, Q8, DB, 1>(p, w) : decode_launch<QT, Q8, DB, MOST>(p, w);
+}
+template <int QT, bool Q8>
+int decode_dim(const AttnCall& p, const AttnPlan& w) {
+  switch (p.cache->head_dim / 32) {
+    case 1: return decode_cols<QT, Q8, 1>(p, w);
+    case 2: return decode_cols<QT, Q8, 2>(p, w);
+    case 3: return decode_cols<QT, Q8, 3>(p, w);
+    case 4: return decode_cols<QT, Q8, 4>(p, w);
+    case 5: return decode_cols<QT, Q8, 5>(p, w);
+    case 6: return decode_cols<QT, Q8, 6>(p, w);
+    case 7: return decode_cols<QT, Q8, 7>(p, w);
+    default: return decode_cols<QT, Q8, 8>(p, w);
+  }
+}
+
+}  // namespace
+
+// Partial results take part in a call only where a table row is longer than
+// the shortest chunk.
+void finish_plan(const kq_kv_cache& c, const kq_kv_batch& b, int heads, AttnPlan& w) {
+  const int64_t G = heads / c.kv_heads;
+  const int64_t tiles = c.kv_heads * ((b.n_tokens * G + w.tile - 1) / w.tile + b.n_seqs);
+  w.grid = w.target + tiles;
+  const bool split = b.table_width > w.least;
+  w.slots = split ? (w.grid < 2ll * w.target ? w.grid : 2ll * w.target) : 0;
+  if (!split) w.grid = tiles;
+  w.bytes = w.slots * w.tile * ((int64_t)c.head_dim + 2) * 4;
+}
+
+AttnPlan decode_plan(const kq_kv_cache& c, const kq_kv_batch& b, int heads) {
+  AttnPlan w;
+  const int64_t cols = ((int64_t)b.n_tokens * (heads / c.kv_heads) + b.n_seqs - 1) / b.n_seqs;   // of a mean sequence
+  w.tile = cols <= 16 ? 16 : c.head_dim <= 128 ? 64 : 32;
+  w.target = 512;
+  w.least = 4;
+  finish_plan(c, b, heads, w);
+  return w;
+}
+
+int launch_attn_decode(const AttnCall& p) {
+  const AttnPlan w = decode_plan(*p.cache, *p.batch, p.heads);
+  const bool q8 = p.cache->type == KQ_KV_Q8_0;
+  if (p.type == KQ_F16) return q8 ? decode_dim<A_F16, true>(p, w) : decode_dim<A_F16, false>(p, w);
+  return q8 ? decode_dim<A_BF16, true>(p, w) : decode_dim<A_BF16, false>(p, w);
+}
+
+}  // namespace kq

@@ -273,6 +273,61 @@ struct Mx4MoeArgs {
 int64_t mx4_moe_workspace_bytes(int64_t hidden, int64_t inter, int M, int top_k, int E);
 int launch_mx4_moe(const Mx4MoeArgs& a);
 
+// ---- rotary positions and the paged key-value cache (kq_rope.hip)
+int launch_rope(const kq_rope_spec* r, int xtype, const void* x, int64_t ldx, int otype, void* y, int64_t ldy, int T,
+                int heads, int D, hipStream_t stream);
+struct KvAppendArgs {
+  const kq_kv_cache* cache;
+  const kq_kv_batch* batch;
+  const kq_rope_spec* rope;   // or null
+  int xtype;
+  const void* k;
+  int64_t ldk;
+  const void* v;
+  int64_t ldv;
+  const void* q;              // or null
+  int64_t ldq;
+  int otype;
+  void* q_out;
+  int64_t ldo;
+  int heads;
+  hipStream_t stream;
+};
+int launch_kv_append(const KvAppendArgs& a);
+int launch_kv_read(const kq_kv_cache& c, const kq_kv_batch& b, int otype, void* k, int64_t ldk, void* v, int64_t ldv,
+                   hipStream_t stream);
+
+// ---- attention over the paged cache (kq_attn.hip, kq_attn_prompt.hip)
+struct AttnCall {
+  int type;                   // kq_type of q and out
+  const void* q;
+  int64_t ldq;
+  const kq_kv_cache* cache;
+  const kq_kv_batch* batch;
+  void* out;
+  int64_t ldo;
+  int heads;
+  float scale;
+  int window;
+  const uint64_t* tree;       // or null
+  void* ws;
+  hipStream_t stream;
+};
+// How a call's work is shared out (see Split in kq_kv_dev.h): columns of a
+// tile, workgroups, and what partial results take.
+struct AttnPlan {
+  int tile;
+  int target;
+  int least;
+  int64_t grid;
+  int64_t slots;
+  int64_t bytes;
+};
+AttnPlan decode_plan(const kq_kv_cache& c, const kq_kv_batch& b, int heads);
+AttnPlan prompt_plan(const kq_kv_cache& c, const kq_kv_batch& b, int heads);
+int launch_attn_decode(const AttnCall& a);
+int launch_attn_prompt(const AttnCall& a);
+
 int64_t argmax_partials(int64_t N);
 int launch_argmax(const float* y, int64_t N, int M, int32_t* out, void* ws, hipStream_t stream);
 int launch_argmax_final(const void* part, int nparts, int M, int32_t* out, hipStream_t stream);

@@ -1,0 +1,234 @@
+// kq_kv_dev.h — the paged key-value cache as the kernels see it: where an
+// element lies in a page, which tokens a batch holds, and how attention's work
+// is shared among workgroups.
+//
+// A page holds 32 positions. Per key-value head it has one region for K and
+// one for V, in pieces of 8 elements ordered as matrix instructions take them:
+// a wave's loads of an operand are 64 consecutive 16-byte pieces, V comes
+// transposed (8 positions of one channel), and the scores' layout is the next
+// product's operand layout without any exchange between lanes. With p the
+// position in the page, r = 4 (p / 8) + p % 4, t = (p / 4) % 2:
+//   16-bit K: (p, d) at element (d / 32 * 2 + t) * 512 + (d % 32 / 8 * 16 + r) * 8 + d % 8
+//   16-bit V: (p, d) at element d / 16 * 512 + (p / 8 * 16 + d % 16) * 8 + p % 8
+//   Q8_0 K:   (p, d) at byte d / 32 * 1024 + (d % 32 / 8 * 16 + r) * 16 + t * 8 + d % 8
+//   Q8_0 V:   (p, d) at byte d / 32 * 1024 + (p / 8 * 16 + d % 16) * 16 + d % 32 / 16 * 8 + p % 8
+//   Q8_0: then the fp16 scales of 32 channels, (p, b) at element b * 32 + p.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kq_dev.h"
+#include "kq_internal.h"
+
+namespace kqd {
+
+constexpr int PAGE = 32;
+
+// Bytes of one head's region of a page.
+__host__ __device__ constexpr int64_t region_bytes(bool q8, int D) { return q8 ? 34ll * D : 64ll * D; }
+
+// Element (16 bits) or byte (Q8_0) indices in a region, as above.
+__device__ __forceinline__ int k_index(bool q8, int p, int d) {
+  const int r = 4 * (p >> 3) + (p & 3), t = (p >> 2) & 1, g = (d & 31) >> 3;
+  return q8 ? (d >> 5) * 1024 + (g * 16 + r) * 16 + t * 8 + (d & 7)
+            : ((d >> 5) * 2 + t) * 512 + (g * 16 + r) * 8 + (d & 7);
+}
+__device__ __forceinline__ int v_index(bool q8, int p, int d) {
+  return q8 ? (d >> 5) * 1024 + ((p >> 3) * 16 + (d & 15)) * 16 + ((d >> 4) & 1) * 8 + (p & 7)
+            : (d >> 4) * 512 + ((p >> 3) * 16 + (d & 15)) * 8 + (p & 7);
+}
+
+// Device view of kq_kv_batch and kq_kv_cache.
+struct Batch {
+  const int32_t* table;
+  int64_t width;
+  const int32_t* q_start;
+  const int32_t* lens;
+  int n_seqs;
+  int n_tokens;
+};
+struct Cache {
+  uint8_t* k;
+  uint8_t* v;
+  int64_t n_pages;
+  int kv_heads;
+};
+
+// The new tokens [begin, begin + n) of a sequence and its length; whatever the
+// arrays hold, the tokens lie inside the batch.
+struct Seq {
+  int begin, n, len;
+};
+__device__ __forceinline__ Seq seq_of(const Batch& b, int s) {
+  int begin = b.q_start[s], end = b.q_start[s + 1];
+  begin = min(max(begin, 0), b.n_tokens);
+  end = min(max(end, begin), b.n_tokens);
+  return Seq{begin, end - begin, min(max(b.lens[s], 0), 0x7fffff00)};
+}
+
+// The sequence of token t: the first whose tokens end behind it, or n_seqs.
+// Called by whole waves with one t.
+__device__ __forceinline__ int seq_at(const Batch& b, int t) {
+  const int lane = threadIdx.x & 63;
+  int at = 0;
+  for (int s0 = 0; s0 < b.n_seqs; s0 += 64) {
+    const int s = s0 + lane;
+    const int done = __popcll(__ballot(s < b.n_seqs && b.q_start[s + 1] <= t));
+    at += done;
+    if (done < 64) break;
+  }
+  return __builtin_amdgcn_readfirstlane(min(at, b.n_seqs));
+}
+
+// Page id of page `page` of sequence s; -1 where the table names none of the
+// cache's pages, -2 behind the table.
+__device__ __forceinline__ int32_t page_id(const Batch& b, int64_t n_pages, int s, int page) {
+  if (page >= b.width) return -2;
+  const int32_t id = b.table[(int64_t)s * b.width + page];
+  return id >= 0 && id < n_pages ? id : -1;
+}
+
+// What a wave wrote to LDS is seen by all its lanes from here on.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Inclusive sum over the lanes of a wave.
+__device__ __forceinline__ int64_t wave_scan(int64_t v) {
+  const int lane = threadIdx.x & 63;
+  for (int o = 1; o < 64; o *= 2) {
+    const int64_t u = __shfl_up(v, o, 64);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+__device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// ---- Which part of attention a workgroup does. The columns of a sequence and
+// key-value head are its n * G queries (token by token, the G heads of a token
+// together), taken `tile` at a time; a tile walks the pages that its sequence's
+// queries can see, and where there are few tiles these are split into chunks of
+// about equal length, joined by a second kernel in chunk order. `per` pages, the
+// longest chunk, is the mean of all the work over `target` workgroups, at least
+// `least`: at most target + (number of tiles) workgroups have a part, and at
+// most 2 target of them belong to a split tile (a sequence of np > per pages has
+// ceil(np / per) < 2 np / per chunks). The order of the sums depends on the
+// batch's lengths alone.
+struct Split {
+  int G;          // query heads per key-value head
+  int kv_heads;
+  int tile;       // columns
+  int window;     // 0: none
+  int target;
+  int least;
+  int slots;      // partial results the workspace holds
+};
+struct Part {
+  int s;          // sequence, or -1: nothing to do
+  Seq seq;
+  int first, np;  // the sequence's pages [first, first + np)
+  int head, tile; // key-value head, column tile
+  int chunk, chunks;
+  int slot;       // of a split tile's partial result
+};
+__device__ __forceinline__ void pages_of(const Batch& b, const Seq& q, int window, int& first, int& np) {
+  const int lo = window > 0 ? max(q.len - q.n - window + 1, 0) : 0;   // len - n is the first query's position
+  first = lo / PAGE;
+  np = (q.len + PAGE - 1) / PAGE - first;
+  if ((int64_t)q.len > b.width * PAGE) first = (int)b.width, np = 1;   // behind the table: one look at it says so
+  np = max(np, 0);
+}
+__device__ __forceinline__ int tiles_of(const Split& w, int n) {
+  return (int)(((int64_t)n * w.G + w.tile - 1) / w.tile);
+}
+__device__ __forceinline__ int chunks_of(int np, int per) { return max((np + per - 1) / per, 1); }
+
+// Pages per chunk. Called by whole waves.
+__device__ __forceinline__ int pages_per_chunk(const Batch& b, const Split& w) {
+  const int lane = threadIdx.x & 63;
+  int64_t total = 0;
+  for (int s0 = 0; s0 < b.n_seqs; s0 += 64) {
+    if (s0 + lane < b.n_seqs) {
+      const Seq q = seq_of(b, s0 + lane);
+      int first, np;
+      pages_of(b, q, w.window, first, np);
+      total += (int64_t)np * tiles_of(w, q.n) * w.kv_heads;
+    }
+  }
+  for (int o = 32; o > 0; o /= 2) total += __shfl_xor(total, o, 64);
+  int64_t per = (total + w.target - 1) / w.target;
+  per = per < w.least ? w.least : per;
+  return scalar((int)(per > 0x7fffffff ? 0x7fffffff : per));
+}
+
+// Part `id` of the grid.
+__device__ __forceinline__ Part part_of(const Batch& b, const Split& w, int id) {
+  const int lane = threadIdx.x & 63;
+  const int per = pages_per_chunk(b, w);
+  Part p;
+  p.s = -1;
+  int64_t before = 0, slots = 0;
+  for (int s0 = 0; s0 < b.n_seqs; s0 += 64) {
+    const int s = s0 + lane;
+    int64_t mine = 0, split = 0;
+    if (s < b.n_seqs) {
+      const Seq q = seq_of(b, s);
+      int first, np;
+      pages_of(b, q, w.window, first, np);
+      const int chunks = chunks_of(np, per);
+      mine = (int64_t)tiles_of(w, q.n) * w.kv_heads * chunks;
+      split = chunks > 1 ? mine : 0;
+    }
+    const int64_t upto = wave_scan(mine) + before, slot = wave_scan(split) + slots;
+    const uint64_t hit = __ballot(id < upto);
+    if (hit) {
+      const int l = __ffsll((unsigned long long)hit) - 1;
+      p.s = s0 + l;
+      p.seq = seq_of(b, p.s);
+      p.seq.begin = scalar(p.seq.begin);
+      p.seq.n = scalar(p.seq.n);
+      p.seq.len = scalar(p.seq.len);
+      pages_of(b, p.seq, w.window, p.first, p.np);
+      p.chunks = chunks_of(p.np, per);
+      const int local = scalar((int)(id - __shfl(upto - mine, l, 64)));
+      // heads next to each other: with 8 of them every tile and chunk of a head lies on one XCD
+      p.head = local % w.kv_heads;
+      p.chunk = local / w.kv_heads % p.chunks;
+      // the last tiles first: they see the most
+      p.tile = tiles_of(w, p.seq.n) - 1 - local / w.kv_heads / p.chunks;
+      p.slot = scalar((int)(__shfl(slot - split, l, 64))) + (p.tile * p.chunks + p.chunk) * w.kv_heads + p.head;
+      return p;
+    }
+    before = __shfl(upto, 63, 64);
+    slots = __shfl(slot, 63, 64);
+  }
+  return p;
+}
+
+// First slot of sequence s's split tiles, and its chunks (1: not split).
+__device__ __forceinline__ void slots_of(const Batch& b, const Split& w, int s, int& slot0, int& chunks) {
+  const int lane = threadIdx.x & 63;
+  const int per = pages_per_chunk(b, w);
+  int64_t sum = 0;
+  for (int s0 = 0; s0 <= s; s0 += 64) {
+    const int i = s0 + lane;
+    if (i < s) {
+      const Seq q = seq_of(b, i);
+      int first, np;
+      pages_of(b, q, w.window, first, np);
+      const int c = chunks_of(np, per);
+      sum += c > 1 ? (int64_t)tiles_of(w, q.n) * w.kv_heads * c : 0;
+    }
+  }
+  for (int o = 32; o > 0; o /= 2) sum += __shfl_xor(sum, o, 64);
+  slot0 = scalar((int)sum);
+  const Seq q = seq_of(b, s);
+  int first, np;
+  pages_of(b, q, w.window, first, np);
+  chunks = scalar(chunks_of(np, per));
+}
+
+}  // namespace kqd

@@ -5,7 +5,9 @@
  * LLM inference: dequantize-and-multiply of block-quantized weights against a
  * few activation columns, and the routed-expert (mixture-of-experts) variant;
  * for microscaled 4-bit weights also the quantiser, the product of two such
- * matrices, the router and the whole mixture-of-experts layer.
+ * matrices, the router and the whole mixture-of-experts layer; and what lies
+ * between the projections of a layer: rotary positions, a paged key-value
+ * cache, and attention over it for new tokens and for prompts.
  *
  * Where the operation comes from (page title, section):
  *  - Kinetic docs, "What makes it fast": generating a token reads every weight
@@ -419,6 +421,187 @@ int kq_mx4_moe_layer(int xtype, const void* x, int wtype, const void* router, co
                      const void* down_scales, float* y, int32_t* ids, float* weights, int64_t hidden, int64_t inter,
                      int M, int top_k, int n_experts, int renorm, void* workspace, int64_t workspace_bytes,
                      void* stream);
+
+/* ---- Rotary positions, the paged key-value cache, attention ----
+ * What lies between a layer's q|k|v and o projections. The pages name the
+ * pieces and print no formula or layout, so the usual ones are the readings
+ * taken: contexts stretched by linear, NTK or YaRN scaling (Kinetic docs, the
+ * context section); a cache in blocks of 32 positions, also as Q8_0 (Kipp
+ * README, "What is in v0.0.6"); verify passes of chains and trees of guessed
+ * tokens (Kapitsa README, "How it works"); requests sharing a pass.
+ *
+ * Tokens are rows: token t of a batch has its heads * head_dim elements at
+ * t * ld elements after the base (ld >= heads * head_dim; the rows of a fused
+ * q|k|v product are read and written in place). Elements are aligned to their
+ * size; 16-byte aligned rows are read in 16-byte pieces. */
+#define KQ_KV_PAGE 32              /* positions per page */
+#define KQ_MAX_HEAD_DIM 256
+#define KQ_MAX_HEADS 1024
+#define KQ_MAX_TOKENS (1 << 20)    /* rows of a batch */
+#define KQ_MAX_SEQS 4096           /* sequences of a batch */
+#define KQ_MAX_WINDOW (1 << 30)
+
+/* How a pair of elements is formed: of the first rot_dim elements of a head,
+ * pair i is (i, i + rot_dim / 2) or (2 i, 2 i + 1). */
+typedef enum kq_rope_pairs { KQ_ROPE_HALF = 0, KQ_ROPE_INTERLEAVED = 1 } kq_rope_pairs;
+
+typedef struct kq_rope_spec {
+  const double* freqs;        /* device, [rot_dim / 2]: radians per position; 8-byte aligned */
+  const int32_t* positions;   /* device, [tokens]; kq_kv_append also takes NULL: the cache positions */
+  double mscale;              /* factor on cos and sin (finite) */
+  int32_t rot_dim;            /* even, 2 .. head_dim; elements from rot_dim on are copied */
+  int32_t pairs;              /* kq_rope_pairs */
+} kq_rope_spec;
+
+/* Scalings of kq_rope_freqs, with f_i = base^(-2 i / rot_dim):
+ *   NONE    f_i
+ *   LINEAR  f_i / factor
+ *   NTK     as NONE with base * factor^(rot_dim / (rot_dim - 2))
+ *   YARN    g f_i + (1 - g) f_i / factor, g = (n - beta_slow) / (beta_fast -
+ *           beta_slow) held in [0, 1], n = original_length f_i / (2 pi) the
+ *           turns of the pair over the original context; mscale = 0.1
+ *           ln(factor) + 1 (1 for factor <= 1; for the others always 1) */
+typedef enum kq_rope_scaling {
+  KQ_ROPE_NONE = 0, KQ_ROPE_LINEAR = 1, KQ_ROPE_NTK = 2, KQ_ROPE_YARN = 3
+} kq_rope_scaling;
+
+/* kq_rope_freqs — host: freqs[rot_dim / 2] and *mscale of a scaling (host
+ * memory; the caller copies freqs to the device once). base > 0 and factor > 0
+ * finite; original_length > 0 and beta_fast > beta_slow for YARN (usually 32
+ * and 1; ignored otherwise).
+ * Errors: KQ_ERR_ARG, KQ_ERR_SHAPE (rot_dim not even or not in [2, KQ_MAX_HEAD_DIM]). */
+int kq_rope_freqs(int scaling, int rot_dim, double base, double factor, int64_t original_length, double beta_fast,
+                  double beta_slow, double* freqs, double* mscale);
+
+/* kq_rope — out[t] = x[t] with every head rotated by its token's position:
+ *   a' = mscale (a cos th - b sin th), b' = mscale (a sin th + b cos th),
+ *   th = positions[t] * freqs[i] for pair i = (a, b).
+ * th, cos, sin and the products are 64-bit; results are rounded to fp32 and
+ * from there to otype (infinite past the largest finite value of fp16).
+ *   x: device, xtype, rows ldx apart. out: device, otype, rows ldo apart; x
+ *   itself (same type and ld) or no overlap with it. T <= KQ_MAX_TOKENS tokens;
+ *   T == 0 is a valid empty call. head_dim: a multiple of 32, at most
+ *   KQ_MAX_HEAD_DIM; heads in [1, KQ_MAX_HEADS].
+ * Errors: KQ_ERR_ARG, KQ_ERR_SHAPE, KQ_ERR_ALIGN, KQ_ERR_HIP. */
+int kq_rope(const kq_rope_spec* rope, int xtype, const void* x, int64_t ldx, int otype, void* out, int64_t ldo, int T,
+            int heads, int head_dim, void* stream);
+
+/* What a cache holds. 16-bit values, or Q8_0 blocks of 32 channels of one
+ * position (the scales and codes of kq_pack; a block that has no finite scale
+ * reads as NaN). */
+typedef enum kq_kv_type { KQ_KV_F16 = 1, KQ_KV_BF16 = 2, KQ_KV_Q8_0 = 8 } kq_kv_type;
+
+/* A layer's cache: n_pages pages of KQ_KV_PAGE positions, in two buffers. A page
+ * has kv_heads regions back to back, of 64 head_dim bytes (16-bit types) or 34
+ * head_dim bytes (Q8_0). With p the position in its page, r = 4 (p / 8) + p % 4
+ * and t = (p / 4) % 2, channel d of position p lies in its region
+ *   16-bit k  at element (d / 32 * 2 + t) * 512 + (d % 32 / 8 * 16 + r) * 8 + d % 8
+ *   16-bit v  at element d / 16 * 512 + (p / 8 * 16 + d % 16) * 8 + p % 8
+ *   Q8_0 k    code at byte d / 32 * 1024 + (d % 32 / 8 * 16 + r) * 16 + t * 8 + d % 8
+ *   Q8_0 v    code at byte d / 32 * 1024 + (p / 8 * 16 + d % 16) * 16 + d % 32 / 16 * 8 + p % 8
+ *   Q8_0      fp16 scales behind the 32 head_dim codes: block d / 32 of position p
+ *             is scale d / 32 * 32 + p
+ * Pages can be copied and shared as they are. */
+typedef struct kq_kv_cache {
+  int32_t type;       /* kq_kv_type */
+  int32_t kv_heads;   /* 1 .. KQ_MAX_HEADS */
+  int32_t head_dim;   /* a multiple of 32, at most KQ_MAX_HEAD_DIM */
+  int32_t reserved;   /* must be 0 */
+  int64_t n_pages;    /* 1 .. 2^31 - 1 */
+  void* k;            /* device, 16-byte aligned, n_pages * kq_kv_page_bytes */
+  void* v;
+} kq_kv_cache;
+
+/* The new tokens of a pass. Sequence s has rows [q_start[s], q_start[s + 1]) and
+ * lens[s] positions in all, its new tokens the last of them: token i of n is at
+ * position lens[s] - n + i, which lies in page page_table[s][position /
+ * KQ_KV_PAGE]. Starts ascend; rows before the first and behind the last
+ * sequence belong to none and are left as they are in every output. The arrays
+ * are device memory, read when the kernels run, so a captured graph follows
+ * what they hold at each replay. Whatever they hold, nothing outside the
+ * buffers is touched: a page id that is not in [0, n_pages) is never followed
+ * (see the calls), and tokens whose position is negative (n > lens[s]) have no
+ * place. */
+typedef struct kq_kv_batch {
+  const int32_t* page_table;   /* device, [n_seqs][table_width] */
+  int64_t table_width;         /* pages per row, 1 .. 2^26 - 1 */
+  const int32_t* q_start;      /* device, [n_seqs + 1] */
+  const int32_t* lens;         /* device, [n_seqs] */
+  int32_t n_seqs;              /* 0 .. KQ_MAX_SEQS */
+  int32_t n_tokens;            /* rows of the batch's tensors, 0 .. KQ_MAX_TOKENS */
+} kq_kv_batch;
+
+/* Bytes of a page in each of k and v: kv_heads * head_dim * 64 (Q8_0: 34), or a
+ * negative kq_status. */
+int64_t kq_kv_page_bytes(int type, int kv_heads, int head_dim);
+
+/* kq_kv_append — writes the new tokens' k and v into their pages, k rotated as
+ * kq_rope does (rope NULL: as it is); and, where q is not NULL, writes q rotated
+ * in the same way to q_out, all in one launch.
+ *   k, v, q: device, xtype, rows ldk, ldv, ldq apart. q_out: device, otype, rows
+ *   ldo apart; q itself (same type and ld) or no overlap with k, v or q. heads:
+ *   q's, at most KQ_MAX_HEADS.
+ * Values are rounded as kq_rope rounds them; Q8_0 blocks are quantised from fp32. A token whose page id is invalid or
+ * behind the table is not stored (its q is rotated all the same); one without a
+ * place is skipped. Sequences must not share the pages written to. n_tokens ==
+ * 0 or n_seqs == 0 is a valid empty call.
+ * Errors: KQ_ERR_ARG, KQ_ERR_SHAPE, KQ_ERR_ALIGN, KQ_ERR_HIP. */
+int kq_kv_append(const kq_kv_cache* cache, const kq_kv_batch* batch, const kq_rope_spec* rope, int xtype, const void* k,
+                 int64_t ldk, const void* v, int64_t ldv, const void* q, int64_t ldq, int otype, void* q_out, int64_t ldo,
+                 int heads, void* stream);
+
+/* kq_kv_read — the rows of the batch's tokens as the cache holds them (NaN where
+ * the page id is invalid or behind the table): k and v, device, otype, rows ldk
+ * and ldv apart, kv_heads * head_dim elements each. With q_start the sums of
+ * lens it reads whole sequences.
+ * Errors: as kq_kv_append. */
+int kq_kv_read(const kq_kv_cache* cache, const kq_kv_batch* batch, int otype, void* k, int64_t ldk, void* v, int64_t ldv,
+               void* stream);
+
+/* Workspace bytes of the two attention calls for this cache and batch (the
+ * sizes count, the pointers may be NULL); 0: none needed. Negative: the error
+ * of an invalid shape. */
+int64_t kq_attn_decode_workspace_bytes(const kq_kv_cache* cache, const kq_kv_batch* batch, int heads);
+int64_t kq_attn_prompt_workspace_bytes(const kq_kv_cache* cache, const kq_kv_batch* batch, int heads);
+
+/* kq_attn_decode — attention of a few new tokens per sequence (decode steps,
+ * verify passes) over the paged cache: for query head h of the token at
+ * position at, with the keys and values of key-value head h / (heads /
+ * kv_heads),
+ *   out = sum_j w_j v_j / sum_j w_j, w_j = exp(scale q . k_j),
+ * over positions j <= at, with window > 0 only j > at - window, and with tree
+ * only those of the sequence's new tokens whose bit is set: bit i of tree[row]
+ * says that the row's query sees new token i (older positions are all seen).
+ * The new tokens' own keys and values have to be in the cache (kq_kv_append).
+ *   q, out: device, [rows][heads * head_dim] of type (KQ_F16 or KQ_BF16), ldq
+ *   and ldo apart; the cache holds the same type or Q8_0. heads: a multiple of
+ *   kv_heads, at most KQ_MAX_HEADS. tree: device, 8-byte aligned, one uint64 per
+ *   row, or NULL. scale: positive, finite. window: 0 (none) .. KQ_MAX_WINDOW.
+ *   At most KQ_MAX_M rows (n_tokens) and as many sequences; workspace: device,
+ *   16-byte aligned, scratch, may be NULL where none is needed.
+ * A query that sees nothing, or no score above minus infinity, gives zeros.
+ * What a query does not see does not reach it, infinities and NaN included.
+ * One that sees a key in a page whose id is invalid gives NaN, as do all
+ * queries of a sequence longer than its table. Scores, softmax and sums are
+ * fp32; weights enter the products with V as two 16-bit parts; results are
+ * rounded once. The cache is split over its length where there are few
+ * sequences and heads; the order of the sums depends on the batch's shape and
+ * lengths alone, so results are deterministic.
+ * Errors: KQ_ERR_ARG, KQ_ERR_SHAPE, KQ_ERR_ALIGN, KQ_ERR_HIP. */
+int kq_attn_decode(int type, const void* q, int64_t ldq, const kq_kv_cache* cache, const kq_kv_batch* batch, void* out,
+                   int64_t ldo, int heads, float scale, int window, const uint64_t* tree, void* workspace,
+                   int64_t workspace_bytes, void* stream);
+
+/* kq_attn_prompt — the same for many new tokens per sequence: whole prompts of
+ * different lengths packed into one batch, or the next part of prompts whose
+ * beginning is in the cache. Arguments and results as kq_attn_decode, without
+ * trees, up to KQ_MAX_TOKENS rows and KQ_MAX_SEQS sequences. Weights enter the
+ * products with V rounded to 16 bits (8-bit caches: two 16-bit parts); their sum
+ * is of the unrounded ones.
+ * Errors: as kq_attn_decode, and KQ_ERR_ARG where the batch is beyond the grid. */
+int kq_attn_prompt(int type, const void* q, int64_t ldq, const kq_kv_cache* cache, const kq_kv_batch* batch, void* out,
+                   int64_t ldo, int heads, float scale, int window, void* workspace, int64_t workspace_bytes,
+                   void* stream);
 
 /* ---- Shortlist: an exact argmax that scores only the rows that can win ----
  * Kinetic docs, "What makes it fast" (the Shortlist paragraph): choosing the
