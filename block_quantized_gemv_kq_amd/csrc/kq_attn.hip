@@ -46,7 +46,7 @@ __device__ __forceinline__ void load_page(Page<Q8, DB>& p, const Cache& c, int32
 }
 
 template <int QT, bool Q8, int DB, int CT>
-__global__ __launch_bounds__(64 * DEC_WAVES) void k_attn_decode(AttnArgs a) {
+__global__ __launch_bounds__(64 * DEC_WAVES, DB * CT <= 4 ? 2 : 1) void k_attn_decode(AttnArgs a) {
   constexpr int D = 32 * DB, DT = 2 * DB, VT = Q8 ? A_BF16 : QT;
   // d-tiles per round of the sum over the waves: 64 KB of LDS
   constexpr int ROUND = DT * CT * DEC_WAVES <= 64 ? DT : 64 / (CT * DEC_WAVES);
@@ -76,6 +76,18 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void k_attn_decode(AttnArgs a) {
       qf[ct][c] = row_piece(q + 32 * c, qwide);
       if (!have) qf[ct][c] = u32x4{0u, 0u, 0u, 0u};
     }
+  }
+  // Codes come with a bias added (see biased16); it leaves the scores through
+  // what the products start from, and o through the sums z of the weights.
+  v4f kbias[Q8 ? CT : 1][Q8 ? DB : 1], z[Q8 ? CT : 1][Q8 ? DB : 1];
+  if constexpr (Q8) {
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int c = 0; c < DB; ++c) {
+        kbias[ct][c] = mfma16<QT>(splat16<QT>(-Bias<QT>::v), qf[ct][c], v4f{0.f, 0.f, 0.f, 0.f});
+        z[ct][c] = v4f{0.f, 0.f, 0.f, 0.f};
+      }
   }
   // a page that every column sees whole needs no mask
   const int newest = p.seq.len - p.seq.n;   // position of the first new token
@@ -111,8 +123,8 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void k_attn_decode(AttnArgs a) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if constexpr (Q8) {
-            const u32x4 kf = codes16<QT>(pg.k[c][2 * h], pg.k[c][2 * h + 1]);
-            const v4f d = mfma16<QT>(kf, qf[ct][c], v4f{0.f, 0.f, 0.f, 0.f});
+            const u32x4 kf = biased16<QT>(pg.k[c][2 * h], pg.k[c][2 * h + 1]);
+            const v4f d = mfma16<QT>(kf, qf[ct][c], kbias[ct][c]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const uint32_t w = pg.ks[c][2 * h + i / 2];
@@ -147,6 +159,10 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void k_attn_decode(AttnArgs a) {
         l[ct] *= by;
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt) o[ct][dt] *= by;
+        if constexpr (Q8) {
+#pragma unroll
+          for (int c = 0; c < DB; ++c) z[ct][c] *= by;
+        }
       }
       const float sub = m[ct] == -__builtin_inff() ? 0.0f : m[ct];   // nothing seen yet: weights 0
       float e[8];
@@ -156,19 +172,32 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void k_attn_decode(AttnArgs a) {
         l[ct] += e[j];
       }
       if constexpr (Q8) {
-        // the scale of V's block goes to the weight: the codes stay whole numbers
+        // The scale of V's block goes to the weight, the codes stay whole numbers.
+        // A masked key's scale may be NaN.
+        u32x4 vs[DB];
 #pragma unroll
-        for (int c = 0; c < DB; ++c)
+        for (int c = 0; c < DB; ++c) vs[c] = pg.vs[c];
+        if (masked) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t w = pg.vs[c][j];
-            const float e0 = seen >> (2 * j) & 1 ? e[2 * j] * h2f(w) : 0.0f;
-            const float e1 = seen >> (2 * j + 1) & 1 ? e[2 * j + 1] * h2f(w >> 16) : 0.0f;
+            const uint32_t keep = (seen >> (2 * j) & 1 ? 0xffffu : 0u) | (seen >> (2 * j + 1) & 1 ? 0xffff0000u : 0u);
+#pragma unroll
+            for (int c = 0; c < DB; ++c) vs[c][j] &= keep;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < DB; ++c) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t w = vs[c][j];
             uint32_t hi, lo;
-            split2<A_BF16>(e0, e1, hi, lo);
+            split2<A_BF16>(e[2 * j] * h2f(w), e[2 * j + 1] * h2f(w >> 16), hi, lo);
             ph[ct][c][j] = hi;
             pl[ct][c][j] = lo;
           }
+          z[ct][c] = mfma16<A_BF16>(splat16<A_BF16>(1.0f), ph[ct][c], z[ct][c]);
+          z[ct][c] = mfma16<A_BF16>(splat16<A_BF16>(1.0f), pl[ct][c], z[ct][c]);
+        }
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -184,7 +213,7 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void k_attn_decode(AttnArgs a) {
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) {
       if constexpr (Q8) {
-        const u32x4 vf = codes16<VT>(pg.v[dt / 2][2 * (dt & 1)], pg.v[dt / 2][2 * (dt & 1) + 1]);
+        const u32x4 vf = biased16<VT>(pg.v[dt / 2][2 * (dt & 1)], pg.v[dt / 2][2 * (dt & 1) + 1]);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
           o[ct][dt] = mfma16<VT>(vf, ph[ct][dt / 2], o[ct][dt]);
@@ -218,11 +247,13 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void k_attn_decode(AttnArgs a) {
 
   if (steps > 0) {
     Page<Q8, DB> now, next;
-    int32_t id = scalar(page_id(a.b, a.c.n_pages, p.s, p0 + wave));
+    PageIds ids;
+    ids.fill(a.b, a.c.n_pages, p.s, p0 + wave, DEC_WAVES, 0);
+    int32_t id = ids.at(a.b, a.c.n_pages, p.s, p0 + wave, DEC_WAVES, 0);
     load_page<Q8, DB>(now, a.c, id, p.head);
     for (int i = 0; i < steps; ++i) {
       const int page = p0 + wave + i * DEC_WAVES;
-      const int32_t id_next = i + 1 < steps ? scalar(page_id(a.b, a.c.n_pages, p.s, page + DEC_WAVES)) : 0;
+      const int32_t id_next = i + 1 < steps ? ids.at(a.b, a.c.n_pages, p.s, p0 + wave, DEC_WAVES, i + 1) : 0;
       if (i + 1 < steps) load_page<Q8, DB>(next, a.c, id_next, p.head);
       step(now, id, page);
       now = next;
@@ -230,6 +261,14 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void k_attn_decode(AttnArgs a) {
     }
   }
 
+  if constexpr (Q8) {
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[ct][dt][i] = __builtin_fmaf(-Bias<VT>::v, z[ct][dt / 2][i], o[ct][dt][i]);
+  }
   // join the waves
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) {
@@ -287,48 +326,70 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void k_attn_decode(AttnArgs a) {
   }
 }
 
-// ---- The join of split tiles: a wave per output row (token, head), lanes over
-// its channels in fours and, where these are fewer than 64 lanes, over chunks.
+// ---- The join of split tiles: a workgroup per output row (token, head), lanes
+// over its channels in fours, groups of lanes over the chunks, several of each
+// group's in flight.
 template <int QT>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int D) {
-  const int token = blockIdx.x, lane = threadIdx.x & 63;
+  const int token = blockIdx.x, lane = threadIdx.x & 63, wave = wave_id();
+  __shared__ v4f sum[4][64];
+  __shared__ float sum_l[4];
   const int s = seq_at(a.b, token);
   if (s >= a.b.n_seqs) return;
   const Seq q = seq_of(a.b, s);
   if (token < q.begin || token >= q.begin + q.n) return;
   int slot0, chunks;
   slots_of(a.b, a.w, s, slot0, chunks);
-  const int mine = a.w.kv_heads * chunks * tiles_of(a.w, q.n);
-  if (chunks == 1 || slot0 + mine > a.w.slots) return;   // the latter for starts that do not ascend
   const int G = a.w.G, Hk = a.w.kv_heads, quads = D / 4;
+  const int mine = Hk * chunks * tiles_of(a.w, q.n);
+  if (chunks == 1 || slot0 + mine > a.w.slots) return;   // the latter for starts that do not ascend
   const int per = quads <= 8 ? 8 : quads <= 16 ? 16 : quads <= 32 ? 32 : 64;   // lanes of a row's channels
-  const int lanes = 64 / per, part = lane / per, quad = lane % per;
-  const bool wide = wide_rows(a.out, a.ldo);
-  for (int h = blockIdx.y * 4 + wave_id(); h < G * Hk; h += 4 * gridDim.y) {
-    const int col = (token - q.begin) * G + h % G, head = h / G, tile = col / a.w.tile;
-    // slot of chunk c: slot0 + (tile * chunks + c) * kv_heads + head
-    const int64_t row0 = ((int64_t)slot0 + (int64_t)tile * chunks * Hk + head) * a.w.tile + col % a.w.tile;
-    const int64_t step = (int64_t)Hk * a.w.tile;
-    float top = -__builtin_inff();
-    for (int c = lane; c < chunks; c += 64) top = fmaxf(top, a.ml[row0 + c * step].x);
-    for (int o = 32; o > 0; o /= 2) top = fmaxf(top, __shfl_xor(top, o, 64));
-    float total = 0.0f;
-    v4f v = {0.f, 0.f, 0.f, 0.f};
-    for (int c = part; c < chunks; c += lanes) {
-      const float2 ml = a.ml[row0 + c * step];
-      const float by = ml.x == -__builtin_inff() ? (ml.y == 0.0f ? 0.0f : 1.0f) : exp2_fast(ml.x - top);
-      total += by * ml.y;
-      if (quad < quads) v += by * *reinterpret_cast<const v4f*>(a.part + (row0 + c * step) * D + 4 * quad);
-    }
-    for (int o = per; o < 64; o *= 2) {
-      total += __shfl_xor(total, o, 64);
+  const int lanes = 64 / per, groups = 4 * lanes, part = wave * lanes + lane / per, quad = lane % per;
+  const int h = blockIdx.y, col = (token - q.begin) * G + h % G, head = h / G, tile = col / a.w.tile;
+  // slot of chunk c: slot0 + (tile * chunks + c) * kv_heads + head
+  const int64_t row0 = ((int64_t)slot0 + (int64_t)tile * chunks * Hk + head) * a.w.tile + col % a.w.tile;
+  const int64_t step = (int64_t)Hk * a.w.tile;
+  float top = -__builtin_inff();
+  for (int c = lane; c < chunks; c += 64) top = fmaxf(top, a.ml[row0 + c * step].x);
+  constexpr int FLY = 4;
+  float total = 0.0f;
+  v4f v = {0.f, 0.f, 0.f, 0.f};
+  float2 ml[FLY];
+  v4f o[FLY];
+  const auto fetch = [&](int c0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += __shfl_xor(v[i], o, 64);
+    for (int i = 0; i < FLY; ++i) {
+      const int c = min(c0 + i * groups, chunks - 1);
+      ml[i] = a.ml[row0 + c * step];
+      o[i] = *reinterpret_cast<const v4f*>(a.part + (row0 + c * step) * D + 4 * min(quad, quads - 1));
     }
-    if (part == 0 && quad < quads) {
-      v = total == 0.0f ? v4f{0.f, 0.f, 0.f, 0.f} : v / total;
-      put_4<QT>(a.out + (int64_t)token * a.ldo + (int64_t)h * D + 4 * quad, wide, v);
+  };
+  fetch(part);
+  for (int off = 32; off > 0; off /= 2) top = fmaxf(top, __shfl_xor(top, off, 64));
+  for (int c0 = part; c0 < chunks; c0 += FLY * groups) {
+    if (c0 > part) fetch(c0);
+#pragma unroll
+    for (int i = 0; i < FLY; ++i) {
+      if (c0 + i * groups >= chunks) continue;
+      const float by = ml[i].x == -__builtin_inff() ? (ml[i].y == 0.0f ? 0.0f : 1.0f) : exp2_fast(ml[i].x - top);
+      total += by * ml[i].y;
+      // a part that saw nothing holds zeros, or what scores of NaN made of it
+      v += by * o[i];
     }
+  }
+  for (int off = per; off < 64; off *= 2) {
+    total += __shfl_xor(total, off, 64);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += __shfl_xor(v[i], off, 64);
+  }
+  sum[wave][lane] = v;
+  if (lane == 0) sum_l[wave] = total;
+  __syncthreads();
+  if (wave == 0 && lane < quads) {
+    total = sum_l[0] + sum_l[1] + sum_l[2] + sum_l[3];
+    v = sum[0][lane] + sum[1][lane] + sum[2][lane] + sum[3][lane];
+    v = total == 0.0f ? v4f{0.f, 0.f, 0.f, 0.f} : v / total;
+    put_4<QT>(a.out + (int64_t)token * a.ldo + (int64_t)h * D + 4 * lane, wide_rows(a.out, a.ldo), v);
   }
 }
 
@@ -338,7 +399,7 @@ namespace kq {
 using namespace kqd;
 
 int launch_attn_join(const AttnArgs& a, int type, int D, hipStream_t stream) {
-  const unsigned heads = (unsigned)((a.w.G * a.w.kv_heads + 3) / 4);
+  const unsigned heads = (unsigned)(a.w.G * a.w.kv_heads);
   const dim3 grid((unsigned)a.b.n_tokens, heads);
   dispatch_log("k_attn_join", -1, a.w.G * a.w.kv_heads, D, a.b.n_tokens, grid.x, grid.y, 256, 0, "-");
   if (type == KQ_F16) hipLaunchKernelGGL(k_attn_join<A_F16>, grid, dim3(256), 0, stream, a, D);
@@ -378,8 +439,7 @@ int decode_launch(const AttnCall& p, const AttnPlan& w) {
 }
 template <int QT, bool Q8, int DB>
 int decode_cols(const AttnCall& p, const AttnPlan& w) {
-  constexpr int MOST = DB <= 4 ? 4 : 2;
-  return w.tile == 16 ? decode_launch<QT, Q8, DB, 1>(p, w) : decode_launch<QT, Q8, DB, MOST>(p, w);
+  return w.tile == 16 ? decode_launch<QT, Q8, DB, 1>(p, w) : decode_launch<QT, Q8, DB, 2>(p, w);
 }
 template <int QT, bool Q8>
 int decode_dim(const AttnCall& p, const AttnPlan& w) {
@@ -412,8 +472,8 @@ void finish_plan(const kq_kv_cache& c, const kq_kv_batch& b, int heads, AttnPlan
 AttnPlan decode_plan(const kq_kv_cache& c, const kq_kv_batch& b, int heads) {
   AttnPlan w;
   const int64_t cols = ((int64_t)b.n_tokens * (heads / c.kv_heads) + b.n_seqs - 1) / b.n_seqs;   // of a mean sequence
-  w.tile = cols <= 16 ? 16 : c.head_dim <= 128 ? 64 : 32;
-  w.target = 512;
+  w.tile = cols <= 16 ? 16 : 32;
+  w.target = 1024;
   w.least = 4;
   finish_plan(c, b, heads, w);
   return w;

@@ -32,9 +32,22 @@ struct AttnArgs {
   float scale;      // scale * log2(e)
 };
 
+__device__ __forceinline__ v16f zero16() {
+  v16f z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.0f;
+  return z;
+}
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 __device__ __forceinline__ uint32_t bits_of(float v) { return __builtin_bit_cast(uint32_t, v); }
 __device__ __forceinline__ float float_of(uint32_t v) { return __builtin_bit_cast(float, v); }
+
+// The larger of v and lane ^ 32's v (permlane32 swap, written out as in add_lane_xor32).
+__device__ __forceinline__ float max_lane_xor32(float v) {
+  uint32_t x = bits_of(v), y = x;
+  asm volatile("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(x), "+v"(y));
+  return fmaxf(float_of(x), float_of(y));
+}
 
 // A pair of fp32 as two 16-bit values of type T, nearest even.
 template <int T>
@@ -52,12 +65,11 @@ __device__ __forceinline__ float low_half(uint32_t v) { return T == A_F16 ? h2f(
 template <int T>
 __device__ __forceinline__ float high_half(uint32_t v) { return T == A_F16 ? h2f(v >> 16) : float_of(v & 0xffff0000u); }
 
-// hi + lo = the pair to twice the type's bits. An infinity or NaN is in hi alone.
+// hi + lo = the pair to twice the type's bits (finite values).
 template <int T>
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
   hi = pack2<T>(a, b);
-  const float ha = low_half<T>(hi), hb = high_half<T>(hi);
-  lo = pack2<T>(a == ha ? 0.0f : a - ha, b == hb ? 0.0f : b - hb);
+  lo = pack2<T>(a - low_half<T>(hi), b - high_half<T>(hi));
 }
 
 template <int T>
@@ -73,6 +85,18 @@ __device__ __forceinline__ v16f mfma32(u32x4 a, u32x4 b, v16f c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
   else
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8b, a), __builtin_bit_cast(v8b, b), c, 0, 0, 0);
+}
+
+// a + b of a packed pair, added to c.
+template <int T>
+__device__ __forceinline__ float add_pair(uint32_t p, float c) {
+  if constexpr (T == A_F16) {
+    return dot2(p, ONES, c);
+  } else {
+    typedef short s2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2, p), __builtin_bit_cast(b2, 0x3f803f80u), c, false);
+  }
 }
 
 // Eight int8 codes as 16-bit values (exact in both types).
@@ -98,6 +122,35 @@ __device__ __forceinline__ u32x4 codes16(uint32_t c0, uint32_t c1) {
     }
   }
   return r;
+}
+
+// Eight int8 codes as 16-bit values of code + BIAS, exact: fp16 1024 + (code +
+// 128) by its bits, bf16 code + 128.
+template <int T> struct Bias { static constexpr float v = T == A_F16 ? 1152.0f : 128.0f; };
+template <int T>
+__device__ __forceinline__ u32x4 biased16(uint32_t c0, uint32_t c1) {
+  u32x4 r;
+  const uint32_t u[2] = {c0 ^ 0x80808080u, c1 ^ 0x80808080u};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if constexpr (T == A_F16) {
+      r[2 * i] = perm(MAGIC, u[i], SEL_LO);
+      r[2 * i + 1] = perm(MAGIC, u[i], SEL_HI);
+    } else {
+      float f[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = (float)((u[i] >> (8 * j)) & 0xffu);
+      r[2 * i] = perm(bits_of(f[1]), bits_of(f[0]), 0x07060302u);   // the upper halves: 8 bits are exact there
+      r[2 * i + 1] = perm(bits_of(f[3]), bits_of(f[2]), 0x07060302u);
+    }
+  }
+  return r;
+}
+// Eight equal 16-bit values.
+template <int T>
+__device__ __forceinline__ u32x4 splat16(float v) {
+  const uint32_t p = pack2<T>(v, v);
+  return u32x4{p, p, p, p};
 }
 
 // Where a 16-bit element is infinite or NaN.

@@ -3,11 +3,11 @@
 //
 // A workgroup has a tile of columns: the queries of one key-value head, token
 // by token, so the heads of a group share what is read and a tile spans few
-// tokens, which keeps the masked corner small. Its waves have 32 columns (or
-// 64) each and walk the tile's pages together: the pages' regions come into
-// LDS by direct copies, one step ahead, in the order in which the operands of
-// the 32 x 32 x 16 matrix instructions are read back (64 lanes, 16 bytes each,
-// in runs of 256 bytes: no bank conflicts, nothing to transpose).
+// tokens, which keeps the masked corner small. Its waves have 32 columns each
+// and walk the tile's pages together: the pages' regions come into LDS by
+// direct copies, in the order in which the operands of the 32 x 32 x 16 matrix
+// instructions are read back (16 lanes read 256 bytes in a row: no bank
+// conflicts, nothing to transpose).
 //   S^T = K Q^T: keys on the rows, queries on the columns, so a lane has 16
 //   scores of one query per page and shares the column with one other lane;
 //   they are the operand of O^T += V^T P^T as they stand.
@@ -16,34 +16,54 @@
 
 #include "kq_attn_dev.h"
 
+// The kernel's parts: a call would put all that they share into memory.
+#define INLINE __attribute__((always_inline))
+
 namespace kqd {
 
-constexpr int PR_WAVES = 4, PR_PAGES = 2;   // pages per step
-
+// A step is PP pages. Step i of a wave is two phases: the matrix instructions
+// (the scores of step i, then V of step i - 1) and the arithmetic (the weights
+// of step i), each ended by a barrier. With 8 waves two share a SIMD; the second
+// four are one phase behind, so one of the two has matrix instructions while
+// the other has arithmetic: left alone they fall into step and take turns.
+// K and V of three steps are in LDS: in the phase in which the first half of
+// the waves begins step i, K of step i + 2 and V of step i + 1 take the places
+// of K of step i - 1 and V of step i - 2, which the second half last read in the
+// phase before; they are waited for two phases later.
 template <bool V> struct Flag { static constexpr bool value = V; };
 
-template <bool Q8, int DB, int NC>
-struct PromptShape {
+template <bool Q8, int DB, int WAVES_>
+struct Prompt {
+  static constexpr int WAVES = WAVES_, TILE = WAVES * 32;
+  static constexpr int PP = DB <= 4 ? 2 : 1;
   static constexpr int REGION = (int)region_bytes(Q8, 32 * DB);
-  static constexpr int STAGE = PR_PAGES * 2 * REGION;
-  static constexpr int TILE = PR_WAVES * 32 * NC;
+  static constexpr int STEP = PP * REGION, RING = 3;
+  static constexpr int LDS = 2 * RING * STEP;
 };
 
-// Copies `bytes` (a multiple of 16) from memory into LDS by the whole workgroup.
-__device__ __forceinline__ void copy_in(uint8_t* dst, const uint8_t* src, int bytes) {
-  const int wave = wave_id(), lane = threadIdx.x & 63;
+// Copies a region from memory into LDS, the workgroup's waves a part each; no
+// bytes: zeros. (Not through global_load_lds: with those in flight the compiler
+// waits for all reads of LDS at each use of one.)
+template <int REGION, int WAVES>
+__device__ __forceinline__ void copy_in(uint8_t* dst, const uint8_t* src, int bytes, int wave) {
+  constexpr int PIECES = REGION / 16, EACH = WAVES * 64;
   const rsrc_t rs = make_rsrc(src, (uint32_t)bytes);
-  for (int i = wave * 64; i < bytes / 16; i += 64 * PR_WAVES)
-    if (i + lane < bytes / 16)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(dst + 16 * i), 16, (i + lane) * 16, 0, 0, 0);
+  const int piece = threadIdx.x;
+#pragma unroll
+  for (int t = 0; t < (PIECES + EACH - 1) / EACH; ++t)
+    if ((t + 1) * EACH <= PIECES || t * EACH + piece < PIECES)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(dst + (t * EACH + wave * 64) * 16), 16, piece * 16,
+                                               t * EACH * 16, 0, 0);
 }
 
-template <int QT, bool Q8, int DB, int NC>
-__global__ __launch_bounds__(64 * PR_WAVES) void k_attn_prompt(AttnArgs a) {
-  typedef PromptShape<Q8, DB, NC> Sh;
-  constexpr int D = 32 * DB, VT = Q8 ? A_BF16 : QT;
+template <int QT, bool Q8, int DB, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void k_attn_prompt(AttnArgs a) {
+  typedef Prompt<Q8, DB, WAVES> Sh;
+  constexpr int D = 32 * DB, VT = Q8 ? A_BF16 : QT, PP = Sh::PP;
+  constexpr float SHIFT = VT == A_F16 ? 7.0f : 0.0f;   // fp16 weights up to 2^SHIFT: fewer fall below its normal range
   extern __shared__ u32x4 lds4[];
-  uint8_t* lds = reinterpret_cast<uint8_t*>(lds4);
+  uint8_t* kring = reinterpret_cast<uint8_t*>(lds4);
+  uint8_t* vring = kring + Sh::RING * Sh::STEP;
 
   const Part p = part_of(a.b, a.w, blockIdx.x);
   if (p.s < 0) return;
@@ -62,286 +82,412 @@ __global__ __launch_bounds__(64 * PR_WAVES) void k_attn_prompt(AttnArgs a) {
   const int p0 = first + p.chunk * base + min(p.chunk, rest), p1 = p0 + base + (p.chunk < rest ? 1 : 0);
 
   // the wave's columns
-  const int wcol = col0 + wave * 32 * NC;
+  const int wcol = col0 + wave * 32;
   const bool works = wcol < cols;
-  const int from = start + wcol / G, to = start + (min(cols, wcol + 32 * NC) - 1) / G;   // positions
-  u32x4 qf[NC][2 * DB];
-  int at[NC];
-  const bool qwide = wide_rows(a.q, a.ldq);
-#pragma unroll
-  for (int n = 0; n < NC; ++n) {
-    const int col = wcol + 32 * n + r;
-    const bool have = col < cols;
-    const int i = have ? col / G : 0, h = p.head * G + (have ? col - i * G : 0);
-    at[n] = have ? start + i : -1;
-    const uint16_t* q = a.q + (int64_t)(p.seq.begin + i) * a.ldq + (int64_t)h * D + 8 * H;
+  const int from = start + wcol / G, to = start + (min(cols, wcol + 32) - 1) / G;   // positions
+  const int col = wcol + r;
+  const bool have = col < cols;
+  const int token = have ? col / G : 0, qhead = p.head * G + (have ? col - token * G : 0);
+  const int at = have ? start + token : -1;
+  u32x4 qf[2 * DB];
+  {
+    const bool wide = wide_rows(a.q, a.ldq);
+    const uint16_t* q = a.q + (int64_t)(p.seq.begin + token) * a.ldq + (int64_t)qhead * D + 8 * H;
 #pragma unroll
     for (int c = 0; c < 2 * DB; ++c) {
-      qf[n][c] = row_piece(q + 16 * c, qwide);
-      if (!have) qf[n][c] = u32x4{0u, 0u, 0u, 0u};
+      qf[c] = row_piece(q + 16 * c, wide);
+      if (!have) qf[c] = u32x4{0u, 0u, 0u, 0u};
     }
   }
 
-  v16f o[NC][DB];
-  float m[NC], l[NC];
+  v16f o[DB], s[PP];
+  u32x4 pf[Q8 ? 1 : PP][2];      // packed weights (Q8_0: s itself holds them)
+  uint32_t seen = 0xffffffffu;   // what the lane's column sees of a step: bit 16 g + 8 h + element of operand h
+  float m = -__builtin_inff(), l = 0.0f;
+  bool poison = false;           // infinities or NaN were left out of V
 #pragma unroll
-  for (int n = 0; n < NC; ++n) {
-    m[n] = -__builtin_inff();
-    l[n] = 0.0f;
-#pragma unroll
-    for (int d = 0; d < DB; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[n][d][i] = 0.0f;
-  }
+  for (int d = 0; d < DB; ++d) o[d] = zero16();
 
-  // where the lane's operands lie in a region: row r of a K tile is key
-  // 16 (r / 16) + 8 (r / 4 % 2) + 4 (r / 8 % 2) + r % 4, so that register i of
-  // lane half H holds key 16 (i / 8) + 8 H + i % 8
-  const int krow = (4 * (2 * (r >> 4) + ((r >> 2) & 1)) + (r & 3)), kt = (r >> 3) & 1;
-  const int k_at = Q8 ? (H * 16 + krow) * 16 + kt * 8 : (kt * 64 + H * 16 + krow) * 16;
-  const int v_at = Q8 ? (H * 16 + (r & 15)) * 16 + (r >> 4) * 8 : ((r >> 4) * 64 + H * 16 + (r & 15)) * 16;
-
-  const auto k_operand = [&](const uint8_t* region, int c) {   // 16 channels
+  // Where the lane's operands lie in a region. Row r of a K tile is piece row
+  // r % 16 of tile r / 16, so 16 lanes read 256 bytes in a row; register i of
+  // lane half H then holds key 16 (i / 4 % 2) + 8 H + 4 (i / 8) + i % 4, and
+  // registers 4 h .. and 8 + 4 h .. are the 8 keys of the second product's
+  // operand h.
+  const int at_lds = Q8 ? (H * 16 + (r & 15)) * 16 + (r >> 4) * 8 : ((r >> 4) * 64 + H * 16 + (r & 15)) * 16;
+  // 16 channels of K; 32 channels and 16 keys of V
+  const auto k_operand = [&](const uint8_t* region, int c) INLINE {
     if constexpr (Q8) {
-      const u32x2v e = *reinterpret_cast<const u32x2v*>(region + k_at + (c >> 1) * 1024 + (c & 1) * 512);
+      const u32x2v e = *reinterpret_cast<const u32x2v*>(region + at_lds + (c >> 1) * 1024 + (c & 1) * 512);
       return codes16<QT>(e[0], e[1]);
     } else {
-      return *reinterpret_cast<const u32x4*>(region + k_at + (c >> 1) * 2048 + (c & 1) * 512);
+      return *reinterpret_cast<const u32x4*>(region + at_lds + (c >> 1) * 2048 + (c & 1) * 512);
     }
   };
-  const auto v_operand = [&](const uint8_t* region, int d, int s) {   // 32 channels, 16 keys
+  const auto v_operand = [&](const uint8_t* region, int d, int h) INLINE {
     if constexpr (Q8) {
-      const u32x2v e = *reinterpret_cast<const u32x2v*>(region + v_at + d * 1024 + s * 512);
+      const u32x2v e = *reinterpret_cast<const u32x2v*>(region + at_lds + d * 1024 + h * 512);
       return codes16<VT>(e[0], e[1]);
     } else {
-      return *reinterpret_cast<const u32x4*>(region + v_at + d * 2048 + s * 512);
+      return *reinterpret_cast<const u32x4*>(region + at_lds + d * 2048 + h * 512);
     }
   };
 
-  const auto step = [&](const uint8_t* stage, int page, const int32_t (&id)[PR_PAGES], auto masked_) {
-    constexpr bool MASKED = decltype(masked_)::value;
-    v16f s[NC][PR_PAGES];
+  // s = scores of a step (16-bit caches): f[first] holds the first page's
+  // operands. Operands are read 2 DB ahead of their products, one read behind each
+  // matrix instruction: left to itself the compiler reads each one just before its
+  // use and waits for it.
+  const auto score_products = [&](u32x4 (&f)[2][2 * DB], int first, const uint8_t* stage) INLINE {
 #pragma unroll
-    for (int g = 0; g < PR_PAGES; ++g) {
-      const uint8_t* region = stage + g * Sh::REGION;
+    for (int g = 0; g < PP; ++g) {
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int n = 0; n < NC; ++n)
+      for (int c = 0; c < 2 * DB; ++c) {
+        if (g + 1 < PP) f[(first + g + 1) & 1][c] = k_operand(stage + (g + 1) * Sh::REGION, c);
+        s[g] = mfma32<QT>(f[(first + g) & 1][c], qf[c], c == 0 ? zero16() : s[g]);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                   // a matrix instruction
+        if (g + 1 < PP) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // a read from LDS
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // s = scores of a step.
+  const auto scores = [&](const uint8_t* stage) INLINE {
+    if constexpr (Q8) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[n][g][i] = 0.0f;
-      if constexpr (Q8) {
+      for (int g = 0; g < PP; ++g) {
+        const uint8_t* region = stage + g * Sh::REGION;
         const u32x4* scales = reinterpret_cast<const u32x4*>(region + 32 * D);
+        s[g] = zero16();
 #pragma unroll
         for (int b = 0; b < DB; ++b) {
           const u32x4 k0 = k_operand(region, 2 * b), k1 = k_operand(region, 2 * b + 1);
           const u32x4 sc[2] = {scales[4 * b + H], scales[4 * b + 2 + H]};
-#pragma unroll
-          for (int n = 0; n < NC; ++n) {
-            v16f d;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) d[i] = 0.0f;
-            d = mfma32<QT>(k0, qf[n][2 * b], d);
-            d = mfma32<QT>(k1, qf[n][2 * b + 1], d);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint32_t w = sc[i >> 3][(i & 7) >> 1];
-              s[n][g][i] = __builtin_fmaf(h2f(i & 1 ? w >> 16 : w), d[i], s[n][g][i]);
-            }
-          }
-        }
-      } else {
-#pragma unroll
-        for (int c = 0; c < 2 * DB; ++c) {
-          const u32x4 k = k_operand(region, c);
-#pragma unroll
-          for (int n = 0; n < NC; ++n) s[n][g] = mfma32<QT>(k, qf[n][c], s[n][g]);
-        }
-      }
-    }
-    uint32_t seen[NC];   // bit 16 g + i
-#pragma unroll
-    for (int n = 0; n < NC; ++n) {
-      seen[n] = 0xffffffffu;
-      if constexpr (MASKED) {
-        seen[n] = 0;
-#pragma unroll
-        for (int g = 0; g < PR_PAGES; ++g)
+          const v16f d = mfma32<QT>(k1, qf[2 * b + 1], mfma32<QT>(k0, qf[2 * b], zero16()));
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int key = (page + g) * PAGE + 16 * (i >> 3) + 8 * H + (i & 7);
-            bool ok = key <= at[n] && (a.w.window <= 0 || key > at[n] - a.w.window);
-            if (id[g] == -2) ok = true;
-            if (id[g] == -3) ok = false;
-            seen[n] |= (ok ? 1u : 0u) << (16 * g + i);
-            s[n][g][i] = !ok ? -__builtin_inff() : id[g] < 0 ? __builtin_nanf("") : s[n][g][i];
+            const uint32_t w = sc[(i >> 2) & 1][2 * (i >> 3) + ((i & 3) >> 1)];
+            s[g][i] = __builtin_fmaf(h2f(i & 1 ? w >> 16 : w), d[i], s[g][i]);
+          }
+        }
+      }
+    } else {
+      u32x4 f[2][2 * DB];
+#pragma unroll
+      for (int c = 0; c < 2 * DB; ++c) f[0][c] = k_operand(stage, c);
+      score_products(f, 0, stage);
+    }
+  };
+
+  // Masks of a step that not every column sees whole.
+  const auto mask = [&](int page, const int32_t (&id)[PP]) INLINE {
+    seen = 0;
+#pragma unroll
+    for (int g = 0; g < PP; ++g)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int j = 8 * ((i >> 2) & 1) + 4 * (i >> 3) + (i & 3);   // its place in the second product's operands
+        const int key = (page + g) * PAGE + 2 * (j & 8) + 8 * H + (j & 7);
+        bool ok = key <= at && (a.w.window <= 0 || key > at - a.w.window);
+        if (id[g] == -2) ok = true;
+        if (id[g] == -3) ok = false;
+        seen |= (ok ? 1u : 0u) << (16 * g + j);
+        s[g][i] = !ok ? -__builtin_inff() : id[g] < 0 ? __builtin_nanf("") : s[g][i];
+      }
+  };
+
+  // Scores to weights; o to the new m.
+  const auto weigh = [&]() INLINE {
+    float top = s[0][0];
+#pragma unroll
+    for (int g = 0; g < PP; ++g)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[g][i]);
+    top = max_lane_xor32(top);
+    top = __builtin_fmaf(top, a.scale, -SHIFT);   // scale > 0
+    // always: a branch around it cost more than it saved
+    const float now = fmaxf(m, top), by = m == now ? 1.0f : exp2_fast(m - now);
+    m = now;
+    l *= by;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[d][i] *= by;
+    const float sub = m == -__builtin_inff() ? 0.0f : m;
+#pragma unroll
+    for (int g = 0; g < PP; ++g) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[g][i] = exp2_fast(__builtin_fmaf(s[g][i], a.scale, -sub));
+      if constexpr (Q8) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) l += s[g][i];
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int i = 8 * (j >> 1) + 4 * h + 2 * (j & 1);
+            pf[g][h][j] = pack2<VT>(s[g][i], s[g][i + 1]);
+            // the sum is of the rounded weights: where one weight is most of it,
+            // its rounding leaves the quotient again
+            l = add_pair<VT>(pf[g][h][j], l);
           }
       }
-      float top = s[n][0][0];
-#pragma unroll
-      for (int g = 0; g < PR_PAGES; ++g)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[n][g][i]);
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
-      top *= a.scale;   // scale > 0
-      if (__any(top > m[n])) {
-        const float now = fmaxf(m[n], top), by = m[n] == now ? 1.0f : exp2_fast(m[n] - now);
-        m[n] = now;
-        l[n] *= by;
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[n][d][i] *= by;
-      }
-      const float sub = m[n] == -__builtin_inff() ? 0.0f : m[n];
-#pragma unroll
-      for (int g = 0; g < PR_PAGES; ++g)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          s[n][g][i] = exp2_fast(__builtin_fmaf(s[n][g][i], a.scale, -sub));
-          l[n] += s[n][g][i];
-        }
     }
+  };
+
+  // o += V^T P^T of a step.
+  const auto add_v = [&](const uint8_t* stage, auto masked_) INLINE {
+    constexpr bool MASKED = decltype(masked_)::value;
+    if constexpr (Q8) {
+      // The scale of V's block goes to the weight, in two parts of 8 bits (bf16 has
+      // the range of the scales); the codes stay whole numbers.
 #pragma unroll
-    for (int g = 0; g < PR_PAGES; ++g) {
-      const uint8_t* region = stage + (PR_PAGES + g) * Sh::REGION;
-      if constexpr (Q8) {
+      for (int g = 0; g < PP; ++g) {
+        const uint8_t* region = stage + g * Sh::REGION;
         const u32x4* scales = reinterpret_cast<const u32x4*>(region + 32 * D);
 #pragma unroll
         for (int b = 0; b < DB; ++b) {
           const u32x4 sc[2] = {scales[4 * b + H], scales[4 * b + 2 + H]};
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const u32x4 v = v_operand(region, b, h);
+            const u32x4 vf = v_operand(region, b, h);
+            u32x4 hi, lo;
 #pragma unroll
-            for (int n = 0; n < NC; ++n) {
-              u32x4 hi, lo;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const uint32_t w = sc[h][j];
-                const int i = 8 * h + 2 * j;
-                // a masked key's scale may be NaN
-                const float e0 = !MASKED || (seen[n] >> (16 * g + i) & 1) ? s[n][g][i] * h2f(w) : 0.0f;
-                const float e1 = !MASKED || (seen[n] >> (16 * g + i + 1) & 1) ? s[n][g][i + 1] * h2f(w >> 16) : 0.0f;
-                uint32_t x, y;
-                split2<VT>(e0, e1, x, y);
-                hi[j] = x;
-                lo[j] = y;
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t w = sc[h][j];
+              const int i = 8 * (j >> 1) + 4 * h + 2 * (j & 1), bit = 16 * g + 8 * h + 2 * j;
+              float e0 = s[g][i] * h2f(w), e1 = s[g][i + 1] * h2f(w >> 16);
+              if constexpr (MASKED) {   // a masked key's scale may be NaN
+                e0 = seen >> bit & 1 ? e0 : 0.0f;
+                e1 = seen >> bit & 2 ? e1 : 0.0f;
               }
-              o[n][b] = mfma32<VT>(v, hi, o[n][b]);
-              o[n][b] = mfma32<VT>(v, lo, o[n][b]);
+              uint32_t x, y;
+              split2<VT>(e0, e1, x, y);
+              hi[j] = x;
+              lo[j] = y;
+            }
+            o[b] = mfma32<VT>(vf, hi, o[b]);
+            o[b] = mfma32<VT>(vf, lo, o[b]);
+          }
+        }
+      }
+    } else {
+      // Infinities and NaN of keys that a column does not see must not reach it
+      // (0 times them is NaN): they are left out here and added at the end.
+#pragma unroll
+      for (int g = 0; g < PP; ++g) {
+        u32x4 v[2 * DB];
+#pragma unroll
+        for (int c = 0; c < 2 * DB; ++c) v[c] = v_operand(stage + g * Sh::REGION, c % DB, c / DB);
+        if constexpr (MASKED) {
+          bool bad = false;
+#pragma unroll
+          for (int c = 0; c < 2 * DB; ++c) bad |= any_not_finite<VT>(v[c]);
+          if (__any(bad)) {
+            poison = true;
+#pragma unroll
+            for (int c = 0; c < 2 * DB; ++c) {
+              u32x4 plus, minus;
+              v[c] = take_finite<VT>(v[c], plus, minus);
             }
           }
         }
+#pragma unroll
+        for (int c = 0; c < 2 * DB; ++c) o[c % DB] = mfma32<VT>(v[c], pf[g][c / DB], o[c % DB]);
+      }
+    }
+  };
+
+  // The matrix instructions of a step between steps that need no masks, V of
+  // the step before first (its weights make room for the scores). The first
+  // operands of V were read in the phase before.
+  u32x4 ahead[Q8 ? 1 : 2 * DB];
+  const auto read_ahead = [&](const uint8_t* stage) INLINE {
+    if constexpr (!Q8) {
+#pragma unroll
+      for (int c = 0; c < 2 * DB; ++c) ahead[c] = v_operand(stage, c % DB, c / DB);
+    }
+  };
+  const auto products = [&](const uint8_t* kstage, const uint8_t* vstage) INLINE {
+    if constexpr (Q8) {
+      add_v(vstage, Flag<false>());
+      scores(kstage);
+    } else {
+      u32x4 f[2][2 * DB];
+#pragma unroll
+      for (int c = 0; c < 2 * DB; ++c) f[0][c] = ahead[c];
+#pragma unroll
+      for (int g = 0; g < PP; ++g) {
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int c = 0; c < 2 * DB; ++c) {
+          f[(g + 1) & 1][c] = g + 1 < PP ? v_operand(vstage + (g + 1) * Sh::REGION, c % DB, c / DB) : k_operand(kstage, c);
+          o[c % DB] = mfma32<VT>(f[g & 1][c], pf[g][c / DB], o[c % DB]);
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+      }
+      score_products(f, PP & 1, kstage);
+    }
+  };
+
+  const int steps = (p1 - p0 + PP - 1) / PP;
+  if (steps > 0) {
+    // Where the regions of 64 steps' pages begin, held by the lanes, from step
+    // held_from on (the cache's first region stands in for pages that there are
+    // none of: any_bad says that there was one).
+    int64_t held[PP];
+    int held_from = 0;
+    bool any_bad = false;
+    const auto fill = [&](int from_step) INLINE {
+#pragma unroll
+      for (int g = 0; g < PP; ++g) {
+        const int64_t page = (int64_t)p0 + (int64_t)(from_step + lane) * PP + g;
+        const int32_t id = page >= p1 ? 0 : page_id(a.b, a.c.n_pages, p.s, (int)page);
+        any_bad |= __any(id < 0);
+        held[g] = ((int64_t)max(id, 0) * a.c.kv_heads + p.head) * Sh::REGION;
+      }
+      held_from = from_step;
+    };
+    struct Step {
+      int64_t at[PP];
+    };
+    const auto step_at = [&](int i) INLINE {
+      Step st;
+#pragma unroll
+      for (int g = 0; g < PP; ++g)
+        st.at[g] = (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)held[g], i - held_from) |
+                   (int64_t)__builtin_amdgcn_readlane((int)(held[g] >> 32), i - held_from) << 32;
+      return st;
+    };
+    const auto copy_step = [&](uint8_t* stage, const uint8_t* plane, const Step& st, int i) INLINE {
+#pragma unroll
+      for (int g = 0; g < PP; ++g)
+        copy_in<Sh::REGION, WAVES>(stage + g * Sh::REGION, plane + st.at[g], p0 + i * PP + g < p1 ? Sh::REGION : 0, wave);
+    };
+    fill(0);
+    // Barriers of their own: __syncthreads would wait for every copy in flight.
+    // A phase's arithmetic stays in it.
+    const auto phase_ends = [] {
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("s_barrier" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    // This wave's copies have landed (they are loads to the compiler).
+    const auto copies_landed = [] { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); };
+    const Step st0 = step_at(0);
+    Step st1 = step_at(1), st2 = step_at(2);
+    copy_step(kring, a.c.k, st0, 0);
+    copy_step(vring, a.c.v, st0, 0);
+    copy_step(kring + Sh::STEP, a.c.k, st1, 1);
+    copies_landed();
+    phase_ends();
+    const bool behind = WAVES == 8 && wave >= 4;
+    if (behind) phase_ends();
+    int now = 0, i = 0;   // step, and its place in both rings
+    bool had = false, had_mask = false;
+    // pages that every column sees whole: a step of them needs no masks
+    const int whole_from = a.w.window > 0 ? max((to - a.w.window + PAGE) / PAGE, 0) : 0;
+    const int whole_to = works ? min(p1, (from + 1) / PAGE) : 0;
+    const auto whole = [&]() INLINE { return p0 + i * PP >= whole_from && p0 + (i + 1) * PP <= whole_to && !any_bad; };
+    const auto walk = [&](auto fast) INLINE {
+      const int next = now == 2 ? 0 : now + 1, last = now == 0 ? 2 : now - 1;
+      copy_step(kring + last * Sh::STEP, a.c.k, st2, i + 2);
+      copy_step(vring + next * Sh::STEP, a.c.v, st1, i + 1);
+      if constexpr (decltype(fast)::value) {
+        products(kring + now * Sh::STEP, vring + last * Sh::STEP);
+        phase_ends();
+        weigh();
+        read_ahead(vring + now * Sh::STEP);
       } else {
-        u32x4 pf[NC][2];
+        const int page = p0 + i * PP;
+        int32_t id[PP];
 #pragma unroll
-        for (int n = 0; n < NC; ++n)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) pf[n][h][j] = pack2<VT>(s[n][g][8 * h + 2 * j], s[n][g][8 * h + 2 * j + 1]);
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            u32x4 v = v_operand(region, d, h);
-            if constexpr (MASKED) {
-              if (__any(any_not_finite<VT>(v))) {
-                // infinities and NaN of keys that a column does not see must not
-                // reach it: the finite part is multiplied, and what a column sees
-                // of the rest is counted and added as it is
-                u32x4 plus, minus;
-                v = take_finite<VT>(v, plus, minus);
-                constexpr uint32_t ONE = VT == A_F16 ? 0x3c00u : 0x3f80u;
-#pragma unroll
-                for (int n = 0; n < NC; ++n) {
-                  u32x4 one;
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    const uint32_t w = seen[n] >> (16 * g + 8 * h + 2 * j);
-                    one[j] = (w & 1 ? ONE : 0u) | (w & 2 ? ONE << 16 : 0u);
-                  }
-                  v16f zero;
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) zero[i] = 0.0f;
-                  const v16f up = mfma32<VT>(plus, one, zero), down = mfma32<VT>(minus, one, zero);
-#pragma unroll
-                  for (int i = 0; i < 16; ++i)
-                    o[n][d][i] += (up[i] > 0.0f ? __builtin_inff() : 0.0f) + (down[i] > 0.0f ? -__builtin_inff() : 0.0f);
-                }
-              }
-            }
-#pragma unroll
-            for (int n = 0; n < NC; ++n) o[n][d] = mfma32<VT>(v, pf[n][h], o[n][d]);
-          }
+        for (int g = 0; g < PP; ++g)
+          id[g] = page + g >= p1 ? -3 : any_bad ? scalar(page_id(a.b, a.c.n_pages, p.s, page + g)) : 0;
+        const bool beyond = page * PAGE > to || (a.w.window > 0 && (page + PP) * PAGE <= from - a.w.window + 1);
+        const bool does = works && (!beyond || id[0] == -2), unmasked = whole();
+        // (what needs no masks may be taken for what does)
+        if (had) add_v(vring + last * Sh::STEP, Flag<true>());
+        if (does) scores(kring + now * Sh::STEP);
+        phase_ends();
+        if (does) {
+          seen = 0xffffffffu;
+          if (!unmasked) mask(page, id);
+          weigh();
+          read_ahead(vring + now * Sh::STEP);
+        }
+        had = does;
+        had_mask = !unmasked;
       }
+      // the next step's pages in this phase: these reads of lanes would queue behind
+      // the other wave's arithmetic in the next one
+      st1 = st2;
+      if constexpr (!decltype(fast)::value)
+        if (i + 3 - held_from > 63) fill(i + 3);
+      st2 = step_at(i + 3);
+      copies_landed();
+      phase_ends();
+      now = next;
+      ++i;
+    };
+    while (i < steps) {
+      if (had && !had_mask && whole()) {
+        // as far as steps are whole, and before the one that moves on to the next 64
+        const int end = min((whole_to - p0) / PP, held_from + 61);
+        while (i < end) walk(Flag<true>());
+      }
+      if (i < steps) walk(Flag<false>());
     }
-  };
-
-  const auto ids_at = [&](int page, int32_t (&id)[PR_PAGES]) {
-#pragma unroll
-    for (int g = 0; g < PR_PAGES; ++g)
-      id[g] = page + g < p1 ? scalar(page_id(a.b, a.c.n_pages, p.s, page + g)) : -3;
-  };
-  const auto copy_step = [&](uint8_t* stage, const int32_t (&id)[PR_PAGES]) {
-#pragma unroll
-    for (int g = 0; g < PR_PAGES; ++g) {
-      if (id[g] == -3) continue;
-      const int64_t off = ((int64_t)(id[g] < 0 ? 0 : id[g]) * a.c.kv_heads + p.head) * Sh::REGION;
-      copy_in(stage + g * Sh::REGION, a.c.k + off, Sh::REGION);
-      copy_in(stage + (PR_PAGES + g) * Sh::REGION, a.c.v + off, Sh::REGION);
-    }
-  };
-
-  if (p0 < p1) {
-    int32_t id[PR_PAGES], next[PR_PAGES];
-    ids_at(p0, id);
-    ids_at(p0 + PR_PAGES, next);
-    copy_step(lds, id);
-    int buf = 0;
-    for (int page = p0; page < p1; page += PR_PAGES) {
-      // this step's copies have landed (they are loads to the compiler), and
-      // every wave is done with the other buffer
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();
-      int32_t after[PR_PAGES];
-      ids_at(page + 2 * PR_PAGES, after);
-      if (page + PR_PAGES < p1) copy_step(lds + (buf ^ 1) * Sh::STAGE, next);
-      const bool beyond = page * PAGE > to || (a.w.window > 0 && (page + PR_PAGES) * PAGE <= from - a.w.window + 1);
-      bool whole = (page + PR_PAGES) * PAGE - 1 <= from && (a.w.window <= 0 || page * PAGE > to - a.w.window);
-#pragma unroll
-      for (int g = 0; g < PR_PAGES; ++g) whole &= id[g] >= 0;
-      if (works && whole) step(lds + buf * Sh::STAGE, page, id, Flag<false>());
-      else if (works && (!beyond || id[0] == -2)) step(lds + buf * Sh::STAGE, page, id, Flag<true>());
-#pragma unroll
-      for (int g = 0; g < PR_PAGES; ++g) id[g] = next[g], next[g] = after[g];
-      buf ^= 1;
-    }
+    if (WAVES == 8 && !behind) phase_ends();
+    if (had) add_v(vring + (now == 0 ? 2 : now - 1) * Sh::STEP, Flag<true>());
   }
-  if (!works) return;
 
-  const bool owide = wide_rows(a.out, a.ldo);
+  if constexpr (!Q8) {
+    if (poison) {
+      // What was left out of V: a column that sees plus and minus infinity, or
+      // NaN, gets NaN, whatever the weights (they are above 0).
+      constexpr uint32_t ONE = VT == A_F16 ? 0x3c00u : 0x3f80u;
+      for (int page = p0; page < p1; ++page) {
+        const int32_t id = scalar(page_id(a.b, a.c.n_pages, p.s, page));
+        if (id < 0) continue;
+        const uint8_t* region = a.c.v + ((int64_t)id * a.c.kv_heads + p.head) * Sh::REGION;
+        for (int h = 0; h < 2; ++h) {
+          u32x4 one = {0u, 0u, 0u, 0u};
 #pragma unroll
-  for (int n = 0; n < NC; ++n) {
-    l[n] += __shfl_xor(l[n], 32, 64);
-    const int in_tile = wave * 32 * NC + 32 * n + r, col = col0 + in_tile;
-    if (col >= cols) continue;
-    const int64_t row = (int64_t)p.slot * Sh::TILE + in_tile;
-    if (p.chunks > 1 && H == 0) a.ml[row] = float2{m[n], l[n]};
-    const int tok = col / G, h = p.head * G + col % G;
-    uint16_t* out = a.out + (int64_t)(p.seq.begin + tok) * a.ldo + (int64_t)h * D + 4 * H;
+          for (int j = 0; j < 8; ++j) {
+            const int key = page * PAGE + 16 * h + 8 * H + j;
+            if (key <= at && (a.w.window <= 0 || key > at - a.w.window)) one[j / 2] |= ONE << (16 * (j & 1));
+          }
 #pragma unroll
-    for (int d = 0; d < DB; ++d)
+          for (int d = 0; d < DB; ++d) {
+            u32x4 plus, minus;
+            take_finite<VT>(v_operand(region, d, h), plus, minus);
+            const v16f up = mfma32<VT>(plus, one, zero16()), down = mfma32<VT>(minus, one, zero16());
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v4f v = {o[n][d][4 * e], o[n][d][4 * e + 1], o[n][d][4 * e + 2], o[n][d][4 * e + 3]};
-        if (p.chunks > 1) {
-          *reinterpret_cast<v4f*>(a.part + row * D + 32 * d + 8 * e + 4 * H) = v;
-        } else {
-          v = l[n] == 0.0f ? v4f{0.f, 0.f, 0.f, 0.f} : v / l[n];
-          put_4<QT>(out + 32 * d + 8 * e, owide, v);
+            for (int i = 0; i < 16; ++i)
+              o[d][i] += (up[i] > 0.0f ? __builtin_inff() : 0.0f) + (down[i] > 0.0f ? -__builtin_inff() : 0.0f);
+          }
         }
       }
+    }
   }
+
+  l += __shfl_xor(l, 32, 64);
+  if (!have) return;
+  const int64_t row = (int64_t)p.slot * Sh::TILE + wave * 32 + r;
+  if (p.chunks > 1 && H == 0) a.ml[row] = float2{m, l};
+  const bool wide = wide_rows(a.out, a.ldo);
+  uint16_t* out = a.out + (int64_t)(p.seq.begin + token) * a.ldo + (int64_t)qhead * D + 4 * H;
+  const float by = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v4f v = {o[d][4 * e], o[d][4 * e + 1], o[d][4 * e + 2], o[d][4 * e + 3]};
+      if (p.chunks > 1) *reinterpret_cast<v4f*>(a.part + row * D + 32 * d + 8 * e + 4 * H) = v;
+      else put_4<QT>(out + 32 * d + 8 * e, wide, l == 0.0f ? v4f{0.f, 0.f, 0.f, 0.f} : v * by);
+    }
 }
 
 }  // namespace kqd
@@ -351,28 +497,32 @@ using namespace kqd;
 
 namespace {
 
-template <int QT, bool Q8, int DB, int NC>
+template <int QT, bool Q8, int DB, int WAVES>
 int prompt_launch(const AttnCall& p, const AttnPlan& w) {
-  typedef PromptShape<Q8, DB, NC> Sh;
+  typedef Prompt<Q8, DB, WAVES> Sh;
   const AttnArgs a = attn_args(p, w);
-  dispatch_log("k_attn_prompt", -1, p.heads, 32 * DB, p.batch->n_tokens, (unsigned)w.grid, 1, 64 * PR_WAVES, 2 * Sh::STAGE,
+  dispatch_log("k_attn_prompt", -1, p.heads, 32 * DB, p.batch->n_tokens, (unsigned)w.grid, 1, 64 * WAVES, Sh::LDS,
                "cache=%d tile=%d slots=%lld", p.cache->type, w.tile, (long long)w.slots);
-  hipLaunchKernelGGL((k_attn_prompt<QT, Q8, DB, NC>), dim3((unsigned)w.grid), dim3(64 * PR_WAVES), 2 * Sh::STAGE, p.stream, a);
+  hipLaunchKernelGGL((k_attn_prompt<QT, Q8, DB, WAVES>), dim3((unsigned)w.grid), dim3(64 * WAVES), Sh::LDS, p.stream, a);
   int err = (int)hipGetLastError();
   if (err || w.slots == 0) return err;
   return launch_attn_join(a, p.type, 32 * DB, p.stream);
 }
+template <int QT, bool Q8, int DB>
+int prompt_tile(const AttnCall& p, const AttnPlan& w) {
+  return w.tile == 128 ? prompt_launch<QT, Q8, DB, 4>(p, w) : prompt_launch<QT, Q8, DB, 8>(p, w);
+}
 template <int QT, bool Q8>
 int prompt_dim(const AttnCall& p, const AttnPlan& w) {
   switch (p.cache->head_dim / 32) {
-    case 1: return prompt_launch<QT, Q8, 1, 1>(p, w);
-    case 2: return prompt_launch<QT, Q8, 2, 1>(p, w);
-    case 3: return prompt_launch<QT, Q8, 3, 1>(p, w);
-    case 4: return prompt_launch<QT, Q8, 4, 1>(p, w);
-    case 5: return prompt_launch<QT, Q8, 5, 1>(p, w);
-    case 6: return prompt_launch<QT, Q8, 6, 1>(p, w);
-    case 7: return prompt_launch<QT, Q8, 7, 1>(p, w);
-    default: return prompt_launch<QT, Q8, 8, 1>(p, w);
+    case 1: return prompt_tile<QT, Q8, 1>(p, w);
+    case 2: return prompt_tile<QT, Q8, 2>(p, w);
+    case 3: return prompt_tile<QT, Q8, 3>(p, w);
+    case 4: return prompt_tile<QT, Q8, 4>(p, w);
+    case 5: return prompt_tile<QT, Q8, 5>(p, w);
+    case 6: return prompt_tile<QT, Q8, 6>(p, w);
+    case 7: return prompt_tile<QT, Q8, 7>(p, w);
+    default: return prompt_tile<QT, Q8, 8>(p, w);
   }
 }
 
@@ -380,8 +530,11 @@ int prompt_dim(const AttnCall& p, const AttnPlan& w) {
 
 AttnPlan prompt_plan(const kq_kv_cache& c, const kq_kv_batch& b, int heads) {
   AttnPlan w;
-  w.tile = 128;
-  w.target = 512;
+  // Tiles of 256 columns for sequences of many: 8 waves share what is read and
+  // two of them a SIMD. Sequences of a few hundred columns fill smaller ones better.
+  const int64_t cols = (int64_t)b.n_tokens * (heads / c.kv_heads) / b.n_seqs;   // of a mean sequence
+  w.tile = cols >= 1024 ? 256 : 128;
+  w.target = 256;
   w.least = 16;
   finish_plan(c, b, heads, w);
   return w;

@@ -89,6 +89,23 @@ __device__ __forceinline__ int32_t page_id(const Batch& b, int64_t n_pages, int 
   return id >= 0 && id < n_pages ? id : -1;
 }
 
+// The ids of a sequence's pages from `first` on, every `step`-th, 64 of them held
+// by the lanes of a wave: the walks take one after the other without waiting for
+// the table. Called by whole waves.
+struct PageIds {
+  int32_t held;
+  int from;   // the pages' index of lane 0's
+  __device__ __forceinline__ void fill(const Batch& b, int64_t n_pages, int s, int first, int step, int index) {
+    const int64_t page = first + (int64_t)(index + (int)(threadIdx.x & 63)) * step;
+    held = page > b.width ? -2 : page_id(b, n_pages, s, (int)page);
+    from = index;
+  }
+  __device__ __forceinline__ int32_t at(const Batch& b, int64_t n_pages, int s, int first, int step, int index) {
+    if (index - from >= 64) fill(b, n_pages, s, first, step, index);
+    return __builtin_amdgcn_readlane(held, index - from);
+  }
+};
+
 // What a wave wrote to LDS is seen by all its lanes from here on.
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -96,16 +113,23 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Inclusive sum over the lanes of a wave.
-__device__ __forceinline__ int64_t wave_scan(int64_t v) {
-  const int lane = threadIdx.x & 63;
-  for (int o = 1; o < 64; o *= 2) {
-    const int64_t u = __shfl_up(v, o, 64);
-    if (lane >= o) v += u;
-  }
+__device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Inclusive sum over the lanes of a wave: four shifts within rows of 16, then the
+// rows' last values carried on.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int add_shifted(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave_scan(int v) {
+  v = add_shifted<0x111, 0xF>(v);   // row_shr:1
+  v = add_shifted<0x112, 0xF>(v);
+  v = add_shifted<0x114, 0xF>(v);
+  v = add_shifted<0x118, 0xF>(v);
+  v = add_shifted<0x142, 0xA>(v);   // row_bcast:15 to rows 1 and 3
+  v = add_shifted<0x143, 0xC>(v);   // row_bcast:31 to rows 2 and 3
   return v;
 }
-__device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // ---- Which part of attention a workgroup does. The columns of a sequence and
 // key-value head are its n * G queries (token by token, the G heads of a token
@@ -148,6 +172,7 @@ __device__ __forceinline__ int chunks_of(int np, int per) { return max((np + per
 
 // Pages per chunk. Called by whole waves.
 __device__ __forceinline__ int pages_per_chunk(const Batch& b, const Split& w) {
+  if (w.slots == 0) return 0x7fffffff;
   const int lane = threadIdx.x & 63;
   int64_t total = 0;
   for (int s0 = 0; s0 < b.n_seqs; s0 += 64) {
@@ -164,46 +189,48 @@ __device__ __forceinline__ int pages_per_chunk(const Batch& b, const Split& w) {
   return scalar((int)(per > 0x7fffffff ? 0x7fffffff : per));
 }
 
-// Part `id` of the grid.
+// Part `id` of the grid. Sums of parts stay below 2^31: the calls take grids
+// below 2^23, and a sum is carried on while it does not pass id.
 __device__ __forceinline__ Part part_of(const Batch& b, const Split& w, int id) {
   const int lane = threadIdx.x & 63;
   const int per = pages_per_chunk(b, w);
   Part p;
   p.s = -1;
-  int64_t before = 0, slots = 0;
+  int before = 0, slots = 0;
   for (int s0 = 0; s0 < b.n_seqs; s0 += 64) {
     const int s = s0 + lane;
-    int64_t mine = 0, split = 0;
+    Seq q{0, 0, 0};
+    int first = 0, np = 0, chunks = 1, tiles = 0;
     if (s < b.n_seqs) {
-      const Seq q = seq_of(b, s);
-      int first, np;
+      q = seq_of(b, s);
       pages_of(b, q, w.window, first, np);
-      const int chunks = chunks_of(np, per);
-      mine = (int64_t)tiles_of(w, q.n) * w.kv_heads * chunks;
-      split = chunks > 1 ? mine : 0;
+      chunks = chunks_of(np, per);
+      tiles = tiles_of(w, q.n);
     }
-    const int64_t upto = wave_scan(mine) + before, slot = wave_scan(split) + slots;
+    const int mine = tiles * w.kv_heads * chunks, split = chunks > 1 ? mine : 0;
+    const int upto = wave_scan(mine) + before, slot = wave_scan(split) + slots;
     const uint64_t hit = __ballot(id < upto);
     if (hit) {
       const int l = __ffsll((unsigned long long)hit) - 1;
+      const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
       p.s = s0 + l;
-      p.seq = seq_of(b, p.s);
-      p.seq.begin = scalar(p.seq.begin);
-      p.seq.n = scalar(p.seq.n);
-      p.seq.len = scalar(p.seq.len);
-      pages_of(b, p.seq, w.window, p.first, p.np);
-      p.chunks = chunks_of(p.np, per);
-      const int local = scalar((int)(id - __shfl(upto - mine, l, 64)));
+      p.seq = Seq{of(q.begin), of(q.n), of(q.len)};
+      p.first = of(first);
+      p.np = of(np);
+      p.chunks = of(chunks);
+      const int local = id - of(upto - mine);
       // heads next to each other: with 8 of them every tile and chunk of a head lies on one XCD
-      p.head = local % w.kv_heads;
-      p.chunk = local / w.kv_heads % p.chunks;
+      const int rest = local / w.kv_heads;
+      p.head = local - rest * w.kv_heads;
       // the last tiles first: they see the most
-      p.tile = tiles_of(w, p.seq.n) - 1 - local / w.kv_heads / p.chunks;
-      p.slot = scalar((int)(__shfl(slot - split, l, 64))) + (p.tile * p.chunks + p.chunk) * w.kv_heads + p.head;
+      const int tile = p.chunks == 1 ? rest : rest / p.chunks;
+      p.chunk = rest - tile * p.chunks;
+      p.tile = of(tiles) - 1 - tile;
+      p.slot = of(slot - split) + (p.tile * p.chunks + p.chunk) * w.kv_heads + p.head;
       return p;
     }
-    before = __shfl(upto, 63, 64);
-    slots = __shfl(slot, 63, 64);
+    before = __builtin_amdgcn_readlane(upto, 63);
+    slots = __builtin_amdgcn_readlane(slot, 63);
   }
   return p;
 }

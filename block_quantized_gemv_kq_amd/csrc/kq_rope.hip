@@ -205,24 +205,26 @@ struct Run {
 __device__ __forceinline__ Run run_of(const Batch& b, int id) {
   const int lane = threadIdx.x & 63;
   Run r{-1, 0, 0, 0};
-  int64_t before = 0;
+  int before = 0;   // at most 2^20 tokens: sums stay below 2^31
   for (int s0 = 0; s0 < b.n_seqs; s0 += 64) {
-    const int64_t mine = s0 + lane < b.n_seqs ? octets_of(seq_of(b, s0 + lane)) : 0;
-    const int64_t upto = wave_scan(mine) + before;
+    const Seq mine_of = s0 + lane < b.n_seqs ? seq_of(b, s0 + lane) : Seq{0, 0, 0};
+    const int mine = octets_of(mine_of);
+    const int upto = wave_scan(mine) + before;
     const uint64_t hit = __ballot(id < upto);
     if (hit) {
       const int l = __ffsll((unsigned long long)hit) - 1;
-      const Seq q = seq_of(b, s0 + l);
-      const int local = (int)(id - __shfl(upto - mine, l, 64));
+      const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+      const Seq q{of(mine_of.begin), of(mine_of.n), of(mine_of.len)};
+      const int local = id - of(upto - mine);
       const int first = max(q.len - q.n, 0);
       const int from = max((first / OCT + local) * OCT, first), to = min((first / OCT + local + 1) * OCT, q.len);
       r.s = s0 + l;
-      r.position = scalar(from);
-      r.n = scalar(to - from);
-      r.token = scalar(q.begin + (from - (q.len - q.n)));
+      r.position = from;
+      r.n = to - from;
+      r.token = q.begin + (from - (q.len - q.n));
       return r;
     }
-    before = __shfl(upto, 63, 64);
+    before = __builtin_amdgcn_readlane(upto, 63);
   }
   return r;
 }
