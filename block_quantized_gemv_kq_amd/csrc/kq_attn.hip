@@ -25,28 +25,21 @@ struct Page {
 };
 
 template <bool Q8, int DB>
-__device__ __forceinline__ void load_page(Page<Q8, DB>& p, const Cache& c, int32_t id, int head) {
+__device__ __forceinline__ void load_half(u32x4 (&x)[Q8 ? DB : 2 * DB], u32x4 (&scales)[Q8 ? DB : 1], const uint8_t* plane,
+                                          const Cache& c, int32_t id, int head) {
   const int lane = threadIdx.x & 63;
-  const int64_t at = ((int64_t)(id < 0 ? 0 : id) * c.kv_heads + head) * region_bytes(Q8, 32 * DB);
-  const u32x4* k = reinterpret_cast<const u32x4*>(c.k + at);
-  const u32x4* v = reinterpret_cast<const u32x4*>(c.v + at);
-  constexpr int N = Q8 ? DB : 2 * DB;
+  const u32x4* p = reinterpret_cast<const u32x4*>(
+      plane + ((int64_t)(id < 0 ? 0 : id) * c.kv_heads + head) * region_bytes(Q8, 32 * DB));
 #pragma unroll
-  for (int i = 0; i < N; ++i) p.k[i] = k[i * 64 + lane];
+  for (int i = 0; i < (Q8 ? DB : 2 * DB); ++i) x[i] = p[i * 64 + lane];
   if constexpr (Q8) {
 #pragma unroll
-    for (int i = 0; i < DB; ++i) p.ks[i] = k[64 * DB + 4 * i + (lane >> 4)];
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) p.v[i] = v[i * 64 + lane];
-  if constexpr (Q8) {
-#pragma unroll
-    for (int i = 0; i < DB; ++i) p.vs[i] = v[64 * DB + 4 * i + (lane >> 4)];
+    for (int i = 0; i < DB; ++i) scales[i] = p[64 * DB + 4 * i + (lane >> 4)];
   }
 }
 
 template <int QT, bool Q8, int DB, int CT>
-__global__ __launch_bounds__(64 * DEC_WAVES, DB * CT <= 4 ? 2 : 1) void k_attn_decode(AttnArgs a) {
+__global__ __launch_bounds__(64 * DEC_WAVES, DB * CT <= 4 || (!Q8 && DB * CT <= 8) ? 2 : 1) void k_attn_decode(AttnArgs a) {
   constexpr int D = 32 * DB, DT = 2 * DB, VT = Q8 ? A_BF16 : QT;
   // d-tiles per round of the sum over the waves: 64 KB of LDS
   constexpr int ROUND = DT * CT * DEC_WAVES <= 64 ? DT : 64 / (CT * DEC_WAVES);
@@ -96,13 +89,20 @@ __global__ __launch_bounds__(64 * DEC_WAVES, DB * CT <= 4 ? 2 : 1) void k_attn_d
 
   v4f o[CT][DT];
   float m[CT], l[CT];
+  const auto reset = [&] {
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
-    m[ct] = -__builtin_inff();
-    l[ct] = 0.0f;
+    for (int ct = 0; ct < CT; ++ct) {
+      m[ct] = -__builtin_inff();
+      l[ct] = 0.0f;
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt) o[ct][dt] = v4f{0.f, 0.f, 0.f, 0.f};
-  }
+      for (int dt = 0; dt < DT; ++dt) o[ct][dt] = v4f{0.f, 0.f, 0.f, 0.f};
+    }
+  };
+  reset();
+  // Pages that every column sees whole are multiplied as they are. Where that
+  // leaves something infinite or NaN, the walk is taken again with care for each
+  // infinity and NaN of V (see below).
+  bool careful = false;
 
   // the chunk's pages, one in DEC_WAVES for this wave
   const int base = p.np / p.chunks, rest = p.np % p.chunks;
@@ -110,14 +110,16 @@ __global__ __launch_bounds__(64 * DEC_WAVES, DB * CT <= 4 ? 2 : 1) void k_attn_d
   const int p1 = p0 + base + (p.chunk < rest ? 1 : 0);
   const int steps = (p1 - p0 - wave + DEC_WAVES - 1) / DEC_WAVES;
 
-  const auto step = [&](const Page<Q8, DB>& pg, int32_t id, int page) {
+  const auto step = [&](Page<Q8, DB>& pg, int32_t id, int page, bool more, int32_t id_next) {
     const int key0 = page * PAGE + 8 * g;    // this lane's keys: key0 + j
     const bool masked = page * PAGE + PAGE > whole_to || page * PAGE < whole_from || id < 0;
+    // V comes in while the scores are computed, the next K from then on
+    load_half<Q8, DB>(pg.v, pg.vs, a.c.v, a.c, id, p.head);
     u32x4 ph[CT][Q8 ? DB : 1], pl[CT][Q8 ? DB : 1], seen1[CT];
+    v4f sc[CT][2];
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
-      float t[8];
-      v4f s[2] = {v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}};
+      sc[ct][0] = sc[ct][1] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < DB; ++c) {
 #pragma unroll
@@ -128,15 +130,20 @@ __global__ __launch_bounds__(64 * DEC_WAVES, DB * CT <= 4 ? 2 : 1) void k_attn_d
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const uint32_t w = pg.ks[c][2 * h + i / 2];
-              s[h][i] = __builtin_fmaf(h2f(i & 1 ? w >> 16 : w), d[i], s[h][i]);
+              sc[ct][h][i] = __builtin_fmaf(h2f(i & 1 ? w >> 16 : w), d[i], sc[ct][h][i]);
             }
           } else {
-            s[h] = mfma16<QT>(pg.k[2 * c + h], qf[ct][c], s[h]);
+            sc[ct][h] = mfma16<QT>(pg.k[2 * c + h], qf[ct][c], sc[ct][h]);
           }
         }
       }
+    }
+    if (more) load_half<Q8, DB>(pg.k, pg.ks, a.c.k, a.c, id_next, p.head);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) t[j] = s[j >> 2][j & 3] * a.scale;
+    for (int ct = 0; ct < CT; ++ct) {
+      float t[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[j] = sc[ct][j >> 2][j & 3] * a.scale;
       uint32_t seen = 0xff;
       if (masked) {
         seen = 0;
@@ -151,8 +158,7 @@ __global__ __launch_bounds__(64 * DEC_WAVES, DB * CT <= 4 ? 2 : 1) void k_attn_d
         }
       }
       float top = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
-      top = fmaxf(top, __shfl_xor(top, 16, 64));
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      top = max_lane_xor32(max_lane_xor16(top));
       if (__any(top > m[ct])) {
         const float now = fmaxf(m[ct], top), by = m[ct] == now ? 1.0f : exp2_fast(m[ct] - now);
         m[ct] = now;
@@ -221,10 +227,11 @@ __global__ __launch_bounds__(64 * DEC_WAVES, DB * CT <= 4 ? 2 : 1) void k_attn_d
         }
       } else {
         u32x4 vf = pg.v[dt];
-        if (__any(any_not_finite<VT>(vf))) {
+        if ((masked || careful) && __any(any_not_finite<VT>(vf))) {
           // Infinities and NaN of V must not reach columns that do not see
-          // them (0 times them is NaN): the finite part is multiplied, and what
-          // a column sees of the rest is counted and added as it is.
+          // them (0 times them is NaN), nor meet the two parts of a weight: the
+          // finite part is multiplied, and what a column sees of the rest is
+          // counted and added as it is.
           u32x4 plus, minus;
           vf = take_finite<VT>(vf, plus, minus);
 #pragma unroll
@@ -246,18 +253,31 @@ __global__ __launch_bounds__(64 * DEC_WAVES, DB * CT <= 4 ? 2 : 1) void k_attn_d
   };
 
   if (steps > 0) {
-    Page<Q8, DB> now, next;
+    Page<Q8, DB> pg;
     PageIds ids;
     ids.fill(a.b, a.c.n_pages, p.s, p0 + wave, DEC_WAVES, 0);
     int32_t id = ids.at(a.b, a.c.n_pages, p.s, p0 + wave, DEC_WAVES, 0);
-    load_page<Q8, DB>(now, a.c, id, p.head);
-    for (int i = 0; i < steps; ++i) {
-      const int page = p0 + wave + i * DEC_WAVES;
-      const int32_t id_next = i + 1 < steps ? ids.at(a.b, a.c.n_pages, p.s, p0 + wave, DEC_WAVES, i + 1) : 0;
-      if (i + 1 < steps) load_page<Q8, DB>(next, a.c, id_next, p.head);
-      step(now, id, page);
-      now = next;
-      id = id_next;
+    for (;;) {
+      load_half<Q8, DB>(pg.k, pg.ks, a.c.k, a.c, id, p.head);
+      for (int i = 0; i < steps; ++i) {
+        const bool more = i + 1 < steps;
+        const int32_t id_next = more ? ids.at(a.b, a.c.n_pages, p.s, p0 + wave, DEC_WAVES, i + 1) : 0;
+        step(pg, id, p0 + wave + i * DEC_WAVES, more, id_next);
+        id = id_next;
+      }
+      if (Q8 || careful) break;
+      bool bad = false;
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) bad |= !(__builtin_fabsf(o[ct][dt][i]) < __builtin_inff());
+      if (!__any(bad)) break;
+      careful = true;
+      reset();
+      ids.fill(a.b, a.c.n_pages, p.s, p0 + wave, DEC_WAVES, 0);
+      id = ids.at(a.b, a.c.n_pages, p.s, p0 + wave, DEC_WAVES, 0);
     }
   }
 
@@ -334,20 +354,14 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int D) {
   const int token = blockIdx.x, lane = threadIdx.x & 63, wave = wave_id();
   __shared__ v4f sum[4][64];
   __shared__ float sum_l[4];
-  const int s = seq_at(a.b, token);
-  if (s >= a.b.n_seqs) return;
-  const Seq q = seq_of(a.b, s);
-  if (token < q.begin || token >= q.begin + q.n) return;
-  int slot0, chunks;
-  slots_of(a.b, a.w, s, slot0, chunks);
-  const int G = a.w.G, Hk = a.w.kv_heads, quads = D / 4;
-  const int mine = Hk * chunks * tiles_of(a.w, q.n);
-  if (chunks == 1 || slot0 + mine > a.w.slots) return;   // the latter for starts that do not ascend
+  const Row w = row_of(a.b, a.w, token);
+  const int G = a.w.G, Hk = a.w.kv_heads, quads = D / 4, chunks = w.chunks;
+  if (w.s < 0 || chunks == 1 || w.slot0 + Hk * chunks * w.tiles > a.w.slots) return;   // the last for starts that do not ascend
   const int per = quads <= 8 ? 8 : quads <= 16 ? 16 : quads <= 32 ? 32 : 64;   // lanes of a row's channels
   const int lanes = 64 / per, groups = 4 * lanes, part = wave * lanes + lane / per, quad = lane % per;
-  const int h = blockIdx.y, col = (token - q.begin) * G + h % G, head = h / G, tile = col / a.w.tile;
+  const int h = blockIdx.y, col = (token - w.begin) * G + h % G, head = h / G, tile = col / a.w.tile;
   // slot of chunk c: slot0 + (tile * chunks + c) * kv_heads + head
-  const int64_t row0 = ((int64_t)slot0 + (int64_t)tile * chunks * Hk + head) * a.w.tile + col % a.w.tile;
+  const int64_t row0 = ((int64_t)w.slot0 + (int64_t)tile * chunks * Hk + head) * a.w.tile + col % a.w.tile;
   const int64_t step = (int64_t)Hk * a.w.tile;
   float top = -__builtin_inff();
   for (int c = lane; c < chunks; c += 64) top = fmaxf(top, a.ml[row0 + c * step].x);
@@ -413,7 +427,7 @@ AttnArgs attn_args(const AttnCall& p, const AttnPlan& w) {
   const kq_kv_cache& c = *p.cache;
   a.b = Batch{b.page_table, b.table_width, b.q_start, b.lens, b.n_seqs, b.n_tokens};
   a.c = Cache{static_cast<uint8_t*>(c.k), static_cast<uint8_t*>(c.v), c.n_pages, c.kv_heads};
-  a.w = Split{p.heads / c.kv_heads, c.kv_heads, w.tile, p.window, w.target, w.least, (int)w.slots};
+  a.w = Split{p.heads / c.kv_heads, c.kv_heads, w.tile, p.window, w.target, w.least, w.places, (int)w.slots};
   a.q = static_cast<const uint16_t*>(p.q);
   a.out = static_cast<uint16_t*>(p.out);
   a.tree = p.tree;
@@ -473,7 +487,11 @@ AttnPlan decode_plan(const kq_kv_cache& c, const kq_kv_batch& b, int heads) {
   AttnPlan w;
   const int64_t cols = ((int64_t)b.n_tokens * (heads / c.kv_heads) + b.n_seqs - 1) / b.n_seqs;   // of a mean sequence
   w.tile = cols <= 16 ? 16 : 32;
-  w.target = 1024;
+  w.target = 768;
+  // two workgroups to a compute unit where a wave's registers allow it (the
+  // kernel's launch bounds)
+  const int work = c.head_dim / 32 * (w.tile / 16);
+  w.places = work <= 4 || (c.type != KQ_KV_Q8_0 && work <= 8) ? 512 : 256;
   w.least = 4;
   finish_plan(c, b, heads, w);
   return w;

@@ -49,6 +49,12 @@ __device__ __forceinline__ float max_lane_xor32(float v) {
   return fmaxf(float_of(x), float_of(y));
 }
 
+__device__ __forceinline__ float max_lane_xor16(float v) {
+  uint32_t x = bits_of(v), y = x;
+  asm volatile("s_nop 1\n\tv_permlane16_swap_b32 %0, %1" : "+v"(x), "+v"(y));
+  return fmaxf(float_of(x), float_of(y));
+}
+
 // A pair of fp32 as two 16-bit values of type T, nearest even.
 template <int T>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {

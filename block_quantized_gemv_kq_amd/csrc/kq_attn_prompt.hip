@@ -535,6 +535,7 @@ AttnPlan prompt_plan(const kq_kv_cache& c, const kq_kv_batch& b, int heads) {
   const int64_t cols = (int64_t)b.n_tokens * (heads / c.kv_heads) / b.n_seqs;   // of a mean sequence
   w.tile = cols >= 1024 ? 256 : 128;
   w.target = 256;
+  w.places = 256;
   w.least = 16;
   finish_plan(c, b, heads, w);
   return w;

@@ -319,6 +319,7 @@ struct AttnPlan {
   int tile;
   int target;
   int least;
+  int places;
   int64_t grid;
   int64_t slots;
   int64_t bytes;

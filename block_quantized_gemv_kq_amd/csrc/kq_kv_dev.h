@@ -136,10 +136,10 @@ __device__ __forceinline__ int wave_scan(int v) {
 // together), taken `tile` at a time; a tile walks the pages that its sequence's
 // queries can see, and where there are few tiles these are split into chunks of
 // about equal length, joined by a second kernel in chunk order. `per` pages, the
-// longest chunk, is the mean of all the work over `target` workgroups, at least
-// `least`: at most target + (number of tiles) workgroups have a part, and at
-// most 2 target of them belong to a split tile (a sequence of np > per pages has
-// ceil(np / per) < 2 np / per chunks). The order of the sums depends on the
+// longest chunk, is at least the mean of all the work over `target` workgroups and
+// at least `least`: at most target + (number of tiles) workgroups have a part,
+// and at most 2 target of them belong to a split tile (a sequence of np > per
+// pages has ceil(np / per) < 2 np / per chunks). The order of the sums depends on the
 // batch's lengths alone.
 struct Split {
   int G;          // query heads per key-value head
@@ -148,6 +148,7 @@ struct Split {
   int window;     // 0: none
   int target;
   int least;
+  int places;     // workgroups the chip holds at once
   int slots;      // partial results the workspace holds
 };
 struct Part {
@@ -170,53 +171,73 @@ __device__ __forceinline__ int tiles_of(const Split& w, int n) {
 }
 __device__ __forceinline__ int chunks_of(int np, int per) { return max((np + per - 1) / per, 1); }
 
-// Pages per chunk. Called by whole waves.
-__device__ __forceinline__ int pages_per_chunk(const Batch& b, const Split& w) {
+// What a lane knows of its sequence.
+struct Share {
+  Seq q;
+  int first, np, tiles;   // np, tiles: 0 behind the last sequence
+};
+__device__ __forceinline__ Share share_of(const Batch& b, const Split& w, int s) {
+  Share h{Seq{0, 0, 0}, 0, 0, 0};
+  if (s < b.n_seqs) {
+    h.q = seq_of(b, s);
+    pages_of(b, h.q, w.window, h.first, h.np);
+    h.tiles = tiles_of(w, h.q.n);
+  }
+  return h;
+}
+
+// Pages per chunk; mine: the shares of the first 64 sequences. Called by whole waves.
+// Where the tiles are few, chunks grow until they all fit the chip at once: a few
+// workgroups more than that cost a second round (three sequences of 16 rows and
+// 6000 positions: 528 workgroups for 512 places 35 us, 480 29).
+__device__ __forceinline__ int pages_per_chunk(const Batch& b, const Split& w, const Share& mine) {
   if (w.slots == 0) return 0x7fffffff;
-  const int lane = threadIdx.x & 63;
-  int64_t total = 0;
-  for (int s0 = 0; s0 < b.n_seqs; s0 += 64) {
-    if (s0 + lane < b.n_seqs) {
-      const Seq q = seq_of(b, s0 + lane);
-      int first, np;
-      pages_of(b, q, w.window, first, np);
-      total += (int64_t)np * tiles_of(w, q.n) * w.kv_heads;
+  int64_t total = (int64_t)mine.np * mine.tiles * w.kv_heads;
+  for (int s0 = 64; s0 < b.n_seqs; s0 += 64) {
+    const Share h = share_of(b, w, s0 + (int)(threadIdx.x & 63));
+    total += (int64_t)h.np * h.tiles * w.kv_heads;
+  }
+  // lower and upper bits apart: a lane's total is below 2^55 for what the calls take
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane(wave_scan((int)(total & 0xffffff)), 63);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane(wave_scan((int)(total >> 24)), 63);
+  const int64_t all = (int64_t)lo + ((int64_t)hi << 24);
+  int64_t want = (all + w.target - 1) / w.target;
+  want = want < w.least ? w.least : want > 0x3fffffff ? 0x3fffffff : want;
+  int per = (int)want;
+  const int tiles = __builtin_amdgcn_readlane(wave_scan(mine.tiles * w.kv_heads), 63);
+  if (b.n_seqs <= 64 && 4 * tiles <= w.places) {
+    per = (int)max((all + w.places - 1) / w.places, (int64_t)w.least);
+    for (int i = 0; i < 16; ++i) {
+      const int parts = __builtin_amdgcn_readlane(wave_scan(mine.tiles * w.kv_heads * chunks_of(mine.np, per)), 63);
+      if (parts <= w.places) break;
+      per += 1 + per / 16;
     }
   }
-  for (int o = 32; o > 0; o /= 2) total += __shfl_xor(total, o, 64);
-  int64_t per = (total + w.target - 1) / w.target;
-  per = per < w.least ? w.least : per;
-  return scalar((int)(per > 0x7fffffff ? 0x7fffffff : per));
+  return per;
 }
 
 // Part `id` of the grid. Sums of parts stay below 2^31: the calls take grids
 // below 2^23, and a sum is carried on while it does not pass id.
 __device__ __forceinline__ Part part_of(const Batch& b, const Split& w, int id) {
   const int lane = threadIdx.x & 63;
-  const int per = pages_per_chunk(b, w);
+  Share h = share_of(b, w, lane);
+  const int per = pages_per_chunk(b, w, h);
   Part p;
   p.s = -1;
   int before = 0, slots = 0;
   for (int s0 = 0; s0 < b.n_seqs; s0 += 64) {
-    const int s = s0 + lane;
-    Seq q{0, 0, 0};
-    int first = 0, np = 0, chunks = 1, tiles = 0;
-    if (s < b.n_seqs) {
-      q = seq_of(b, s);
-      pages_of(b, q, w.window, first, np);
-      chunks = chunks_of(np, per);
-      tiles = tiles_of(w, q.n);
-    }
-    const int mine = tiles * w.kv_heads * chunks, split = chunks > 1 ? mine : 0;
+    if (s0 > 0) h = share_of(b, w, s0 + lane);
+    const int chunks = chunks_of(h.np, per);
+    const int mine = h.tiles * w.kv_heads * chunks, split = chunks > 1 ? mine : 0;
     const int upto = wave_scan(mine) + before, slot = wave_scan(split) + slots;
     const uint64_t hit = __ballot(id < upto);
     if (hit) {
       const int l = __ffsll((unsigned long long)hit) - 1;
       const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
       p.s = s0 + l;
-      p.seq = Seq{of(q.begin), of(q.n), of(q.len)};
-      p.first = of(first);
-      p.np = of(np);
+      p.seq = Seq{of(h.q.begin), of(h.q.n), of(h.q.len)};
+      p.first = of(h.first);
+      p.np = of(h.np);
       p.chunks = of(chunks);
       const int local = id - of(upto - mine);
       // heads next to each other: with 8 of them every tile and chunk of a head lies on one XCD
@@ -225,8 +246,9 @@ __device__ __forceinline__ Part part_of(const Batch& b, const Split& w, int id) 
       // the last tiles first: they see the most
       const int tile = p.chunks == 1 ? rest : rest / p.chunks;
       p.chunk = rest - tile * p.chunks;
-      p.tile = of(tiles) - 1 - tile;
+      p.tile = of(h.tiles) - 1 - tile;
       p.slot = of(slot - split) + (p.tile * p.chunks + p.chunk) * w.kv_heads + p.head;
+      if (p.chunks > 1 && p.slot >= w.slots) p.s = -1;   // for starts that do not ascend
       return p;
     }
     before = __builtin_amdgcn_readlane(upto, 63);
@@ -235,27 +257,30 @@ __device__ __forceinline__ Part part_of(const Batch& b, const Split& w, int id) 
   return p;
 }
 
-// First slot of sequence s's split tiles, and its chunks (1: not split).
-__device__ __forceinline__ void slots_of(const Batch& b, const Split& w, int s, int& slot0, int& chunks) {
+// The sequence of a token, its new tokens, the first slot of its split tiles and
+// its chunks (1: not split); s < 0: none. Called by whole waves.
+struct Row {
+  int s, begin, n, slot0, chunks, tiles;
+};
+__device__ __forceinline__ Row row_of(const Batch& b, const Split& w, int token) {
   const int lane = threadIdx.x & 63;
-  const int per = pages_per_chunk(b, w);
-  int64_t sum = 0;
-  for (int s0 = 0; s0 <= s; s0 += 64) {
-    const int i = s0 + lane;
-    if (i < s) {
-      const Seq q = seq_of(b, i);
-      int first, np;
-      pages_of(b, q, w.window, first, np);
-      const int c = chunks_of(np, per);
-      sum += c > 1 ? (int64_t)tiles_of(w, q.n) * w.kv_heads * c : 0;
+  Share h = share_of(b, w, lane);
+  const int per = pages_per_chunk(b, w, h);
+  int slots = 0;
+  for (int s0 = 0; s0 < b.n_seqs; s0 += 64) {
+    if (s0 > 0) h = share_of(b, w, s0 + lane);
+    const int chunks = chunks_of(h.np, per);
+    const int split = chunks > 1 ? h.tiles * w.kv_heads * chunks : 0;
+    const int slot = wave_scan(split) + slots;
+    const uint64_t hit = __ballot(token >= h.q.begin && token < h.q.begin + h.q.n);
+    if (hit) {
+      const int l = __ffsll((unsigned long long)hit) - 1;
+      const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+      return Row{s0 + l, of(h.q.begin), of(h.q.n), of(slot - split), of(chunks), of(h.tiles)};
     }
+    slots = __builtin_amdgcn_readlane(slot, 63);
   }
-  for (int o = 32; o > 0; o /= 2) sum += __shfl_xor(sum, o, 64);
-  slot0 = scalar((int)sum);
-  const Seq q = seq_of(b, s);
-  int first, np;
-  pages_of(b, q, w.window, first, np);
-  chunks = scalar(chunks_of(np, per));
+  return Row{-1, 0, 0, 0, 1, 0};
 }
 
 }  // namespace kqd

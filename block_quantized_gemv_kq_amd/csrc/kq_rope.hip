@@ -106,59 +106,85 @@ struct RopeArgs {
   int interleaved;
 };
 
-// Element d of a head row (fp32, in LDS) after rotation, in 64 bits.
-__device__ __forceinline__ double rotated(const float* row, const double2* cs, const RopeArgs& a, int d) {
-  const int half = a.rot / 2;
-  if (a.freqs == nullptr || d >= a.rot) return (double)row[d];
-  const bool second = a.interleaved ? (d & 1) : d >= half;
-  const int i = a.interleaved ? d >> 1 : second ? d - half : d;
-  const int other = a.interleaved ? d ^ 1 : second ? d - half : d + half;
-  const double2 t = cs[i];
-  const double x = (double)row[d], y = (double)row[other];
-  return second ? __builtin_fma(y, t.y, x * t.x) : __builtin_fma(-y, t.y, x * t.x);
-}
-
 constexpr int ROPE_WAVES = 4, OCT = 8;
-constexpr int ROW_PAD = 4;   // floats after each token's row in LDS
+constexpr int ROW_PAD = 4;   // floats after each token's row in LDS (16-byte pieces stay aligned)
+typedef float v4f __attribute__((ext_vector_type(4)));
 // LDS: OCT tables of rot / 2 (cos, sin), then per wave OCT rows of D floats.
 __host__ __device__ constexpr int rope_lds(int D, int rot) {
   return OCT * (rot / 2) * 16 + ROPE_WAVES * OCT * (D + ROW_PAD) * 4;
 }
 
-// Rows [tokens t0, t0 + n) of one head into the wave's LDS region.
+// Rows [tokens t0, t0 + n) of one head, on their way into the wave's LDS region:
+// the loads are issued in one place and waited for in another.
 template <int T>
-__device__ __forceinline__ void rows_in(const void* x, int64_t ld, int64_t col, int t0, int n, int D, float* rows) {
-  const int lane = threadIdx.x & 63, pieces = D / 8;
-  const bool wide = is_aligned<T>(static_cast<const uint8_t*>(x) + col * type_size<T>(), ld);
-  for (int i = lane; i < n * pieces; i += 64) {
-    const int t = i / pieces, o = i % pieces;
-    float v[8];
-    load_8<T>(x, (int64_t)(t0 + t) * ld + col + 8 * o, wide, v);
-    float* p = rows + t * (D + ROW_PAD) + 8 * o;
+struct Rows {
+  static constexpr int EACH = 4;   // pieces of 8 elements per lane: 8 tokens of up to 256
+  float v[EACH][8];
+  int n8, pieces;
+  __device__ __forceinline__ void load(const void* x, int64_t ld, int64_t col, int t0, int n, int D) {
+    const bool wide = is_aligned<T>(static_cast<const uint8_t*>(x) + col * type_size<T>(), ld);
+    pieces = D / 8;
+    n8 = n * pieces;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) p[j] = v[j];
+    for (int k = 0; k < EACH; ++k) {
+      const int i = (threadIdx.x & 63) + 64 * k;
+      if (i < n8) load_8<T>(x, (int64_t)(t0 + i / pieces) * ld + col + 8 * (i % pieces), wide, v[k]);
+    }
+  }
+  __device__ __forceinline__ void put(float* rows) const {
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+      const int i = (threadIdx.x & 63) + 64 * k;
+      if (i < n8) {
+        v4f* p = reinterpret_cast<v4f*>(rows + (i / pieces) * (8 * pieces + ROW_PAD) + 8 * (i % pieces));
+        p[0] = v4f{v[k][0], v[k][1], v[k][2], v[k][3]};
+        p[1] = v4f{v[k][4], v[k][5], v[k][6], v[k][7]};
+      }
+    }
+    wave_sync();
+  }
+};
+
+// Turns the pairs of n rows in LDS; neighbouring lanes have neighbouring pairs.
+__device__ __forceinline__ void turn_rows(float* rows, const double2* cs, const RopeArgs& a, int n, int D) {
+  if (a.freqs == nullptr) return;
+  const int lane = threadIdx.x & 63, half = a.rot / 2;
+  for (int i = lane; i < half; i += 64) {
+    const int ia = a.interleaved ? 2 * i : i, ib = a.interleaved ? 2 * i + 1 : i + half;
+    for (int t = 0; t < n; ++t) {
+      float* row = rows + t * (D + ROW_PAD);
+      const double2 w = cs[t * half + i];
+      const double x = (double)row[ia], y = (double)row[ib];
+      row[ia] = (float)__builtin_fma(-y, w.y, x * w.x);
+      row[ib] = (float)__builtin_fma(x, w.y, y * w.x);
+    }
   }
   wave_sync();
 }
 
-// Rotated rows out.
+// Eight elements of a row in LDS.
+__device__ __forceinline__ void row_8(const float* p, float (&v)[8]) {
+  const v4f a = reinterpret_cast<const v4f*>(p)[0], b = reinterpret_cast<const v4f*>(p)[1];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
+}
+
+// Rows out.
 template <int T>
-__device__ __forceinline__ void rows_out(void* y, int64_t ld, int64_t col, int t0, int n, int D, const float* rows,
-                                         const double2* cs, const RopeArgs& a) {
+__device__ __forceinline__ void rows_out(void* y, int64_t ld, int64_t col, int t0, int n, int D, const float* rows) {
   const int lane = threadIdx.x & 63, pieces = D / 8;
   const bool wide = is_aligned<T>(static_cast<const uint8_t*>(y) + col * type_size<T>(), ld);
   for (int i = lane; i < n * pieces; i += 64) {
     const int t = i / pieces, o = i % pieces;
     float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = (float)rotated(rows + t * (D + ROW_PAD), cs + t * (a.rot / 2), a, 8 * o + j);
+    row_8(rows + t * (D + ROW_PAD) + 8 * o, v);
     store_8<T>(y, (int64_t)(t0 + t) * ld + col + 8 * o, wide, v);
   }
   wave_sync();
 }
 
 // ---- kq_rope: a workgroup takes up to 8 tokens and a part of the heads, its
-// waves a head at a time.
+// waves a head at a time. The first rows' loads run while the angles are computed.
 template <int XT, int YT>
 __global__ __launch_bounds__(64 * ROPE_WAVES) void k_rope(RopeArgs a, const void* x, int64_t ldx, void* y, int64_t ldy,
                                                          int T, int heads, int D) {
@@ -166,13 +192,18 @@ __global__ __launch_bounds__(64 * ROPE_WAVES) void k_rope(RopeArgs a, const void
   double2* cs = reinterpret_cast<double2*>(lds4);
   const int half = a.rot / 2, wave = wave_id();
   float* rows = reinterpret_cast<float*>(cs + OCT * half) + wave * OCT * (D + ROW_PAD);
-  const int t0 = blockIdx.x * OCT, n = min(OCT, T - t0);
+  const int t0 = blockIdx.x * OCT, n = min(OCT, T - t0), step = ROPE_WAVES * gridDim.y;
+  Rows<XT> next;
+  int h = blockIdx.y * ROPE_WAVES + wave;
+  if (h < heads) next.load(x, ldx, (int64_t)h * D, t0, n, D);
   for (int i = threadIdx.x; i < n * half; i += 64 * ROPE_WAVES)
     cs[i] = cos_sin(a.positions[t0 + i / half], a.freqs[i % half], a.m);
   __syncthreads();
-  for (int h = blockIdx.y * ROPE_WAVES + wave; h < heads; h += ROPE_WAVES * gridDim.y) {
-    rows_in<XT>(x, ldx, (int64_t)h * D, t0, n, D, rows);
-    rows_out<YT>(y, ldy, (int64_t)h * D, t0, n, D, rows, cs, a);
+  for (; h < heads; h += step) {
+    next.put(rows);
+    if (h + step < heads) next.load(x, ldx, (int64_t)(h + step) * D, t0, n, D);
+    turn_rows(rows, cs, a, n, D);
+    rows_out<YT>(y, ldy, (int64_t)h * D, t0, n, D, rows);
   }
 }
 
@@ -184,12 +215,40 @@ __device__ __forceinline__ uint32_t q8_scale(uint32_t bits) {
   const uint32_t d = f2h_bits(__builtin_bit_cast(float, bits) / 127.0f);
   return d == 0x7c00u ? 0x7e00u : d;
 }
-__device__ __forceinline__ int q8_code(float x, uint32_t scale) {
-  if (scale == 0u || scale == 0x7e00u) return 0;
-  const float q = x / h2f(scale);
-  float t = truncf(q);
-  if (fabsf(q - t) >= 0.5f) t += copysignf(1.0f, q);
-  return (int)fminf(fmaxf(t, -127.0f), 127.0f);
+// The code is round(x / d), halves away from zero, of the quotient in fp32: the
+// largest c with (c - 1/2) d <= |x|. (That product is exact, 8 bits by 11; and
+// where x is below it, x / d is below c - 1/2 by 2^-24 of it at least, which is
+// more than half an fp32 step there, so the quotient does not round up to it.) An
+// approximate quotient is at most one off.
+struct Q8Scale {
+  float d, inverse;   // 0: every code is 0
+};
+__device__ __forceinline__ Q8Scale q8_of(uint32_t scale) {
+  const float d = h2f(scale);
+  const bool none = scale == 0u || scale == 0x7e00u;
+  return Q8Scale{none ? 0.0f : d, none ? 0.0f : __builtin_amdgcn_rcpf(d)};
+}
+__device__ __forceinline__ int q8_code(float x, const Q8Scale& s) {
+  const float m = fabsf(x);
+  float c = truncf(fminf(__builtin_fmaf(m, s.inverse, 0.5f), 127.0f));
+  if ((c - 0.5f) * s.d > m) c -= 1.0f;
+  else if ((c + 0.5f) * s.d <= m && s.d > 0.0f) c += 1.0f;
+  c = fminf(c, 127.0f);
+  return (int)(x < 0.0f ? -c : c);
+}
+// The largest of the 32 lanes of a half wave (neighbours, quads, eights, rows of
+// 16 through DPP; the neighbouring row by a permlane swap), in every lane.
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_dpp(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ uint32_t max_xor16(uint32_t v) {
+  uint32_t x = v, y = v;
+  asm volatile("s_nop 1\n\tv_permlane16_swap_b32 %0, %1" : "+v"(x), "+v"(y));
+  return max(x, y);
+}
+__device__ __forceinline__ uint32_t max_32(uint32_t v) {
+  return max_xor16(max_dpp<0x140>(max_dpp<0x141>(max_dpp<0x4E>(max_dpp<0xB1>(v)))));
 }
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7fffffffu; }
 
@@ -244,26 +303,23 @@ struct AppendArgs {
 // K rows of a run (rotated) into a page: a lane has the 8 channels of one
 // position, positions next to each other, so 4 lanes fill 64 bytes.
 template <int CT>
-__device__ __forceinline__ void put_k(uint8_t* region, int p0, int n, int D, const float* rows, const double2* cs,
-                                      const RopeArgs& a) {
-  const int lane = threadIdx.x & 63, half = a.rot / 2;
+__device__ __forceinline__ void put_k(uint8_t* region, int p0, int n, int D, const float* rows) {
+  const int lane = threadIdx.x & 63;
   for (int i = lane; i < OCT * (D / 8); i += 64) {   // D / 8 is a multiple of 4: lanes of a block take part together
     const int t = i & 7, o = i >> 3, p = p0 + t;
     const bool have = t < n;
     float v[8];
+    row_8(rows + t * (D + ROW_PAD) + 8 * o, v);   // rows that there are none of hold anything, and are not used
     uint32_t big = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[j] = have ? (float)rotated(rows + t * (D + ROW_PAD), cs + t * half, a, 8 * o + j) : 0.0f;
-      big = max(big, abs_bits(v[j]));
-    }
+    for (int j = 0; j < 8; ++j) big = max(big, abs_bits(v[j]));
     if constexpr (CT == KQ_KV_Q8_0) {
-      big = max(big, (uint32_t)__shfl_xor((int)big, 8, 64));
-      big = max(big, (uint32_t)__shfl_xor((int)big, 16, 64));
+      big = max_xor16(max_dpp<0x128>(big));   // the lanes 8 (row_ror:8) and 16 away: the block's other pieces
       const uint32_t scale = q8_scale(big);
+      const Q8Scale by = q8_of(scale);
       u32x2v c = {0u, 0u};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) c[j / 4] |= ((uint32_t)q8_code(v[j], scale) & 0xffu) << (8 * (j & 3));
+      for (int j = 0; j < 8; ++j) c[j / 4] |= ((uint32_t)q8_code(v[j], by) & 0xffu) << (8 * (j & 3));
       if (have) {
         *reinterpret_cast<u32x2v*>(region + k_index(true, p, 8 * o)) = c;
         if ((o & 3) == 0) reinterpret_cast<uint16_t*>(region + 32 * D)[(o >> 2) * 32 + p] = (uint16_t)scale;
@@ -287,9 +343,7 @@ __device__ __forceinline__ void put_v(uint8_t* region, int p0, int n, int D, con
       u32x2v c = {0u, 0u};
 #pragma unroll
       for (int t = 0; t < OCT; ++t) {
-        uint32_t big = abs_bits(v[t]);
-        for (int o = 1; o < 32; o *= 2) big = max(big, (uint32_t)__shfl_xor((int)big, o, 64));
-        const uint32_t scale = q8_scale(big), code = (uint32_t)q8_code(v[t], scale) & 0xffu;
+        const uint32_t scale = q8_scale(max_32(abs_bits(v[t]))), code = (uint32_t)q8_code(v[t], q8_of(scale)) & 0xffu;
         c[t / 4] |= code << (8 * (t & 3));
         if (t < n) {
           if ((d & 31) == 0) reinterpret_cast<uint16_t*>(region + 32 * D)[(d >> 5) * 32 + p0 + t] = (uint16_t)scale;
@@ -320,7 +374,16 @@ __global__ __launch_bounds__(64 * ROPE_WAVES) void k_kv_append(AppendArgs a) {
   double2* cs = reinterpret_cast<double2*>(lds4);
   const int half = a.rope.rot / 2, wave = wave_id(), D = a.D, Hk = a.c.kv_heads;
   float* rows = reinterpret_cast<float*>(cs + OCT * half) + wave * OCT * (D + ROW_PAD);
-  const int H = a.q != nullptr ? a.heads : 0;
+  const int H = a.q != nullptr ? a.heads : 0, rows_in_all = H + 2 * Hk, step = ROPE_WAVES * gridDim.y;
+  Rows<XT> next;
+  const auto load = [&](int row) {
+    if (row < H) next.load(a.q, a.ldq, (int64_t)row * D, run.token, run.n, D);
+    else if (row < H + Hk) next.load(a.k, a.ldk, (int64_t)(row - H) * D, run.token, run.n, D);
+    else next.load(a.v, a.ldv, (int64_t)(row - H - Hk) * D, run.token, run.n, D);
+  };
+  int row = blockIdx.y * ROPE_WAVES + wave;
+  if (row < rows_in_all) load(row);
+  const int32_t page = scalar(page_id(a.b, a.c.n_pages, run.s, run.position / PAGE));
   if (a.rope.freqs != nullptr) {
     for (int i = threadIdx.x; i < run.n * half; i += 64 * ROPE_WAVES) {
       const int t = i / half;
@@ -329,21 +392,20 @@ __global__ __launch_bounds__(64 * ROPE_WAVES) void k_kv_append(AppendArgs a) {
     }
   }
   __syncthreads();
-  const int32_t page = scalar(page_id(a.b, a.c.n_pages, run.s, run.position / PAGE));
   const int p0 = run.position % PAGE;
   const int64_t region = region_bytes(CT == KQ_KV_Q8_0, D);
-  for (int row = blockIdx.y * ROPE_WAVES + wave; row < H + 2 * Hk; row += ROPE_WAVES * gridDim.y) {
+  for (; row < rows_in_all; row += step) {
+    next.put(rows);
+    if (row + step < rows_in_all) load(row + step);
+    if (row < H + Hk) turn_rows(rows, cs, a.rope, run.n, D);
     if (row < H) {
-      rows_in<XT>(a.q, a.ldq, (int64_t)row * D, run.token, run.n, D, rows);
-      rows_out<OT>(a.q_out, a.ldo, (int64_t)row * D, run.token, run.n, D, rows, cs, a.rope);
+      rows_out<OT>(a.q_out, a.ldo, (int64_t)row * D, run.token, run.n, D, rows);
     } else if (page >= 0) {
       const bool is_v = row >= H + Hk;
-      const int h = row - H - (is_v ? Hk : 0);
-      rows_in<XT>(is_v ? a.v : a.k, is_v ? a.ldv : a.ldk, (int64_t)h * D, run.token, run.n, D, rows);
-      uint8_t* at = (is_v ? a.c.v : a.c.k) + ((int64_t)page * Hk + h) * region;
+      uint8_t* at = (is_v ? a.c.v : a.c.k) + ((int64_t)page * Hk + (row - H - (is_v ? Hk : 0))) * region;
       // V's pieces start at position 8 (p / 8); a run that starts inside one has fewer than 8 positions
       if (is_v) put_v<CT>(at, p0, run.n, D, rows);
-      else put_k<CT>(at, p0, run.n, D, rows, cs, a.rope);
+      else put_k<CT>(at, p0, run.n, D, rows);
       wave_sync();
     }
   }
