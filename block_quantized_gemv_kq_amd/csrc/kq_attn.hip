@@ -346,64 +346,96 @@ __global__ __launch_bounds__(64 * DEC_WAVES, DB * CT <= 4 || (!Q8 && DB * CT <= 
   }
 }
 
-// ---- The join of split tiles: a workgroup per output row (token, head), lanes
-// over its channels in fours, groups of lanes over the chunks, several of each
-// group's in flight.
-template <int QT>
-__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int D) {
-  const int token = blockIdx.x, lane = threadIdx.x & 63, wave = wave_id();
-  __shared__ v4f sum[4][64];
-  __shared__ float sum_l[4];
-  const Row w = row_of(a.b, a.w, token);
-  const int G = a.w.G, Hk = a.w.kv_heads, quads = D / 4, chunks = w.chunks;
-  if (w.s < 0 || chunks == 1 || w.slot0 + Hk * chunks * w.tiles > a.w.slots) return;   // the last for starts that do not ascend
+// ---- The join of split tiles. Parts [first, chunks) of a row, every `step`-th:
+// lanes over its channels in fours, groups of lanes over the parts, several of
+// each group's in flight. Returns the lane's channels' sum and the weights' sum
+// over the wave's parts, relative to the largest m of the row.
+struct Joined {
+  v4f v;
+  float l;
+};
+__device__ __forceinline__ Joined join_row(const AttnArgs& a, int64_t row0, int64_t stride, int chunks, int first, int step,
+                                           int D) {
+  const int lane = threadIdx.x & 63, quads = D / 4;
   const int per = quads <= 8 ? 8 : quads <= 16 ? 16 : quads <= 32 ? 32 : 64;   // lanes of a row's channels
-  const int lanes = 64 / per, groups = 4 * lanes, part = wave * lanes + lane / per, quad = lane % per;
-  const int h = blockIdx.y, col = (token - w.begin) * G + h % G, head = h / G, tile = col / a.w.tile;
-  // slot of chunk c: slot0 + (tile * chunks + c) * kv_heads + head
-  const int64_t row0 = ((int64_t)w.slot0 + (int64_t)tile * chunks * Hk + head) * a.w.tile + col % a.w.tile;
-  const int64_t step = (int64_t)Hk * a.w.tile;
-  float top = -__builtin_inff();
-  for (int c = lane; c < chunks; c += 64) top = fmaxf(top, a.ml[row0 + c * step].x);
+  const int lanes = 64 / per, quad = min(lane % per, quads - 1);
+  const int part = first * lanes + lane / per, all = step * lanes;
   constexpr int FLY = 4;
-  float total = 0.0f;
-  v4f v = {0.f, 0.f, 0.f, 0.f};
   float2 ml[FLY];
   v4f o[FLY];
   const auto fetch = [&](int c0) {
 #pragma unroll
     for (int i = 0; i < FLY; ++i) {
-      const int c = min(c0 + i * groups, chunks - 1);
-      ml[i] = a.ml[row0 + c * step];
-      o[i] = *reinterpret_cast<const v4f*>(a.part + (row0 + c * step) * D + 4 * min(quad, quads - 1));
+      const int64_t row = row0 + min(c0 + i * all, chunks - 1) * stride;
+      ml[i] = a.ml[row];
+      o[i] = *reinterpret_cast<const v4f*>(a.part + row * D + 4 * quad);
     }
   };
   fetch(part);
+  float top = -__builtin_inff();
+  for (int c = lane; c < chunks; c += 64) top = fmaxf(top, a.ml[row0 + c * stride].x);
   for (int off = 32; off > 0; off /= 2) top = fmaxf(top, __shfl_xor(top, off, 64));
-  for (int c0 = part; c0 < chunks; c0 += FLY * groups) {
+  Joined j{v4f{0.f, 0.f, 0.f, 0.f}, 0.0f};
+  for (int c0 = part; c0 < chunks; c0 += FLY * all) {
     if (c0 > part) fetch(c0);
 #pragma unroll
     for (int i = 0; i < FLY; ++i) {
-      if (c0 + i * groups >= chunks) continue;
-      const float by = ml[i].x == -__builtin_inff() ? (ml[i].y == 0.0f ? 0.0f : 1.0f) : exp2_fast(ml[i].x - top);
-      total += by * ml[i].y;
+      if (c0 + i * all >= chunks) continue;
       // a part that saw nothing holds zeros, or what scores of NaN made of it
-      v += by * o[i];
+      const float by = ml[i].x == -__builtin_inff() ? (ml[i].y == 0.0f ? 0.0f : 1.0f) : exp2_fast(ml[i].x - top);
+      j.l += by * ml[i].y;
+      j.v += by * o[i];
     }
   }
   for (int off = per; off < 64; off *= 2) {
-    total += __shfl_xor(total, off, 64);
+    j.l += __shfl_xor(j.l, off, 64);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += __shfl_xor(v[i], off, 64);
+    for (int i = 0; i < 4; ++i) j.v[i] += __shfl_xor(j.v[i], off, 64);
   }
-  sum[wave][lane] = v;
-  if (lane == 0) sum_l[wave] = total;
+  return j;
+}
+template <int QT>
+__device__ __forceinline__ void put_joined(const AttnArgs& a, int64_t token, int h, int D, const Joined& j) {
+  const int lane = threadIdx.x & 63;
+  if (lane < D / 4)
+    put_4<QT>(a.out + token * a.ldo + (int64_t)h * D + 4 * lane, wide_rows(a.out, a.ldo),
+              j.l == 0.0f ? v4f{0.f, 0.f, 0.f, 0.f} : j.v / j.l);
+}
+
+// Few rows: a workgroup per (token, head), its waves sharing the parts.
+template <int QT>
+__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int D) {
+  __shared__ v4f sum[4][64];
+  __shared__ float sum_l[4];
+  const int token = blockIdx.x, lane = threadIdx.x & 63, wave = wave_id();
+  const Row w = row_of(a.b, a.w, token);
+  const int G = a.w.G, Hk = a.w.kv_heads;
+  if (w.s < 0 || w.chunks == 1 || w.slot0 + Hk * w.chunks * w.tiles > a.w.slots) return;   // the last for starts that do not ascend
+  const int h = blockIdx.y, col = (token - w.begin) * G + h % G, head = h / G, tile = col / a.w.tile;
+  // slot of chunk c: slot0 + (tile * chunks + c) * kv_heads + head
+  const int64_t row0 = ((int64_t)w.slot0 + (int64_t)tile * w.chunks * Hk + head) * a.w.tile + col % a.w.tile;
+  Joined j = join_row(a, row0, (int64_t)Hk * a.w.tile, w.chunks, wave, 4, D);
+  sum[wave][lane] = j.v;
+  if (lane == 0) sum_l[wave] = j.l;
   __syncthreads();
-  if (wave == 0 && lane < quads) {
-    total = sum_l[0] + sum_l[1] + sum_l[2] + sum_l[3];
-    v = sum[0][lane] + sum[1][lane] + sum[2][lane] + sum[3][lane];
-    v = total == 0.0f ? v4f{0.f, 0.f, 0.f, 0.f} : v / total;
-    put_4<QT>(a.out + (int64_t)token * a.ldo + (int64_t)h * D + 4 * lane, wide_rows(a.out, a.ldo), v);
+  if (wave > 0) return;
+  j.l = sum_l[0] + sum_l[1] + sum_l[2] + sum_l[3];
+  j.v = sum[0][lane] + sum[1][lane] + sum[2][lane] + sum[3][lane];
+  put_joined<QT>(a, token, h, D, j);
+}
+
+// Many rows, few of them split: workgroups by split tile (there are at most half
+// as many as slots), a wave per column.
+template <int QT>
+__global__ __launch_bounds__(256) void k_attn_join_tiles(AttnArgs a, int D) {
+  const SplitTile t = split_tile(a.b, a.w, blockIdx.x);
+  if (t.begin < 0) return;
+  const int G = a.w.G;
+  for (int c = blockIdx.y * 4 + wave_id(); c < a.w.tile; c += 4 * gridDim.y) {
+    const int col = t.tile * a.w.tile + c;
+    if (col >= t.n * G) return;
+    const Joined j = join_row(a, (int64_t)t.slot * a.w.tile + c, (int64_t)a.w.kv_heads * a.w.tile, t.chunks, 0, 1, D);
+    put_joined<QT>(a, t.begin + col / G, t.head * G + col % G, D, j);
   }
 }
 
@@ -413,11 +445,17 @@ namespace kq {
 using namespace kqd;
 
 int launch_attn_join(const AttnArgs& a, int type, int D, hipStream_t stream) {
-  const unsigned heads = (unsigned)(a.w.G * a.w.kv_heads);
-  const dim3 grid((unsigned)a.b.n_tokens, heads);
+  const dim3 grid((unsigned)a.b.n_tokens, (unsigned)(a.w.G * a.w.kv_heads));
   dispatch_log("k_attn_join", -1, a.w.G * a.w.kv_heads, D, a.b.n_tokens, grid.x, grid.y, 256, 0, "-");
   if (type == KQ_F16) hipLaunchKernelGGL(k_attn_join<A_F16>, grid, dim3(256), 0, stream, a, D);
   else hipLaunchKernelGGL(k_attn_join<A_BF16>, grid, dim3(256), 0, stream, a, D);
+  return (int)hipGetLastError();
+}
+int launch_attn_join_tiles(const AttnArgs& a, int type, int D, hipStream_t stream) {
+  const dim3 grid((unsigned)(a.w.slots / 2), (unsigned)(a.w.tile / 16));
+  dispatch_log("k_attn_join_tiles", -1, a.w.G * a.w.kv_heads, D, a.b.n_tokens, grid.x, grid.y, 256, 0, "-");
+  if (type == KQ_F16) hipLaunchKernelGGL(k_attn_join_tiles<A_F16>, grid, dim3(256), 0, stream, a, D);
+  else hipLaunchKernelGGL(k_attn_join_tiles<A_BF16>, grid, dim3(256), 0, stream, a, D);
   return (int)hipGetLastError();
 }
 

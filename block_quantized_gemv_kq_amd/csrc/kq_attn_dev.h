@@ -219,4 +219,5 @@ kqd::AttnArgs attn_args(const AttnCall& p, const AttnPlan& w);
 void finish_plan(const kq_kv_cache& c, const kq_kv_batch& b, int heads, AttnPlan& w);
 // Joins the partial results of split tiles (kq_attn.hip).
 int launch_attn_join(const kqd::AttnArgs& a, int type, int D, hipStream_t stream);
+int launch_attn_join_tiles(const kqd::AttnArgs& a, int type, int D, hipStream_t stream);
 }  // namespace kq

@@ -506,7 +506,7 @@ int prompt_launch(const AttnCall& p, const AttnPlan& w) {
   hipLaunchKernelGGL((k_attn_prompt<QT, Q8, DB, WAVES>), dim3((unsigned)w.grid), dim3(64 * WAVES), Sh::LDS, p.stream, a);
   int err = (int)hipGetLastError();
   if (err || w.slots == 0) return err;
-  return launch_attn_join(a, p.type, 32 * DB, p.stream);
+  return launch_attn_join_tiles(a, p.type, 32 * DB, p.stream);
 }
 template <int QT, bool Q8, int DB>
 int prompt_tile(const AttnCall& p, const AttnPlan& w) {
@@ -533,7 +533,7 @@ AttnPlan prompt_plan(const kq_kv_cache& c, const kq_kv_batch& b, int heads) {
   // Tiles of 256 columns for sequences of many: 8 waves share what is read and
   // two of them a SIMD. Sequences of a few hundred columns fill smaller ones better.
   const int64_t cols = (int64_t)b.n_tokens * (heads / c.kv_heads) / b.n_seqs;   // of a mean sequence
-  w.tile = cols >= 1024 ? 256 : 128;
+  w.tile = cols >= 1024 && c.type != KQ_KV_Q8_0 ? 256 : 128;
   w.target = 256;
   w.places = 256;
   w.least = 16;

@@ -283,4 +283,34 @@ __device__ __forceinline__ Row row_of(const Batch& b, const Split& w, int token)
   return Row{-1, 0, 0, 0, 1, 0};
 }
 
+// Split tile `id` (of all sequences' split tiles): its sequence's new tokens, the
+// slot of its first chunk, its chunks. begin < 0: there are fewer.
+struct SplitTile {
+  int begin, n, tile, head, slot, chunks;
+};
+__device__ __forceinline__ SplitTile split_tile(const Batch& b, const Split& w, int id) {
+  const int lane = threadIdx.x & 63;
+  Share h = share_of(b, w, lane);
+  const int per = pages_per_chunk(b, w, h);
+  int before = 0, slots = 0;
+  for (int s0 = 0; s0 < b.n_seqs; s0 += 64) {
+    if (s0 > 0) h = share_of(b, w, s0 + lane);
+    const int chunks = chunks_of(h.np, per);
+    const int mine = chunks > 1 ? h.tiles * w.kv_heads : 0, split = mine * chunks;
+    const int upto = wave_scan(mine) + before, slot = wave_scan(split) + slots;
+    const uint64_t hit = __ballot(id < upto);
+    if (hit) {
+      const int l = __ffsll((unsigned long long)hit) - 1;
+      const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+      const int local = id - of(upto - mine), tile = local / w.kv_heads, head = local - tile * w.kv_heads;
+      const int first = of(slot - split) + tile * of(chunks) * w.kv_heads + head;
+      const bool fits = first + (of(chunks) - 1) * w.kv_heads < w.slots;   // not for starts that do not ascend
+      return SplitTile{fits ? of(h.q.begin) : -1, of(h.q.n), tile, head, first, of(chunks)};
+    }
+    before = __builtin_amdgcn_readlane(upto, 63);
+    slots = __builtin_amdgcn_readlane(slot, 63);
+  }
+  return SplitTile{-1, 0, 0, 0, 0, 1};
+}
+
 }  // namespace kqd
