@@ -465,7 +465,7 @@ AttnArgs attn_args(const AttnCall& p, const AttnPlan& w) {
   const kq_kv_cache& c = *p.cache;
   a.b = Batch{b.page_table, b.table_width, b.q_start, b.lens, b.n_seqs, b.n_tokens};
   a.c = Cache{static_cast<uint8_t*>(c.k), static_cast<uint8_t*>(c.v), c.n_pages, c.kv_heads};
-  a.w = Split{p.heads / c.kv_heads, c.kv_heads, w.tile, p.window, w.target, w.least, w.places, (int)w.slots};
+  a.w = Split{p.heads / c.kv_heads, c.kv_heads, w.tile, p.window, w.target, w.least, w.places, w.search, (int)w.slots};
   a.q = static_cast<const uint16_t*>(p.q);
   a.out = static_cast<uint16_t*>(p.out);
   a.tree = p.tree;
@@ -523,6 +523,7 @@ void finish_plan(const kq_kv_cache& c, const kq_kv_batch& b, int heads, AttnPlan
 
 AttnPlan decode_plan(const kq_kv_cache& c, const kq_kv_batch& b, int heads) {
   AttnPlan w;
+  w.search = 0;
   const int64_t cols = ((int64_t)b.n_tokens * (heads / c.kv_heads) + b.n_seqs - 1) / b.n_seqs;   // of a mean sequence
   w.tile = cols <= 16 ? 16 : 32;
   w.target = 768;
@@ -530,7 +531,10 @@ AttnPlan decode_plan(const kq_kv_cache& c, const kq_kv_batch& b, int heads) {
   // kernel's launch bounds)
   const int work = c.head_dim / 32 * (w.tile / 16);
   w.places = work <= 4 || (c.type != KQ_KV_Q8_0 && work <= 8) ? 512 : 256;
-  w.least = 4;
+  // one page per wave is the least; where tiles alone fill half the chip, shorter
+  // chunks cost more in the join than they spread
+  const int64_t tiles = c.kv_heads * ((b.n_tokens * (int64_t)(heads / c.kv_heads) + w.tile - 1) / w.tile + b.n_seqs);
+  w.least = tiles >= 256 ? 16 : 4;
   finish_plan(c, b, heads, w);
   return w;
 }

@@ -178,21 +178,31 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_prompt(AttnArgs a) {
     }
   };
 
-  // Masks of a step that not every column sees whole.
+  // Masks of a step that not every column sees whole: of a page's keys, element j
+  // of the lane's operands is key 2 (j & 8) + 8 H + (j & 7).
   const auto mask = [&](int page, const int32_t (&id)[PP]) INLINE {
-    seen = 0;
 #pragma unroll
-    for (int g = 0; g < PP; ++g)
+    for (int g = 0; g < PP; ++g) {
+      // the column sees keys above `below` and up to `last` of this page
+      int last = at - (page + g) * PAGE - 8 * H, below = a.w.window > 0 ? last - a.w.window : -64;
+      if (id[g] == -3) last = -64;
+      if (id[g] == -2) last = 64, below = -64;
+      const uint32_t span = (uint32_t)max(min(last, 64) - max(below, -64), 0);
+      below = max(below, -64);
+      uint32_t bits = 0;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int j = 8 * ((i >> 2) & 1) + 4 * (i >> 3) + (i & 3);   // its place in the second product's operands
-        const int key = (page + g) * PAGE + 2 * (j & 8) + 8 * H + (j & 7);
-        bool ok = key <= at && (a.w.window <= 0 || key > at - a.w.window);
-        if (id[g] == -2) ok = true;
-        if (id[g] == -3) ok = false;
-        seen |= (ok ? 1u : 0u) << (16 * g + j);
-        s[g][i] = !ok ? -__builtin_inff() : id[g] < 0 ? __builtin_nanf("") : s[g][i];
+        const int j = 8 * ((i >> 2) & 1) + 4 * (i >> 3) + (i & 3);   // register i's place
+        const bool ok = (uint32_t)(2 * (j & 8) + (j & 7) - below - 1) < span;
+        if constexpr (Q8) bits |= (ok ? 1u : 0u) << j;
+        s[g][i] = ok ? s[g][i] : -__builtin_inff();
       }
+      if (id[g] == -1 || id[g] == -2) {   // no such page: what sees it becomes NaN
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[g][i] = s[g][i] == -__builtin_inff() ? s[g][i] : __builtin_nanf("");
+      }
+      if constexpr (Q8) seen = (seen & ~(0xffffu << (16 * g))) | bits << (16 * g);
+    }
   };
 
   // Scores to weights; o to the new m.
@@ -530,10 +540,15 @@ int prompt_dim(const AttnCall& p, const AttnPlan& w) {
 
 AttnPlan prompt_plan(const kq_kv_cache& c, const kq_kv_batch& b, int heads) {
   AttnPlan w;
-  // Tiles of 256 columns for sequences of many: 8 waves share what is read and
-  // two of them a SIMD. Sequences of a few hundred columns fill smaller ones better.
+  w.search = 1;
+  // Tiles of 256 columns, 8 waves that share what is read, two of them to a SIMD,
+  // where a workgroup of 4 waves would leave a SIMD one (three steps of 16-bit
+  // heads of more than 96 are above half of LDS) and sequences have the columns:
+  // 8191 bf16 tokens of 32 x 128 600 us (128 columns 709), 100 to 300 tokens
+  // fewer tiles than the chip has places. Elsewhere 128: 4000 fp16 tokens of 32 x
+  // 64 102 us (256 columns 114), twelve prompts of 16 x 64 in 8 bits 202 (265).
   const int64_t cols = (int64_t)b.n_tokens * (heads / c.kv_heads) / b.n_seqs;   // of a mean sequence
-  w.tile = cols >= 1024 && c.type != KQ_KV_Q8_0 ? 256 : 128;
+  w.tile = cols >= 1024 && c.type != KQ_KV_Q8_0 && c.head_dim > 96 ? 256 : 128;
   w.target = 256;
   w.places = 256;
   w.least = 16;

@@ -320,6 +320,7 @@ struct AttnPlan {
   int target;
   int least;
   int places;
+  int search;
   int64_t grid;
   int64_t slots;
   int64_t bytes;

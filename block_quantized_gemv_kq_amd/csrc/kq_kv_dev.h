@@ -149,6 +149,7 @@ struct Split {
   int target;
   int least;
   int places;     // workgroups the chip holds at once
+  int search;     // look for the shortest chunks that fit them (prompts, whose pages take long)
   int slots;      // partial results the workspace holds
 };
 struct Part {
@@ -187,9 +188,10 @@ __device__ __forceinline__ Share share_of(const Batch& b, const Split& w, int s)
 }
 
 // Pages per chunk; mine: the shares of the first 64 sequences. Called by whole waves.
-// Where the tiles are few, chunks grow until they all fit the chip at once: a few
-// workgroups more than that cost a second round (three sequences of 16 rows and
-// 6000 positions: 528 workgroups for 512 places 35 us, 480 29).
+// Where the tiles are few, chunks are long enough for all of them to fit the chip
+// at once (a tile has less than one part more than its share of the pages): a few
+// workgroups above that cost a second round (three sequences of 16 rows and 6000
+// positions: 528 workgroups for 512 places 35 us, 480 27).
 __device__ __forceinline__ int pages_per_chunk(const Batch& b, const Split& w, const Share& mine) {
   if (w.slots == 0) return 0x7fffffff;
   int64_t total = (int64_t)mine.np * mine.tiles * w.kv_heads;
@@ -201,17 +203,19 @@ __device__ __forceinline__ int pages_per_chunk(const Batch& b, const Split& w, c
   const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane(wave_scan((int)(total & 0xffffff)), 63);
   const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane(wave_scan((int)(total >> 24)), 63);
   const int64_t all = (int64_t)lo + ((int64_t)hi << 24);
-  int64_t want = (all + w.target - 1) / w.target;
-  want = want < w.least ? w.least : want > 0x3fffffff ? 0x3fffffff : want;
-  int per = (int)want;
+  const auto share = [&](int parts) {   // pages, at least `least`
+    const int64_t each = all >> 31 == 0 ? (int64_t)(((uint32_t)all + parts - 1) / (uint32_t)parts) : (all + parts - 1) / parts;
+    return (int)(each < w.least ? w.least : each > 0x3fffffff ? 0x3fffffff : each);
+  };
   const int tiles = __builtin_amdgcn_readlane(wave_scan(mine.tiles * w.kv_heads), 63);
-  if (b.n_seqs <= 64 && 4 * tiles <= w.places) {
-    per = (int)max((all + w.places - 1) / w.places, (int64_t)w.least);
-    for (int i = 0; i < 16; ++i) {
-      const int parts = __builtin_amdgcn_readlane(wave_scan(mine.tiles * w.kv_heads * chunks_of(mine.np, per)), 63);
-      if (parts <= w.places) break;
-      per += 1 + per / 16;
-    }
+  if (b.n_seqs > 64 || 4 * tiles > w.places) return share(w.target);
+  const int enough = share(w.places - tiles);
+  if (!w.search) return enough;
+  int per = share(w.places);   // less may do
+  for (int i = 0; i < 4; ++i) {
+    const int parts = __builtin_amdgcn_readlane(wave_scan(mine.tiles * w.kv_heads * chunks_of(mine.np, per)), 63);
+    if (parts <= w.places || per >= enough) break;
+    per = i == 3 ? enough : min(per + (enough - per + 2) / 3, enough);
   }
   return per;
 }

@@ -340,3 +340,134 @@ def test_graph_follows_the_arrays():
         out.zero_()
         step()
         assert np.array_equal(got, T.host(out, "f16")) and np.isfinite(got).all() and (got != 0).any()
+
+
+LARGE = [
+    # enough columns for tiles of 256: new, lens, heads, kv_heads, D, window
+    ([130], [130], 8, 1, 128, 0), ([300], [333], 4, 1, 160, 0), ([200, 150], [200, 700], 16, 2, 128, 0), ([140], [140], 8, 1, 256, 0),
+    ([257], [300], 5, 1, 192, 0), ([150], [900], 8, 1, 224, 100), ([400], [400], 4, 1, 128, 33), ([128], [2200], 16, 1, 128, 0),
+    ([160], [2150], 8, 1, 256, 1500),
+]
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("new,lens,heads,kv_heads,D,window", LARGE)
+def test_prompt_large_tiles(kind, new, lens, heads, kv_heads, D, window, capfd):
+    """Tiles of 256 columns (two groups of waves a phase apart), whole and split."""
+    with U.tuning({"log": "1"}):
+        run(False, 30, new, lens, kind, kind, heads, kv_heads, D, window)
+    assert "tile=256" in capfd.readouterr().err
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("new,lens,window,where", [([300], [300], 0, 290), ([300], [310], 0, 5), ([300], [300], 60, 100), ([280], [700], 200, 410)])
+def test_not_finite_in_masked_places_of_large_tiles(kind, new, lens, window, where):
+    change = poison(1, (0, where))
+    change.kind[0] = kind
+    run(False, 31, new, lens, kind, kind, 4, 1, 128, window, change=change)
+
+
+def test_bad_pages_of_large_tiles():
+    """A page id outside the cache in the middle, and a sequence longer than its table."""
+    def change(b, pools, values):
+        b.table[0, 3] = -1       # positions 96..127
+    b = T.Batch(32, [300, 30], [300, 200])
+    pools, values = T.random_cache(33, b, "bf16", 1, 128)
+    b.table[0, 3] = -1
+    b.width = 10
+    b.table = np.ascontiguousarray(b.table[:, :10])
+    b.lens[1] = 400              # 13 pages
+    cache, keep = T.cache_of("bf16", pools, 1, 128)
+    q = T.narrow(np.random.default_rng(34).standard_normal((330, 8 * 128)), "bf16")
+    qd, od = T.dev(q), T.dev(np.zeros_like(q))
+    batch = b.upload()
+    size = kq.kq_attn_prompt_workspace_bytes(cache, batch, 8)
+    ws = U.empty_dev((size + 16,), "uint8")
+    kq.kq_attn_prompt("bf16", qd, 1024, cache, batch, od, 1024, 8, 0.1, workspace=ws, workspace_bytes=size)
+    out = A.widen(T.host(od, "bf16"))
+    nan = np.isnan(out)
+    assert not nan[:96].any() and nan[96:].all()
+
+
+def test_long_walks():
+    """Walks of more steps than the lanes hold places for, whole and with a window."""
+    for window in (0, 4500):
+        run(False, 35, [130], [9000], "bf16", "bf16", 8, 1, 128, window)
+        run(False, 36, [10], [9000], "f16", "q8_0", 2, 1, 64, window)
+        run(True, 37, [2], [9000], "f16", "f16", 2, 1, 64, window)
+
+
+@pytest.mark.parametrize("kind,tile", [("f16", 16), ("q8_0", 16), ("f16", 32), ("q8_0", 32)])
+def test_decode_variants(kind, tile, capfd):
+    """Up to 16 columns of a mean sequence take tiles of 16, more of 32; a table of a few pages needs no join."""
+    with U.tuning({"log": "1"}):
+        run(True, 38, [1 if tile == 16 else 5], [60], "f16", kind, 4, 1, 64)
+    err = capfd.readouterr().err
+    assert f"tile={tile} slots=0" in err and "k_attn_join" not in err
+    with U.tuning({"log": "1"}):
+        run(True, 39, [1 if tile == 16 else 5], [300], "f16", kind, 4, 1, 64)
+    err = capfd.readouterr().err
+    assert f"tile={tile}" in err and "k_attn_join" in err
+
+
+def test_a_layer_from_projection_to_projection():
+    """q|k|v of a quantised product into the cache, attention, and the o projection, for a prompt and then
+    decode steps: each stage against the oracle on the stage's own input."""
+    torch = U.torch_cuda()
+    from oracle import ref as R
+    rng = np.random.default_rng(40)
+    hidden, heads, kv_heads, D = 256, 8, 2, 64
+    row = (heads + 2 * kv_heads) * D
+    Wqkv, fq = U.quantize_both("affine4", (rng.standard_normal((row, hidden)) * 0.1).astype(np.float32))
+    Wo, fo = U.quantize_both("q8_0", (rng.standard_normal((hidden, heads * D)) * 0.1).astype(np.float32))
+    Wqkv, Wo = U.to_dev(Wqkv), U.to_dev(Wo)
+    f, m = kq.kq_rope_freqs("yarn", D, 1e4, 4.0, 64)
+    fd = U.to_dev(f)
+    b = T.Batch(41, [20, 33], [20, 33], width=3)
+    free = [p for p in range(b.n_pages) if p not in set(b.table[(b.table >= 0) & (b.table < b.n_pages)].tolist())]
+    b.table[0, 1] = free[0]
+    pools = [np.full((b.n_pages, kv_heads, 34 * D), 0xFF, np.uint8) for _ in range(2)]
+    cache, (kd, vd) = T.cache_of("q8_0", pools, kv_heads, D)
+    rope = kq.kq_rope_spec(fd, D, kq.KQ_ROPE_HALF, m)
+    for step in range(4):
+        if step:
+            b.new = [1, 1]
+            b.lens = [n + 1 for n in b.lens]
+            b.q_start = np.array([0, 1, 2], np.int32)
+            b.T = 2
+            b.dev = None
+        batch = b.upload()
+        x = rng.standard_normal((b.T, hidden)).astype(np.float16)
+        qkv = U.empty_dev((b.T, row))
+        xd = U.to_dev(x)
+        for t0 in range(0, b.T, kq.KQ_MAX_M):
+            n = min(kq.KQ_MAX_M, b.T - t0)
+            kq.kq_gemv("affine4", Wqkv, xd[t0:], qkv[t0:], row, hidden, n)
+        q, out = T.dev(np.zeros((b.T, heads * D), np.float16)), T.dev(np.zeros((b.T, heads * D), np.float16))
+        kq.kq_kv_append(cache, batch, rope, "f32", qkv[:, heads * D:], row, qkv[:, (heads + kv_heads) * D:], row, qkv, row, "f16", q,
+                        heads * D, heads)
+        decode = step > 0
+        size = (kq.kq_attn_decode_workspace_bytes if decode else kq.kq_attn_prompt_workspace_bytes)(cache, batch, heads)
+        ws = U.empty_dev((size + 16,), "uint8")
+        (kq.kq_attn_decode if decode else kq.kq_attn_prompt)("f16", q, heads * D, cache, batch, out, heads * D, heads, D ** -0.5,
+                                                             workspace=ws, workspace_bytes=size)
+        y = U.empty_dev((b.T, hidden))
+        kq.kq_gemv("q8_0", Wo, out, y, hidden, heads * D, b.T)
+
+        hq = U.to_host(qkv)
+        ref, bound = R.gemv("affine4", fq, x)
+        U.assert_parity(hq, ref, bound, "q|k|v")
+        for r, s, i, at in b.tokens():
+            k = A.rope(hq[r, heads * D:(heads + kv_heads) * D].astype(np.float64).reshape(1, kv_heads, D), [at], f, m, False)[0]
+            v = hq[r, (heads + kv_heads) * D:].astype(np.float64).reshape(kv_heads, D)
+            for h in range(kv_heads):
+                A.put(pools[0][b.table[s, at // 32], h], "q8_0", False, at % 32, k[h])
+                A.put(pools[1][b.table[s, at // 32], h], "q8_0", True, at % 32, v[h])
+        assert np.array_equal(U.to_host(kd), pools[0]) and np.array_equal(U.to_host(vd), pools[1])
+        values = [[np.stack([np.concatenate([A.get(pool[p, h], "q8_0", w) for p in b.table[s, :-(-b.lens[s] // 32)]])[:b.lens[s]]
+                             for h in range(kv_heads)], 1) for s in range(2)] for pool, w in zip(pools, (False, True))]
+        q16, o16 = T.host(q, "f16"), T.host(out, "f16")
+        want = T.attention(b, values, A.widen(q16).reshape(b.T, heads, D), heads, kv_heads, D, D ** -0.5, 0, None, "f16", TWO["q8_0"])
+        T.check_rows(o16, want, b.T, o16, f"step {step}")
+        ref, bound = R.gemv("q8_0", fo, o16)
+        U.assert_parity(U.to_host(y), ref, bound, "o")
