@@ -968,7 +968,7 @@ int check_attn_values(const char* who, const kq::AttnCall& a) {
   if (a.type != KQ_F16 && a.type != KQ_BF16) return fail(KQ_ERR_ARG, "%s: type must be KQ_F16 or KQ_BF16", who);
   if (a.cache->type != KQ_KV_Q8_0 && a.cache->type != (a.type == KQ_F16 ? KQ_KV_F16 : KQ_KV_BF16))
     return fail(KQ_ERR_ARG, "%s: the cache must hold the type of q, or Q8_0", who);
-  if (!(a.scale > 0.0f) || !isfinite(a.scale)) return fail(KQ_ERR_ARG, "%s: scale must be positive and finite", who);
+  if (!(a.scale > 0.0f) || !(a.scale <= 0x1p126f)) return fail(KQ_ERR_ARG, "%s: scale must be positive and at most 2^126", who);
   if (a.window < 0 || a.window > KQ_MAX_WINDOW) return fail(KQ_ERR_ARG, "%s: window=%d must be in [0, 2^30]", who, a.window);
   return KQ_OK;
 }

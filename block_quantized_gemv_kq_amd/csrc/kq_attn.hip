@@ -5,7 +5,18 @@
 // S^T = K Q^T on matrix instructions, 16 keys by 16 columns (the queries of one
 // key-value head, token by token); the scores of a lane are 8 consecutive keys
 // of one column, which is the operand of O^T += V^T P^T as it stands.
-// Every byte of K and V is read once per column tile.
+// Every byte of K and V is read once per column tile, so there are as few tiles
+// as the registers carry (1 or 2 of 16 columns), and where that leaves few
+// workgroups the walk is split over the pages. V's loads run under the scores,
+// the next K's under the softmax.
+//
+// Bound by memory where the cache is long: one token of 32 heads over 131071
+// bf16 positions of 8 key-value heads x 128 100 us (5.4 TB/s; a plain read of as
+// much 87), 48 such tokens over up to 8000 positions in 8 bits 102 us (4.6 TB/s:
+// the conversion of codes shares the time), 64 over 500 in fp16 17 us (4.2 TB/s).
+// Trees of 16 rows x 40 heads are bound by the two parts of the weights and the
+// softmax of 80 columns a page (22.6 us; the bytes alone 7.5), a token at 1000
+// positions by two launches and the latency of one page after another (10.8 us).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -15,7 +26,7 @@ namespace kqd {
 
 constexpr int DEC_WAVES = 4;
 
-// Column tiles of 16 that a workgroup's waves carry.
+// A wave's page of one head, as operands.
 template <bool Q8, int DB>
 struct Page {
   u32x4 k[Q8 ? DB : 2 * DB];
@@ -38,6 +49,7 @@ __device__ __forceinline__ void load_half(u32x4 (&x)[Q8 ? DB : 2 * DB], u32x4 (&
   }
 }
 
+// CT: tiles of 16 columns that every wave carries.
 template <int QT, bool Q8, int DB, int CT>
 __global__ __launch_bounds__(64 * DEC_WAVES, DB * CT <= 4 || (!Q8 && DB * CT <= 8) ? 2 : 1) void k_attn_decode(AttnArgs a) {
   constexpr int D = 32 * DB, DT = 2 * DB, VT = Q8 ? A_BF16 : QT;
@@ -491,7 +503,9 @@ int decode_launch(const AttnCall& p, const AttnPlan& w) {
 }
 template <int QT, bool Q8, int DB>
 int decode_cols(const AttnCall& p, const AttnPlan& w) {
-  return w.tile == 16 ? decode_launch<QT, Q8, DB, 1>(p, w) : decode_launch<QT, Q8, DB, 2>(p, w);
+  if constexpr (!Q8 || DB <= 2)   // (decode_plan)
+    if (w.tile == 32) return decode_launch<QT, Q8, DB, 2>(p, w);
+  return decode_launch<QT, Q8, DB, 1>(p, w);
 }
 template <int QT, bool Q8>
 int decode_dim(const AttnCall& p, const AttnPlan& w) {
@@ -525,14 +539,27 @@ AttnPlan decode_plan(const kq_kv_cache& c, const kq_kv_batch& b, int heads) {
   AttnPlan w;
   w.search = 0;
   const int64_t cols = ((int64_t)b.n_tokens * (heads / c.kv_heads) + b.n_seqs - 1) / b.n_seqs;   // of a mean sequence
-  w.tile = cols <= 16 ? 16 : 32;
+  // Tiles of 32 columns read the cache half as often, tiles of 16 have half the
+  // latency per page and fill the chip better; what is read again comes out of the
+  // caches unless there is much of it. So 32 where a mean sequence has the columns
+  // and the table's pages are above 160 MB: 8 rows x 32 heads (8 of keys) of 131000
+  // bf16 positions 107 us (16: 158), of 48000 49 (60); 16 rows of 4 sequences to 8000
+  // (131 MB) 34 (33), trees of 16 rows x 40 heads to 6000 25.2 (22.6). In 8 bits the
+  // conversions bound it, and 32 columns of heads above 64 leave the registers of
+  // one workgroup: 8 rows of 131000 105 (92), with heads of 64 of 260000 86 (96).
+  const int64_t read = 2ll * b.n_seqs * b.table_width * c.kv_heads * region_bytes(c.type == KQ_KV_Q8_0, c.head_dim);
+  const bool wide = cols > 16 && read > 160000000 && (c.type != KQ_KV_Q8_0 || c.head_dim <= 64);
+  w.tile = wide ? 32 : 16;
+  // Where tiles alone fill more than a quarter of the places: 64 tokens over 4000
+  // positions of 8 heads 119 us, 512 parts 124.
   w.target = 768;
   // two workgroups to a compute unit where a wave's registers allow it (the
   // kernel's launch bounds)
   const int work = c.head_dim / 32 * (w.tile / 16);
   w.places = work <= 4 || (c.type != KQ_KV_Q8_0 && work <= 8) ? 512 : 256;
-  // one page per wave is the least; where tiles alone fill half the chip, shorter
-  // chunks cost more in the join than they spread
+  // One page per wave is the least; where tiles alone fill half the chip, shorter
+  // chunks cost more in the join than they spread: 64 tokens over 500 positions of
+  // 8 heads 17.2 us with 16, 27.3 with 4 (one token at 1000 10.8 with 4, 13.1 with 16).
   const int64_t tiles = c.kv_heads * ((b.n_tokens * (int64_t)(heads / c.kv_heads) + w.tile - 1) / w.tile + b.n_seqs);
   w.least = tiles >= 256 ? 16 : 4;
   finish_plan(c, b, heads, w);

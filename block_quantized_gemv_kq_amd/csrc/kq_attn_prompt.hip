@@ -11,6 +11,14 @@
 //   S^T = K Q^T: keys on the rows, queries on the columns, so a lane has 16
 //   scores of one query per page and shares the column with one other lane;
 //   they are the operand of O^T += V^T P^T as they stand.
+//
+// Bound by the matrix instructions and, nearly as long, the softmax's arithmetic
+// between them: 8191 bf16 tokens of 32 heads x 128 579 us (945 TFLOP/s of visible
+// products; a plain 8192^3 product of the library 1255), 500 tokens behind 32000
+// 290 us (907 TFLOP/s). In 8 bits every wave converts the codes that it reads, and V
+// takes two products: twelve prompts of up to 2500 tokens of 16 heads x 64 193 us,
+// bound by that arithmetic. Five prompts of up to 150 tokens 14.4 us, bound by
+// the latency of one step after another.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -417,7 +425,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_prompt(AttnArgs a) {
           id[g] = page + g >= p1 ? -3 : any_bad ? scalar(page_id(a.b, a.c.n_pages, p.s, page + g)) : 0;
         const bool beyond = page * PAGE > to || (a.w.window > 0 && (page + PP) * PAGE <= from - a.w.window + 1);
         const bool does = works && (!beyond || id[0] == -2), unmasked = whole();
-        // (what needs no masks may be taken for what does)
+        // V of a step that needed no masks is also multiplied this way here
         if (had) add_v(vring + last * Sh::STEP, Flag<true>());
         if (does) scores(kring + now * Sh::STEP);
         phase_ends();
@@ -520,7 +528,9 @@ int prompt_launch(const AttnCall& p, const AttnPlan& w) {
 }
 template <int QT, bool Q8, int DB>
 int prompt_tile(const AttnCall& p, const AttnPlan& w) {
-  return w.tile == 128 ? prompt_launch<QT, Q8, DB, 4>(p, w) : prompt_launch<QT, Q8, DB, 8>(p, w);
+  if constexpr (!Q8 && DB > 3)   // (prompt_plan)
+    if (w.tile == 256) return prompt_launch<QT, Q8, DB, 8>(p, w);
+  return prompt_launch<QT, Q8, DB, 4>(p, w);
 }
 template <int QT, bool Q8>
 int prompt_dim(const AttnCall& p, const AttnPlan& w) {
@@ -544,9 +554,9 @@ AttnPlan prompt_plan(const kq_kv_cache& c, const kq_kv_batch& b, int heads) {
   // Tiles of 256 columns, 8 waves that share what is read, two of them to a SIMD,
   // where a workgroup of 4 waves would leave a SIMD one (three steps of 16-bit
   // heads of more than 96 are above half of LDS) and sequences have the columns:
-  // 8191 bf16 tokens of 32 x 128 600 us (128 columns 709), 100 to 300 tokens
+  // 8191 bf16 tokens of 32 x 128 579 us (128 columns 709), 100 to 300 tokens
   // fewer tiles than the chip has places. Elsewhere 128: 4000 fp16 tokens of 32 x
-  // 64 102 us (256 columns 114), twelve prompts of 16 x 64 in 8 bits 202 (265).
+  // 64 102 us (256 columns 114), twelve prompts of 16 x 64 in 8 bits 193 (265).
   const int64_t cols = (int64_t)b.n_tokens * (heads / c.kv_heads) / b.n_seqs;   // of a mean sequence
   w.tile = cols >= 1024 && c.type != KQ_KV_Q8_0 && c.head_dim > 96 ? 256 : 128;
   w.target = 256;

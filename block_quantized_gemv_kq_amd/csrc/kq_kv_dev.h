@@ -67,20 +67,6 @@ __device__ __forceinline__ Seq seq_of(const Batch& b, int s) {
   return Seq{begin, end - begin, min(max(b.lens[s], 0), 0x7fffff00)};
 }
 
-// The sequence of token t: the first whose tokens end behind it, or n_seqs.
-// Called by whole waves with one t.
-__device__ __forceinline__ int seq_at(const Batch& b, int t) {
-  const int lane = threadIdx.x & 63;
-  int at = 0;
-  for (int s0 = 0; s0 < b.n_seqs; s0 += 64) {
-    const int s = s0 + lane;
-    const int done = __popcll(__ballot(s < b.n_seqs && b.q_start[s + 1] <= t));
-    at += done;
-    if (done < 64) break;
-  }
-  return __builtin_amdgcn_readfirstlane(min(at, b.n_seqs));
-}
-
 // Page id of page `page` of sequence s; -1 where the table names none of the
 // cache's pages, -2 behind the table.
 __device__ __forceinline__ int32_t page_id(const Batch& b, int64_t n_pages, int s, int page) {
@@ -191,9 +177,12 @@ __device__ __forceinline__ Share share_of(const Batch& b, const Split& w, int s)
 // Where the tiles are few, chunks are long enough for all of them to fit the chip
 // at once (a tile has less than one part more than its share of the pages): a few
 // workgroups above that cost a second round (three sequences of 16 rows and 6000
-// positions: 528 workgroups for 512 places 35 us, 480 27).
+// positions, tiles of 32: 528 workgroups for 512 places 35 us, 480 25). Prompts
+// look for the shortest such chunks, up to four tries (500 tokens behind 32000:
+// 290 us, 324 with the length taken at once); for decode the tries cost more than
+// they gain (one token at 1000 11.3 us, 10.8 without).
 __device__ __forceinline__ int pages_per_chunk(const Batch& b, const Split& w, const Share& mine) {
-  if (w.slots == 0) return 0x7fffffff;
+  if (w.slots == 0) return 0x3fffffff;   // no walk is longer
   int64_t total = (int64_t)mine.np * mine.tiles * w.kv_heads;
   for (int s0 = 64; s0 < b.n_seqs; s0 += 64) {
     const Share h = share_of(b, w, s0 + (int)(threadIdx.x & 63));

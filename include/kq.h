@@ -541,10 +541,11 @@ int64_t kq_kv_page_bytes(int type, int kv_heads, int head_dim);
  *   k, v, q: device, xtype, rows ldk, ldv, ldq apart. q_out: device, otype, rows
  *   ldo apart; q itself (same type and ld) or no overlap with k, v or q. heads:
  *   q's, at most KQ_MAX_HEADS.
- * Values are rounded as kq_rope rounds them; Q8_0 blocks are quantised from fp32. A token whose page id is invalid or
- * behind the table is not stored (its q is rotated all the same); one without a
- * place is skipped. Sequences must not share the pages written to. n_tokens ==
- * 0 or n_seqs == 0 is a valid empty call.
+ * Values are rounded as kq_rope rounds them; Q8_0 blocks are quantised from
+ * fp32. A token whose page id is invalid or behind the table is not stored (its
+ * q is rotated all the same); one without a place is skipped. No page that is
+ * written to may stand twice in the table's rows. n_tokens == 0 or n_seqs == 0
+ * is a valid empty call.
  * Errors: KQ_ERR_ARG, KQ_ERR_SHAPE, KQ_ERR_ALIGN, KQ_ERR_HIP. */
 int kq_kv_append(const kq_kv_cache* cache, const kq_kv_batch* batch, const kq_rope_spec* rope, int xtype, const void* k,
                  int64_t ldk, const void* v, int64_t ldv, const void* q, int64_t ldq, int otype, void* q_out, int64_t ldo,
@@ -575,12 +576,16 @@ int64_t kq_attn_prompt_workspace_bytes(const kq_kv_cache* cache, const kq_kv_bat
  * The new tokens' own keys and values have to be in the cache (kq_kv_append).
  *   q, out: device, [rows][heads * head_dim] of type (KQ_F16 or KQ_BF16), ldq
  *   and ldo apart; the cache holds the same type or Q8_0. heads: a multiple of
- *   kv_heads, at most KQ_MAX_HEADS. tree: device, 8-byte aligned, one uint64 per
- *   row, or NULL. scale: positive, finite. window: 0 (none) .. KQ_MAX_WINDOW.
- *   At most KQ_MAX_M rows (n_tokens) and as many sequences; workspace: device,
- *   16-byte aligned, scratch, may be NULL where none is needed.
+ *   kv_heads, at most KQ_MAX_HEADS. out: no overlap with q. tree: device, 8-byte
+ *   aligned, one uint64 per row, or NULL. scale: positive, at most 2^126. window:
+ *   0 (none) .. KQ_MAX_WINDOW. At most KQ_MAX_M rows (n_tokens) and as many
+ *   sequences; workspace: device, 16-byte aligned, scratch, may be NULL where
+ *   none is needed. Calls that share a workspace must not overlap in time.
  * A query that sees nothing, or no score above minus infinity, gives zeros.
  * What a query does not see does not reach it, infinities and NaN included.
+ * What it sees of them makes its results infinite or NaN: which of the two, where
+ * an infinity of V meets a weight below the range of 16 bits, is not defined; nor
+ * is it for a query that itself holds them, or whose scores pass the range of fp32.
  * One that sees a key in a page whose id is invalid gives NaN, as do all
  * queries of a sequence longer than its table. Scores, softmax and sums are
  * fp32; weights enter the products with V as two 16-bit parts; results are
@@ -596,8 +601,8 @@ int kq_attn_decode(int type, const void* q, int64_t ldq, const kq_kv_cache* cach
  * different lengths packed into one batch, or the next part of prompts whose
  * beginning is in the cache. Arguments and results as kq_attn_decode, without
  * trees, up to KQ_MAX_TOKENS rows and KQ_MAX_SEQS sequences. Weights enter the
- * products with V rounded to 16 bits (8-bit caches: two 16-bit parts); their sum
- * is of the unrounded ones.
+ * products with V rounded to 16 bits and are summed as rounded (8-bit caches:
+ * two 16-bit parts, and the sum of the weights themselves).
  * Errors: as kq_attn_decode, and KQ_ERR_ARG where the batch is beyond the grid. */
 int kq_attn_prompt(int type, const void* q, int64_t ldq, const kq_kv_cache* cache, const kq_kv_batch* batch, void* out,
                    int64_t ldo, int heads, float scale, int window, void* workspace, int64_t workspace_bytes,

@@ -342,6 +342,53 @@ def test_graph_follows_the_arrays():
         assert np.array_equal(got, T.host(out, "f16")) and np.isfinite(got).all() and (got != 0).any()
 
 
+def test_prompts_on_two_streams_and_in_a_graph():
+    """Two prompt calls at once (their own workspaces) and a captured one, replayed: the bits of calls alone."""
+    torch = U.torch_cuda()
+    heads, kv_heads, D = 8, 1, 128
+    b = T.Batch(50, [60, 3], [1500, 300])
+    pools, _ = T.random_cache(51, b, "bf16", kv_heads, D)
+    cache, keep = T.cache_of("bf16", pools, kv_heads, D)
+    batch = b.upload()
+    rng = np.random.default_rng(52)
+    qs = [T.narrow(rng.standard_normal((b.T, heads * D)), "bf16") for _ in range(2)]
+    size = kq.kq_attn_prompt_workspace_bytes(cache, batch, heads)
+    assert size > 0
+    qd, outs = [T.dev(q) for q in qs], [T.dev(np.zeros_like(q)) for q in qs]
+    ws = [U.empty_dev((size,), "uint8") for _ in qs]
+
+    def call(i):
+        kq.kq_attn_prompt("bf16", qd[i], heads * D, cache, batch, outs[i], heads * D, heads, 0.1, 700, ws[i], size)
+
+    alone = []
+    for i in range(2):
+        call(i)
+        alone.append(T.host(outs[i], "bf16").copy())
+        assert np.isfinite(A.widen(alone[i])).all() and (alone[i] != 0).any()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for o in outs:
+        o.zero_()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                call(i)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert np.array_equal(T.host(outs[i], "bf16"), alone[i])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=streams[0]):
+        call(0)
+    for rep in range(3):
+        outs[0].zero_()
+        if rep == 1:
+            qd[0].copy_(qd[1])
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(T.host(outs[0], "bf16"), alone[min(rep, 1)])
+
+
 LARGE = [
     # enough columns for tiles of 256: new, lens, heads, kv_heads, D, window
     ([130], [130], 8, 1, 128, 0), ([300], [333], 4, 1, 160, 0), ([200, 150], [200, 700], 16, 2, 128, 0), ([140], [140], 8, 1, 256, 0),
@@ -397,17 +444,48 @@ def test_long_walks():
         run(True, 37, [2], [9000], "f16", "f16", 2, 1, 64, window)
 
 
-@pytest.mark.parametrize("kind,tile", [("f16", 16), ("q8_0", 16), ("f16", 32), ("q8_0", 32)])
-def test_decode_variants(kind, tile, capfd):
-    """Up to 16 columns of a mean sequence take tiles of 16, more of 32; a table of a few pages needs no join."""
+WIDE = [
+    # tiles of 32 columns: new, lens, heads, kv_heads, D, window, trees
+    ([5], [60], 4, 1, 64, 0, False), ([5, 17, 1], [900, 17, 33], 8, 1, 64, 0, False), ([20], [700], 6, 2, 64, 130, False),
+    ([9, 12], [200, 500], 4, 1, 32, 0, True), ([33], [2500], 2, 1, 64, 0, True),
+]
+
+
+@pytest.mark.parametrize("kind,cache_kind", BOTH)
+@pytest.mark.parametrize("new,lens,heads,kv_heads,D,window,trees", WIDE)
+def test_decode_wide_tiles(kind, cache_kind, new, lens, heads, kv_heads, D, window, trees, capfd):
     with U.tuning({"log": "1"}):
-        run(True, 38, [1 if tile == 16 else 5], [60], "f16", kind, 4, 1, 64)
+        run(True, 38, new, lens, kind, cache_kind, heads, kv_heads, D, window, trees, width=1 + 160000000 // (34 * D * 2 * kv_heads))
     err = capfd.readouterr().err
-    assert f"tile={tile} slots=0" in err and "k_attn_join" not in err
+    assert "tile=32" in err and "k_attn_join" in err
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("new,lens,heads,kv_heads,D,window,trees", [([6], [300], 4, 1, 96, 0, False), ([18, 2], [90, 1000], 8, 2, 128, 50, False),
+                                                                    ([10], [400], 5, 1, 256, 0, True), ([7], [200], 3, 1, 160, 0, False)])
+def test_decode_wide_tiles_of_long_heads(kind, new, lens, heads, kv_heads, D, window, trees, capfd):
     with U.tuning({"log": "1"}):
-        run(True, 39, [1 if tile == 16 else 5], [300], "f16", kind, 4, 1, 64)
-    err = capfd.readouterr().err
-    assert f"tile={tile}" in err and "k_attn_join" in err
+        run(True, 39, new, lens, kind, kind, heads, kv_heads, D, window, trees, width=1 + 160000000 // (64 * D * 2 * kv_heads))
+    assert "tile=32" in capfd.readouterr().err
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("new,lens,window,where", [([6], [40], 0, 36), ([6], [300], 0, 5), ([6], [300], 60, 100), ([9], [700], 200, 510)])
+def test_not_finite_in_masked_places_of_wide_tiles(kind, new, lens, window, where):
+    change = poison(1, (0, where))
+    change.kind[0] = kind
+    run(True, 40, new, lens, kind, kind, 4, 1, 128, window, width=10000, change=change)
+
+
+def test_decode_variants(capfd):
+    """Tiles of 16 unless the table's pages are many; a table of a few pages needs no join."""
+    for new, lens, cache_kind, D, width, tile, join in (
+            (1, 60, "f16", 64, 2, 16, False), (5, 60, "q8_0", 64, 4, 16, False), (5, 300, "f16", 64, 10, 16, True),
+            (4, 300, "f16", 64, 20000, 16, True), (5, 300, "q8_0", 128, 20000, 16, True)):
+        with U.tuning({"log": "1"}):
+            run(True, 41, [new], [lens], "f16", cache_kind, 4, 1, D, width=width)
+        err = capfd.readouterr().err
+        assert f"tile={tile}" in err and ("k_attn_join" in err) == join
 
 
 def test_a_layer_from_projection_to_projection():

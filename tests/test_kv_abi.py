@@ -91,7 +91,7 @@ def test_read_refusals():
 
 ATTN = [({"type": F32}, ARG), ({"type": 3}, ARG), ({"type": BF16}, ARG), ({"c": cache("bf16")}, ARG), ({"heads": 0}, ARG),
         ({"heads": 3}, SHAPE), ({"heads": 2 * kq.KQ_MAX_HEADS}, ARG), ({"scale": 0.0}, ARG), ({"scale": -1.0}, ARG),
-        ({"scale": float("nan")}, ARG), ({"scale": float("inf")}, ARG), ({"window": -1}, ARG),
+        ({"scale": float("nan")}, ARG), ({"scale": float("inf")}, ARG), ({"scale": 3e38}, ARG), ({"window": -1}, ARG),
         ({"window": kq.KQ_MAX_WINDOW + 1}, ARG)] + bad_rows("q", "ldq", 2) + bad_rows("out", "ldo", 2)
 
 
