@@ -16,7 +16,7 @@
 // between them: 8191 bf16 tokens of 32 heads x 128 579 us (945 TFLOP/s of visible
 // products; a plain 8192^3 product of the library 1255), 500 tokens behind 32000
 // 290 us (907 TFLOP/s). In 8 bits every wave converts the codes that it reads, and V
-// takes two products: twelve prompts of up to 2500 tokens of 16 heads x 64 193 us,
+// takes two products: twelve prompts of up to 2500 tokens of 16 heads x 64 189 us,
 // bound by that arithmetic. Five prompts of up to 150 tokens 14.4 us, bound by
 // the latency of one step after another.
 #include <hip/hip_runtime.h>
@@ -69,6 +69,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_prompt(AttnArgs a) {
   typedef Prompt<Q8, DB, WAVES> Sh;
   constexpr int D = 32 * DB, VT = Q8 ? A_BF16 : QT, PP = Sh::PP;
   constexpr float SHIFT = VT == A_F16 ? 7.0f : 0.0f;   // fp16 weights up to 2^SHIFT: fewer fall below its normal range
+  // In 8 bits m follows the largest score only in steps of 2^GROWTH, each column by
+  // itself, and most steps leave o as it is (twelve prompts of 16 x 64: 189 us, with
+  // every step 193). Weights that are rounded to 16 bits keep 1 for the largest one,
+  // which is exact: following in steps costs them a third more error and gains nothing
+  // with heads of 128.
+  constexpr float GROWTH = Q8 ? 8.0f : 0.0f;
   extern __shared__ u32x4 lds4[];
   uint8_t* kring = reinterpret_cast<uint8_t*>(lds4);
   uint8_t* vring = kring + Sh::RING * Sh::STEP;
@@ -222,14 +228,17 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_prompt(AttnArgs a) {
       for (int i = 0; i < 16; ++i) top = fmaxf(top, s[g][i]);
     top = max_lane_xor32(top);
     top = __builtin_fmaf(top, a.scale, -SHIFT);   // scale > 0
-    // always: a branch around it cost more than it saved
-    const float now = fmaxf(m, top), by = m == now ? 1.0f : exp2_fast(m - now);
-    m = now;
+    const bool grows = top > m + GROWTH;
+    const float by = grows ? exp2_fast(m - top) : 1.0f;
+    m = grows ? top : m;
     l *= by;
+    // 16 bits, always: a branch around it cost more than it saved
+    if (!Q8 || __any(grows)) {
 #pragma unroll
-    for (int d = 0; d < DB; ++d)
+      for (int d = 0; d < DB; ++d)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[d][i] *= by;
+        for (int i = 0; i < 16; ++i) o[d][i] *= by;
+    }
     const float sub = m == -__builtin_inff() ? 0.0f : m;
 #pragma unroll
     for (int g = 0; g < PP; ++g) {
@@ -556,7 +565,7 @@ AttnPlan prompt_plan(const kq_kv_cache& c, const kq_kv_batch& b, int heads) {
   // heads of more than 96 are above half of LDS) and sequences have the columns:
   // 8191 bf16 tokens of 32 x 128 579 us (128 columns 709), 100 to 300 tokens
   // fewer tiles than the chip has places. Elsewhere 128: 4000 fp16 tokens of 32 x
-  // 64 102 us (256 columns 114), twelve prompts of 16 x 64 in 8 bits 193 (265).
+  // 64 102 us (256 columns 114), twelve prompts of 16 x 64 in 8 bits 189 (265).
   const int64_t cols = (int64_t)b.n_tokens * (heads / c.kv_heads) / b.n_seqs;   // of a mean sequence
   w.tile = cols >= 1024 && c.type != KQ_KV_Q8_0 && c.head_dim > 96 ? 256 : 128;
   w.target = 256;
