@@ -51,7 +51,7 @@ __device__ __forceinline__ void load_half(u32x4 (&x)[Q8 ? DB : 2 * DB], u32x4 (&
 
 // CT: tiles of 16 columns that every wave carries.
 template <int QT, bool Q8, int DB, int CT>
-__global__ __launch_bounds__(64 * DEC_WAVES, DB * CT <= 4 || (!Q8 && DB * CT <= 8) ? 2 : 1) void k_attn_decode(AttnArgs a) {
+__global__ __launch_bounds__(64 * DEC_WAVES, DB * CT <= 2 ? 4 : DB * CT <= 4 || (!Q8 && DB * CT <= 8) ? 2 : 1) void k_attn_decode(AttnArgs a) {
   constexpr int D = 32 * DB, DT = 2 * DB, VT = Q8 ? A_BF16 : QT;
   // d-tiles per round of the sum over the waves: 64 KB of LDS
   constexpr int ROUND = DT * CT * DEC_WAVES <= 64 ? DT : 64 / (CT * DEC_WAVES);
@@ -550,13 +550,14 @@ AttnPlan decode_plan(const kq_kv_cache& c, const kq_kv_batch& b, int heads) {
   const int64_t read = 2ll * b.n_seqs * b.table_width * c.kv_heads * region_bytes(c.type == KQ_KV_Q8_0, c.head_dim);
   const bool wide = cols > 16 && read > 160000000 && (c.type != KQ_KV_Q8_0 || c.head_dim <= 64);
   w.tile = wide ? 32 : 16;
+  // two workgroups to a compute unit where a wave's registers allow it, four with
+  // heads up to 64 (the kernel's launch bounds): one token at 131071 positions of
+  // heads of 64 45 us, 53 with two; in 8 bits 28.5 (34.7)
+  const int work = c.head_dim / 32 * (w.tile / 16);
+  w.places = work <= 2 ? 1024 : work <= 4 || (c.type != KQ_KV_Q8_0 && work <= 8) ? 512 : 256;
   // Where tiles alone fill more than a quarter of the places: 64 tokens over 4000
   // positions of 8 heads 119 us, 512 parts 124.
-  w.target = 768;
-  // two workgroups to a compute unit where a wave's registers allow it (the
-  // kernel's launch bounds)
-  const int work = c.head_dim / 32 * (w.tile / 16);
-  w.places = work <= 4 || (c.type != KQ_KV_Q8_0 && work <= 8) ? 512 : 256;
+  w.target = w.places > 768 ? w.places : 768;
   // One page per wave is the least; where tiles alone fill half the chip, shorter
   // chunks cost more in the join than they spread: 64 tokens over 500 positions of
   // 8 heads 17.2 us with 16, 27.3 with 4 (one token at 1000 10.8 with 4, 13.1 with 16).

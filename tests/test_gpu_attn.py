@@ -136,6 +136,20 @@ def test_peaked_and_large_scores(decode, kind, cache_kind):
     run(decode, 12, [5], [150], kind, cache_kind, 4, 2, 64, scale=1e-30)
 
 
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("kind,cache_kind", [("f16", "f16"), ("bf16", "q8_0")])
+@pytest.mark.parametrize("heads,kv_heads", [(1024, 1), (1024, 1024), (1023, 341)])
+def test_most_heads(decode, kind, cache_kind, heads, kv_heads):
+    run(decode, 42, [1, 1], [40, 170], kind, cache_kind, heads, kv_heads, 32)
+
+
+def test_most_sequences():
+    """4096 sequences, most of them without new tokens."""
+    lens = [(7 * s) % 50 for s in range(4096)]
+    new = [1 if s % 61 == 60 and lens[s] else 0 for s in range(4096)]
+    run(False, 43, new, lens, "f16", "f16", 2, 1, 32)
+
+
 def poison(which, where):
     """Puts infinities and NaN into K or V of one position, in the cache and the values."""
     def change(b, pools, values):
