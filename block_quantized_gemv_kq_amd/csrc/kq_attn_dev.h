@@ -55,6 +55,18 @@ __device__ __forceinline__ float max_lane_xor16(float v) {
   return fmaxf(float_of(x), float_of(y));
 }
 
+// What a column's weights 2^(t - m) are relative to: m is its largest t, for fp16
+// weights SHIFT below it (weights up to 2^SHIFT: fewer fall below the type's normal
+// range). Not where t is FAR from zero or further: nearer, m is off by at most 0.5
+// (two roundings) and no weight passes 2^(SHIFT + 0.5); there, the shift itself
+// would be rounded.
+template <int T> constexpr float SHIFT = T == A_F16 ? 7.0f : 0.0f;
+constexpr float FAR = 0x1p22f;
+template <int T>
+__device__ __forceinline__ float lowered(float top) {
+  return __builtin_fabsf(top) < FAR ? top - SHIFT<T> : top;
+}
+
 // A pair of fp32 as two 16-bit values of type T, nearest even.
 template <int T>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {

@@ -39,6 +39,7 @@ namespace kqd {
 // of K of step i - 1 and V of step i - 2, which the second half last read in the
 // phase before; they are waited for two phases later.
 template <bool V> struct Flag { static constexpr bool value = V; };
+template <int N> struct Count { static constexpr int value = N; };
 
 template <bool Q8, int DB, int WAVES_>
 struct Prompt {
@@ -68,7 +69,6 @@ template <int QT, bool Q8, int DB, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_prompt(AttnArgs a) {
   typedef Prompt<Q8, DB, WAVES> Sh;
   constexpr int D = 32 * DB, VT = Q8 ? A_BF16 : QT, PP = Sh::PP;
-  constexpr float SHIFT = VT == A_F16 ? 7.0f : 0.0f;   // fp16 weights up to 2^SHIFT: fewer fall below its normal range
   // In 8 bits m follows the largest score only in steps of 2^GROWTH, each column by
   // itself, and most steps leave o as it is (twelve prompts of 16 x 64: 189 us, with
   // every step 193). Weights that are rounded to 16 bits keep 1 for the largest one,
@@ -104,7 +104,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_prompt(AttnArgs a) {
   const int token = have ? col / G : 0, qhead = p.head * G + (have ? col - token * G : 0);
   const int at = have ? start + token : -1;
   u32x4 qf[2 * DB];
-  {
+  const auto load_q = [&]() INLINE {
     const bool wide = wide_rows(a.q, a.ldq);
     const uint16_t* q = a.q + (int64_t)(p.seq.begin + token) * a.ldq + (int64_t)qhead * D + 8 * H;
 #pragma unroll
@@ -112,7 +112,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_prompt(AttnArgs a) {
       qf[c] = row_piece(q + 16 * c, wide);
       if (!have) qf[c] = u32x4{0u, 0u, 0u, 0u};
     }
-  }
+  };
+  load_q();
 
   v16f o[DB], s[PP];
   u32x4 pf[Q8 ? 1 : PP][2];      // packed weights (Q8_0: s itself holds them)
@@ -164,11 +165,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_prompt(AttnArgs a) {
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  // s = scores of a step.
-  const auto scores = [&](const uint8_t* stage) INLINE {
+  // s = scores of a step, or of one page.
+  const auto scores = [&](const uint8_t* stage, auto pages) INLINE {
+    constexpr int N = decltype(pages)::value;
     if constexpr (Q8) {
 #pragma unroll
-      for (int g = 0; g < PP; ++g) {
+      for (int g = 0; g < N; ++g) {
         const uint8_t* region = stage + g * Sh::REGION;
         const u32x4* scales = reinterpret_cast<const u32x4*>(region + 32 * D);
         s[g] = zero16();
@@ -184,11 +186,14 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_prompt(AttnArgs a) {
           }
         }
       }
-    } else {
+    } else if constexpr (N == PP) {
       u32x4 f[2][2 * DB];
 #pragma unroll
       for (int c = 0; c < 2 * DB; ++c) f[0][c] = k_operand(stage, c);
       score_products(f, 0, stage);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 2 * DB; ++c) s[0] = mfma32<QT>(k_operand(stage, c), qf[c], c == 0 ? zero16() : s[0]);
     }
   };
 
@@ -219,16 +224,19 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_prompt(AttnArgs a) {
     }
   };
 
-  // Scores to weights; o to the new m.
-  const auto weigh = [&]() INLINE {
+  // Scores to weights; o to the new m. t = scale * s: the hot loop's are exact
+  // products, and m is a product that was rounded, so where they are far from zero
+  // (see again below) t - m is off by many powers of two; there t is rounded as m is.
+  const auto weigh = [&](auto far_) INLINE {
+    constexpr bool ROUNDED = decltype(far_)::value;
     float top = s[0][0];
 #pragma unroll
     for (int g = 0; g < PP; ++g)
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = fmaxf(top, s[g][i]);
     top = max_lane_xor32(top);
-    top = __builtin_fmaf(top, a.scale, -SHIFT);   // scale > 0
-    const bool grows = top > m + GROWTH;
+    top = ROUNDED ? lowered<VT>(top * a.scale) : __builtin_fmaf(top, a.scale, -SHIFT<VT>);   // scale > 0
+    const bool grows = top > m + (ROUNDED ? 0.0f : GROWTH);
     const float by = grows ? exp2_fast(m - top) : 1.0f;
     m = grows ? top : m;
     l *= by;
@@ -243,7 +251,15 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_prompt(AttnArgs a) {
 #pragma unroll
     for (int g = 0; g < PP; ++g) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[g][i] = exp2_fast(__builtin_fmaf(s[g][i], a.scale, -sub));
+      for (int i = 0; i < 16; ++i) {
+        if constexpr (ROUNDED) {
+#pragma clang fp contract(off)
+          const float t = s[g][i] * a.scale;
+          s[g][i] = exp2_fast(t - sub);
+        } else {
+          s[g][i] = exp2_fast(__builtin_fmaf(s[g][i], a.scale, -sub));
+        }
+      }
       if constexpr (Q8) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) l += s[g][i];
@@ -262,14 +278,15 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_prompt(AttnArgs a) {
     }
   };
 
-  // o += V^T P^T of a step.
-  const auto add_v = [&](const uint8_t* stage, auto masked_) INLINE {
+  // o += V^T P^T of a step, or of one page.
+  const auto add_v = [&](const uint8_t* stage, auto masked_, auto pages) INLINE {
     constexpr bool MASKED = decltype(masked_)::value;
+    constexpr int N = decltype(pages)::value;
     if constexpr (Q8) {
       // The scale of V's block goes to the weight, in two parts of 8 bits (bf16 has
       // the range of the scales); the codes stay whole numbers.
 #pragma unroll
-      for (int g = 0; g < PP; ++g) {
+      for (int g = 0; g < N; ++g) {
         const uint8_t* region = stage + g * Sh::REGION;
         const u32x4* scales = reinterpret_cast<const u32x4*>(region + 32 * D);
 #pragma unroll
@@ -302,7 +319,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_prompt(AttnArgs a) {
       // Infinities and NaN of keys that a column does not see must not reach it
       // (0 times them is NaN): they are left out here and added at the end.
 #pragma unroll
-      for (int g = 0; g < PP; ++g) {
+      for (int g = 0; g < N; ++g) {
         u32x4 v[2 * DB];
 #pragma unroll
         for (int c = 0; c < 2 * DB; ++c) v[c] = v_operand(stage + g * Sh::REGION, c % DB, c / DB);
@@ -337,8 +354,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_prompt(AttnArgs a) {
   };
   const auto products = [&](const uint8_t* kstage, const uint8_t* vstage) INLINE {
     if constexpr (Q8) {
-      add_v(vstage, Flag<false>());
-      scores(kstage);
+      add_v(vstage, Flag<false>(), Count<PP>());
+      scores(kstage, Count<PP>());
     } else {
       u32x4 f[2][2 * DB];
 #pragma unroll
@@ -424,7 +441,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_prompt(AttnArgs a) {
       if constexpr (decltype(fast)::value) {
         products(kring + now * Sh::STEP, vring + last * Sh::STEP);
         phase_ends();
-        weigh();
+        weigh(Flag<false>());
         read_ahead(vring + now * Sh::STEP);
       } else {
         const int page = p0 + i * PP;
@@ -435,13 +452,13 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_prompt(AttnArgs a) {
         const bool beyond = page * PAGE > to || (a.w.window > 0 && (page + PP) * PAGE <= from - a.w.window + 1);
         const bool does = works && (!beyond || id[0] == -2), unmasked = whole();
         // V of a step that needed no masks is also multiplied this way here
-        if (had) add_v(vring + last * Sh::STEP, Flag<true>());
-        if (does) scores(kring + now * Sh::STEP);
+        if (had) add_v(vring + last * Sh::STEP, Flag<true>(), Count<PP>());
+        if (does) scores(kring + now * Sh::STEP, Count<PP>());
         phase_ends();
         if (does) {
           seen = 0xffffffffu;
           if (!unmasked) mask(page, id);
-          weigh();
+          weigh(Flag<false>());
           read_ahead(vring + now * Sh::STEP);
         }
         had = does;
@@ -467,7 +484,31 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_prompt(AttnArgs a) {
       if (i < steps) walk(Flag<false>());
     }
     if (WAVES == 8 && !behind) phase_ends();
-    if (had) add_v(vring + (now == 0 ? 2 : now - 1) * Sh::STEP, Flag<true>());
+    if (had) add_v(vring + (now == 0 ? 2 : now - 1) * Sh::STEP, Flag<true>(), Count<PP>());
+  }
+
+  // Where scores are far from zero the walk is taken again, by the waves that have
+  // such columns, a page at a time from memory. (m only rises: what it passed on its
+  // way up from below -FAR has no weight, or left l infinite or NaN. A branch in
+  // every step instead: 8191 bf16 tokens 568 -> 619 us, heads of 256 870 -> 1400.)
+  if (__any(have && m != -__builtin_inff() && !(__builtin_fabsf(m) < FAR && l < __builtin_inff()))) {
+    m = -__builtin_inff();
+    l = 0.0f;
+#pragma unroll
+    for (int d = 0; d < DB; ++d) o[d] = zero16();
+    // Heads of 256 are short of registers: there q does not outlast the loop above
+    // (4000 bf16 tokens of 32 x 256 737 us, 950 with q kept; of 32 x 224 1262, 875).
+    if constexpr (DB == 8) load_q();
+    for (int page = p0; page < p1; ++page) {
+      int32_t id[PP];
+#pragma unroll
+      for (int g = 0; g < PP; ++g) id[g] = g == 0 ? scalar(page_id(a.b, a.c.n_pages, p.s, page)) : -3;
+      const int64_t region = ((int64_t)max(id[0], 0) * a.c.kv_heads + p.head) * Sh::REGION;
+      scores(a.c.k + region, Count<1>());
+      mask(page, id);
+      weigh(Flag<true>());
+      add_v(a.c.v + region, Flag<true>(), Count<1>());
+    }
   }
 
   if constexpr (!Q8) {

@@ -61,18 +61,23 @@ class Batch:
 
 
 def random_cache(seed, batch, kind, kv_heads, D, spread=1.0):
-    """(k, v) uint8 [pages][kv_heads][region] with the sequences' positions
-    holding random values and every other byte of every page 0xFF (NaN in all
-    16-bit types and in the scales), and the values fp64 per sequence
-    [len][kv_heads][D]."""
+    """cache_with of normal values."""
     rng = np.random.default_rng(seed)
+    return cache_with(batch, kind, kv_heads, D, lambda is_v, length: rng.standard_normal((length, kv_heads, D)) * spread)
+
+
+def cache_with(batch, kind, kv_heads, D, rows):
+    """(k, v) uint8 [pages][kv_heads][region] with the sequences' positions
+    holding rows(is_v, length) [length][kv_heads][D] and every other byte of every
+    page 0xFF (NaN in all 16-bit types and in the scales), and the values fp64
+    per sequence [len][kv_heads][D]."""
     nb = A.region_bytes(kind, D)
     pools, values = [], []
     for is_v in (False, True):
         pool = np.full((batch.n_pages, kv_heads, nb), 0xFF, np.uint8)
         vals = []
         for s, length in enumerate(batch.lens):
-            x = rng.standard_normal((length, kv_heads, D)) * spread
+            x = rows(is_v, length)
             if kind == "q8_0":
                 codes, scales = A.q8_blocks(A.narrow(x, "f32"))
                 got = codes.astype(np.float64) * np.repeat(scales.astype(np.float64), 32, -1)
