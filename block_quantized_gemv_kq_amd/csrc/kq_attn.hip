@@ -154,8 +154,11 @@ __global__ __launch_bounds__(64 * DEC_WAVES, DB * CT <= 2 ? 4 : DB * CT <= 4 || 
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
       float t[8];
+      {
+#pragma clang fp contract(off)   // t as m has it
 #pragma unroll
-      for (int j = 0; j < 8; ++j) t[j] = sc[ct][j >> 2][j & 3] * a.scale;
+        for (int j = 0; j < 8; ++j) t[j] = sc[ct][j >> 2][j & 3] * a.scale;
+      }
       uint32_t seen = 0xff;
       if (masked) {
         seen = 0;
@@ -170,7 +173,7 @@ __global__ __launch_bounds__(64 * DEC_WAVES, DB * CT <= 2 ? 4 : DB * CT <= 4 || 
         }
       }
       float top = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
-      top = max_lane_xor32(max_lane_xor16(top));
+      top = lowered<VT>(max_lane_xor32(max_lane_xor16(top)));
       if (__any(top > m[ct])) {
         const float now = fmaxf(m[ct], top), by = m[ct] == now ? 1.0f : exp2_fast(m[ct] - now);
         m[ct] = now;

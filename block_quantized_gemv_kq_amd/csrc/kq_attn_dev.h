@@ -56,11 +56,13 @@ __device__ __forceinline__ float max_lane_xor16(float v) {
 }
 
 // What a column's weights 2^(t - m) are relative to: m is its largest t, for fp16
-// weights SHIFT below it (weights up to 2^SHIFT: fewer fall below the type's normal
-// range). Not where t is FAR from zero or further: nearer, m is off by at most 0.5
-// (two roundings) and no weight passes 2^(SHIFT + 0.5); there, the shift itself
-// would be rounded.
-template <int T> constexpr float SHIFT = T == A_F16 ? 7.0f : 0.0f;
+// weights SHIFT below it: weights are up to 2^15, so one that is a 2^-29th of the
+// largest keeps all its bits, and one below a 2^-40th none. (With weights up to 1 in
+// decode and 2^7 in prompts, keys with scores 14.9 below one other came out 0.1 to
+// 0.6 % wrong, 21 below it 4 to 6 %.) Not where t is FAR from zero or further:
+// nearer, m is off by at most 0.5 (two roundings) and no weight passes 2^15.5,
+// which fp16 holds; there, the shift itself would be rounded.
+template <int T> constexpr float SHIFT = T == A_F16 ? 15.0f : 0.0f;
 constexpr float FAR = 0x1p22f;
 template <int T>
 __device__ __forceinline__ float lowered(float top) {
@@ -83,7 +85,8 @@ __device__ __forceinline__ float low_half(uint32_t v) { return T == A_F16 ? h2f(
 template <int T>
 __device__ __forceinline__ float high_half(uint32_t v) { return T == A_F16 ? h2f(v >> 16) : float_of(v & 0xffff0000u); }
 
-// hi + lo = the pair to twice the type's bits (finite values).
+// hi + lo = the pair to twice the type's bits (finite values; fp16 to 2^-25, which
+// is fewer below 2^-3: see SHIFT).
 template <int T>
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
   hi = pack2<T>(a, b);

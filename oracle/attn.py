@@ -162,11 +162,11 @@ def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, scale: float, ok: np.nda
         return (w @ v) / w.sum(), (w @ np.abs(v)) / w.sum(), float(np.abs(t).max()), unit, np.abs(v).sum(0) / w.sum()
 
 
-def attention_tolerance(out, mass, unit, spread, n_keys, kind, weight_step):
+def attention_tolerance(out, mass, unit, spread, n_keys, kind, weight_step, lost=2.0 ** -25):
     """What an output may be off by: its rounding; and, relative to the weighted
     mass of |v|: errors of the scores (fp32 products and sums over the channels,
     the scale) on both sides of the quotient, of exp2 (2^-21), of the sums over
-    the keys in fp32, of the weights' rounding; a weight below 2^-14 of the
-    largest keeps 2^-25 of it in fp16."""
+    the keys in fp32, of the weights' rounding; and `lost`, what the smallest
+    weights may be off by, relative to the largest."""
     rel = 2 * unit + 2.0 ** -20 + 2 * (n_keys + 16) * 2.0 ** -24 + weight_step
-    return HALF_STEP[kind] * (np.abs(out) + mass * rel) + mass * rel + spread * 2.0 ** -25 + 2.0 ** -25
+    return HALF_STEP[kind] * (np.abs(out) + mass * rel) + mass * rel + spread * lost + 2.0 ** -25

@@ -111,7 +111,7 @@ def cache_of(kind, pools, kv_heads, D, extra=0):
     return kq.kq_kv_cache(kind, k, v, pools[0].shape[0], kv_heads, D), (k, v)
 
 
-def attention(batch, values, q, heads, kv_heads, D, scale, window, tree, kind, weight_step):
+def attention(batch, values, q, heads, kv_heads, D, scale, window, tree, kind, weight_step, lost=2.0 ** -25):
     """The oracle's rows and their tolerances: {row: (out [heads][D], tolerance)}."""
     got = {}
     for row, s, i, at in batch.tokens():
@@ -123,7 +123,7 @@ def attention(batch, values, q, heads, kv_heads, D, scale, window, tree, kind, w
             k, v = values[0][s][:, kh], values[1][s][:, kh]
             out, mass, _, unit, spread = A.attend(q[row, h], k, v, scale, ok)
             outs.append(out)
-            tols.append(A.attention_tolerance(out, mass, unit, spread, int(ok.sum()), kind, weight_step))
+            tols.append(A.attention_tolerance(out, mass, unit, spread, int(ok.sum()), kind, weight_step, lost))
         got[row] = (np.array(outs), np.array(tols))
     return got
 

@@ -112,6 +112,10 @@ def test_scores_that_grow_large(decode, kind, cache_kind, new, lens, heads, kv_h
 # What a weight's rounding is off by, relative (one 16-bit value, or two parts).
 ONE = {"f16": 2.0 ** -11, "bf16": 2.0 ** -8}
 TWO = {"f16": 2.0 ** -22, "bf16": 2.0 ** -16, "q8_0": 2.0 ** -16}
+# What the smallest weights may be off by besides: those of fp16 are multiples of
+# 2^-24, rounded by half of that, and the largest is 2^14.5 or more (2^15, and two
+# roundings). bf16 has no such border near the range of a softmax.
+LOST = 2.0 ** -39.5
 
 
 @pytest.mark.parametrize("decode", [True, False])
@@ -131,7 +135,7 @@ def test_large_and_small_scores_side_by_side(decode, kind, cache_kind, new, lens
     q = T.narrow(np.broadcast_to(size, (b.T, heads, D)).reshape(b.T, heads * D), kind)
     got = attend(decode, kind, cache_kind, b, pools, q, kv_heads, D, 1.0)
     step = TWO["q8_0" if cache_kind == "q8_0" else kind] if decode or cache_kind == "q8_0" else ONE[kind]
-    want = T.attention(b, values, A.widen(q).reshape(b.T, heads, D), heads, kv_heads, D, 1.0, 0, None, kind, step)
+    want = T.attention(b, values, A.widen(q).reshape(b.T, heads, D), heads, kv_heads, D, 1.0, 0, None, kind, step, LOST)
     for row, s, i, at in b.tokens():
         ok = A.visible(at, b.lens[s], 0)
         k, v = values[0][s][ok, 0], values[1][s][ok, 0]
@@ -139,3 +143,62 @@ def test_large_and_small_scores_side_by_side(decode, kind, cache_kind, new, lens
         for h in range(0, heads, 2):
             want[row][0][h], want[row][1][h] = v.mean(0), tolerance(v.mean(0), v, kind, cache_kind)
     T.check_rows(got, want, b.T, got, f"{new} {lens}")
+
+
+# One key far above the rest, with a small V, and all the others equally far below:
+# what they have in common adds up, and their weights' rounding with it. (Over 8-bit
+# caches decode sums codes with 128 added, three times the mass here at most: its
+# chains have one rounding per 32 keys, the tolerance two per key.)
+GAPS = [9.0, 11.890625, 13.0, 13.859375, 14.90625, 16.109375, 17.5, 21.0]
+
+
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("kind,cache_kind", BOTH)
+@pytest.mark.parametrize("new,lens,heads,kv_heads,D,window,width", [
+    ([1], [3000], 4, 1, 64, 0, None), ([1], [60], 2, 2, 128, 0, None), ([9], [2000], 4, 1, 64, 0, 40000), ([3, 1], [500, 3000], 4, 2, 96, 2999, None),
+    ([40], [700], 32, 1, 128, 0, None), ([2], [1500], 1, 1, 256, 0, None)])
+def test_small_weights(decode, kind, cache_kind, new, lens, heads, kv_heads, D, window, width):
+    for gap in GAPS:
+        rng = np.random.default_rng(66)
+        b = T.Batch(67, new, lens, width=width)
+
+        def rows(is_v, length):
+            if is_v:
+                v = rng.uniform(0.5, 1.5, (length, kv_heads, D))
+                v[0] *= 2.0 ** -20
+                return v
+            k = rng.standard_normal((length, kv_heads, D))
+            k[..., :32] = 0.0           # a block of its own
+            k[0, :, 0] = gap
+            return k
+        pools, values = T.cache_with(b, cache_kind, kv_heads, D, rows)
+        q = np.zeros((b.T, heads, D))
+        q[..., 0] = 1.0
+        q = T.narrow(q.reshape(b.T, heads * D), kind)
+        got = attend(decode, kind, cache_kind, b, pools, q, kv_heads, D, 1.0, window)
+        step = TWO["q8_0" if cache_kind == "q8_0" else kind] if decode or cache_kind == "q8_0" else ONE[kind]
+        want = T.attention(b, values, A.widen(q).reshape(b.T, heads, D), heads, kv_heads, D, 1.0, window, None, kind, step, LOST)
+        T.check_rows(got, want, b.T, got, f"{new} {lens} gap {gap}")
+
+
+def test_a_long_tail_far_below():
+    """131071 positions, all but the first 17.5 below it: their share (0.0033) comes out whole, in a token's call and a prompt's."""
+    heads, D, length = 2, 32, 131071
+    rng = np.random.default_rng(68)
+    b = T.Batch(69, [1], [length])
+
+    def rows(is_v, length):
+        x = np.ones((length, 1, D)) if is_v else np.zeros((length, 1, D))
+        x[0] = 0.0 if is_v else 17.5 / D
+        return x
+    for kind, cache_kind in BOTH:
+        pools, values = T.cache_with(b, cache_kind, 1, D, rows)
+        q = T.narrow(np.ones((1, heads * D)), kind)
+        sink = float(values[0][0][0, 0].sum())
+        tail = (length - 1) * np.exp(-sink)
+        want = tail / (1 + tail)
+        for decode in (True, False):
+            got = A.widen(attend(decode, kind, cache_kind, b, pools, q, 1, D, 1.0))
+            # its rounding; the weights' (2^-11 and 2^-8 at most); sums of 131071 in 512 parts of at most 1024 in fp32
+            tol = want * (A.HALF_STEP[kind] + (TWO["q8_0" if cache_kind == "q8_0" else kind] if decode else ONE[kind]) + 2 * 1024 * 2.0 ** -24)
+            assert (np.abs(got - want) <= tol).all(), (kind, cache_kind, decode, got, want)
