@@ -961,6 +961,7 @@ int check_attn(const char* who, const kq::AttnCall& a, int64_t need, int64_t giv
   if ((st = check_rows(who, "out", a.out, a.type, a.ldo, width))) return st;
   if (!aligned(a.tree, 8)) return fail(KQ_ERR_ALIGN, "%s: tree must be 8-byte aligned", who);
   if (need > 0 && (st = check_workspace(who, a.ws, given, need))) return st;
+  if (a.out == a.q) return fail(KQ_ERR_ARG, "%s: out must not be q", who);
   return KQ_OK;
 }
 

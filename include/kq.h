@@ -576,11 +576,11 @@ int64_t kq_attn_prompt_workspace_bytes(const kq_kv_cache* cache, const kq_kv_bat
  * The new tokens' own keys and values have to be in the cache (kq_kv_append).
  *   q, out: device, [rows][heads * head_dim] of type (KQ_F16 or KQ_BF16), ldq
  *   and ldo apart; the cache holds the same type or Q8_0. heads: a multiple of
- *   kv_heads, at most KQ_MAX_HEADS. out: no overlap with q. tree: device, 8-byte
- *   aligned, one uint64 per row, or NULL. scale: positive, at most 2^126. window:
- *   0 (none) .. KQ_MAX_WINDOW. At most KQ_MAX_M rows (n_tokens) and as many
- *   sequences; workspace: device, 16-byte aligned, scratch, may be NULL where
- *   none is needed. Calls that share a workspace must not overlap in time.
+ *   kv_heads, at most KQ_MAX_HEADS. out: no overlap with q (q itself is refused).
+ *   tree: device, 8-byte aligned, one uint64 per row, or NULL. scale: positive, at
+ *   most 2^126. window: 0 (none) .. KQ_MAX_WINDOW. At most KQ_MAX_M rows (n_tokens)
+ *   and as many sequences; workspace: device, 16-byte aligned, scratch, may be NULL
+ *   where none is needed. Calls that share a workspace must not overlap in time.
  * A query that sees nothing, or no score above minus infinity, gives zeros.
  * What a query does not see does not reach it, infinities and NaN included.
  * What it sees of them makes its results infinite or NaN: which of the two, where
