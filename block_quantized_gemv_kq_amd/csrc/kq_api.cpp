@@ -987,6 +987,7 @@ int kq_rope_freqs(int scaling, int rot_dim, double base, double factor, int64_t 
   if (scaling == KQ_ROPE_YARN && (original_length <= 0 || !isfinite(beta_fast) || !isfinite(beta_slow) || !(beta_fast > beta_slow)))
     return fail(KQ_ERR_ARG, "kq_rope_freqs: YARN needs original_length > 0 and beta_fast > beta_slow");
   if (scaling == KQ_ROPE_NTK && rot_dim > 2) base *= pow(factor, (double)rot_dim / (rot_dim - 2));
+  if (!isfinite(base)) return fail(KQ_ERR_ARG, "kq_rope_freqs: base and factor give an infinite base");
   *mscale = scaling == KQ_ROPE_YARN && factor > 1 ? 0.1 * log(factor) + 1 : 1.0;
   for (int i = 0; i < rot_dim / 2; ++i) {
     const double f = pow(base, -2.0 * i / rot_dim);
@@ -997,6 +998,7 @@ int kq_rope_freqs(int scaling, int rot_dim, double base, double factor, int64_t 
       const double g = fmin(1.0, fmax(0.0, (turns - beta_slow) / (beta_fast - beta_slow)));
       freqs[i] = g * f + (1 - g) * f / factor;
     }
+    if (!isfinite(freqs[i])) return fail(KQ_ERR_ARG, "kq_rope_freqs: base and factor give infinite frequencies");
   }
   return ok();
 }

@@ -467,8 +467,9 @@ typedef enum kq_rope_scaling {
 
 /* kq_rope_freqs — host: freqs[rot_dim / 2] and *mscale of a scaling (host
  * memory; the caller copies freqs to the device once). base > 0 and factor > 0
- * finite; original_length > 0 and beta_fast > beta_slow for YARN (usually 32
- * and 1; ignored otherwise).
+ * finite, and so that NTK's base and every frequency are finite;
+ * original_length > 0 and beta_fast > beta_slow for YARN (usually 32 and 1;
+ * ignored otherwise).
  * Errors: KQ_ERR_ARG, KQ_ERR_SHAPE (rot_dim not even or not in [2, KQ_MAX_HEAD_DIM]). */
 int kq_rope_freqs(int scaling, int rot_dim, double base, double factor, int64_t original_length, double beta_fast,
                   double beta_slow, double* freqs, double* mscale);
