@@ -14,9 +14,13 @@
 // bf16 positions of 8 key-value heads x 128 100 us (5.4 TB/s; a plain read of as
 // much 87), 48 such tokens over up to 8000 positions in 8 bits 102 us (4.6 TB/s:
 // the conversion of codes shares the time), 64 over 500 in fp16 17 us (4.2 TB/s).
-// Trees of 16 rows x 40 heads are bound by the two parts of the weights and the
-// softmax of 80 columns a page (22.6 us; the bytes alone 7.5), a token at 1000
-// positions by two launches and the latency of one page after another (10.8 us).
+// Three trees of 16 rows x 32 heads (8 of keys) over up to 6000 positions are bound
+// by the two parts of the weights and the softmax of 64 columns a page, in four
+// tiles that each read it (22.7 us; the bytes alone 7.5), a token at 1000 positions
+// by two launches and the latency of one page after another (10.9 us). Above heads
+// of 192 registers run out: one token at 131071 bf16 positions 147 us with heads of
+// 192 (5.5 TB/s), 181 with 224 (5.2), 265 with 256 (4.1; 8 scratch stores and 11
+// loads of 16 bytes a page).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -547,15 +551,22 @@ AttnPlan decode_plan(const kq_kv_cache& c, const kq_kv_batch& b, int heads) {
   // caches unless there is much of it. So 32 where a mean sequence has the columns
   // and the table's pages are above 160 MB: 8 rows x 32 heads (8 of keys) of 131000
   // bf16 positions 107 us (16: 158), of 48000 49 (60); 16 rows of 4 sequences to 8000
-  // (131 MB) 34 (33), trees of 16 rows x 40 heads to 6000 25.2 (22.6). In 8 bits the
+  // (131 MB) 34 (33), three trees of 16 rows to 6000 25.3 (22.7). In 8 bits the
   // conversions bound it, and 32 columns of heads above 64 leave the registers of
   // one workgroup: 8 rows of 131000 105 (92), with heads of 64 of 260000 86 (96).
+  // The host knows the table's width, not the lengths. With room for 131072
+  // positions, as a captured graph keeps it, short sequences pay for it: those trees
+  // 25.3, eight sequences of 8 rows at 500 18.3 (a table of their length 15.8), one
+  // row at 100 9.3 (6.9, and no workspace).
   const int64_t read = 2ll * b.n_seqs * b.table_width * c.kv_heads * region_bytes(c.type == KQ_KV_Q8_0, c.head_dim);
   const bool wide = cols > 16 && read > 160000000 && (c.type != KQ_KV_Q8_0 || c.head_dim <= 64);
   w.tile = wide ? 32 : 16;
-  // two workgroups to a compute unit where a wave's registers allow it, four with
-  // heads up to 64 (the kernel's launch bounds): one token at 131071 positions of
-  // heads of 64 45 us, 53 with two; in 8 bits 28.5 (34.7)
+  // Two workgroups to a compute unit, four with heads up to 64, one for wide tiles
+  // and heads above 128 in 8 bits (the kernel's launch bounds). With heads of 64: one
+  // token at 131071 positions 55.2 us, 53.1 with two, in 8 bits 33.6 (34.7), eight at
+  // 8000 18.1 (18.5), in 8 bits 15.5 (16.0). Not all of it fits the registers: 16-bit
+  // heads of 224 and 256 keep 12 and 64 of a wave's in scratch (32 columns of 32,
+  // 128 and 256: 12, 2 and 50; 8 bits of 256: 67).
   const int work = c.head_dim / 32 * (w.tile / 16);
   w.places = work <= 2 ? 1024 : work <= 4 || (c.type != KQ_KV_Q8_0 && work <= 8) ? 512 : 256;
   // Where tiles alone fill more than a quarter of the places: 64 tokens over 4000

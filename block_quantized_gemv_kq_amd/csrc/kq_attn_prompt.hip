@@ -13,12 +13,16 @@
 //   they are the operand of O^T += V^T P^T as they stand.
 //
 // Bound by the matrix instructions and, nearly as long, the softmax's arithmetic
-// between them: 8191 bf16 tokens of 32 heads x 128 579 us (945 TFLOP/s of visible
-// products; a plain 8192^3 product of the library 1255), 500 tokens behind 32000
-// 290 us (907 TFLOP/s). In 8 bits every wave converts the codes that it reads, and V
-// takes two products: twelve prompts of up to 2500 tokens of 16 heads x 64 189 us,
-// bound by that arithmetic. Five prompts of up to 150 tokens 14.4 us, bound by
-// the latency of one step after another.
+// between them: 8191 bf16 tokens of 32 heads x 128 555 to 605 us with the clock
+// (991 to 909 TFLOP/s of visible products; a plain 8192^3 product of the library
+// 1255), 500 tokens behind 32000 285 to 310 us (926 to 850 TFLOP/s). In 8 bits every
+// wave converts the codes that it reads, and V takes two products: twelve prompts of
+// up to 2500 tokens of 16 heads x 64 190 us, bound by that arithmetic. Five prompts
+// of up to 150 tokens 14.5 us, bound by the latency of one step after another.
+// Two waves to a SIMD leave each 256 registers. Heads of 192 and more pass them in
+// 16 bits (45, 138 and 260 of a wave's in scratch, in the loop without masks 1, 15
+// and 14 loads of 16 bytes and 8 stores a step): 4000 bf16 tokens of 32 heads x 160
+// 223 us (733 TFLOP/s), of 192 302 (651), of 224 907 to 990 (253), of 256 700 (374).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -489,8 +493,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_prompt(AttnArgs a) {
 
   // Where scores are far from zero the walk is taken again, by the waves that have
   // such columns, a page at a time from memory. (m only rises: what it passed on its
-  // way up from below -FAR has no weight, or left l infinite or NaN. A branch in
-  // every step instead: 8191 bf16 tokens 568 -> 619 us, heads of 256 870 -> 1400.)
+  // way up from below -FAR has no weight, or left l infinite or NaN. 4000 bf16 tokens
+  // of 32 x 128 that all have such scores 452 us, 178 without. A branch in every
+  // step instead: 8191 tokens 568 -> 619 us, heads of 256 870 -> 1400.)
   if (__any(have && m != -__builtin_inff() && !(__builtin_fabsf(m) < FAR && l < __builtin_inff()))) {
     m = -__builtin_inff();
     l = 0.0f;
@@ -604,9 +609,10 @@ AttnPlan prompt_plan(const kq_kv_cache& c, const kq_kv_batch& b, int heads) {
   // Tiles of 256 columns, 8 waves that share what is read, two of them to a SIMD,
   // where a workgroup of 4 waves would leave a SIMD one (three steps of 16-bit
   // heads of more than 96 are above half of LDS) and sequences have the columns:
-  // 8191 bf16 tokens of 32 x 128 579 us (128 columns 709), 100 to 300 tokens
-  // fewer tiles than the chip has places. Elsewhere 128: 4000 fp16 tokens of 32 x
-  // 64 102 us (256 columns 114), twelve prompts of 16 x 64 in 8 bits 189 (265).
+  // 8191 bf16 tokens of 32 x 128 579 us (128 columns 709). Prompts of up to 300
+  // tokens have fewer tiles than the chip has places even with 128 columns, which
+  // the others take too: 4000 fp16 tokens of 32 x 64 102 us (256 columns 114), twelve
+  // prompts of 16 x 64 in 8 bits 189 (265).
   const int64_t cols = (int64_t)b.n_tokens * (heads / c.kv_heads) / b.n_seqs;   // of a mean sequence
   w.tile = cols >= 1024 && c.type != KQ_KV_Q8_0 && c.head_dim > 96 ? 256 : 128;
   w.target = 256;

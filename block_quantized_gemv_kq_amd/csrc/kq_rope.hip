@@ -10,11 +10,12 @@
 // Tokens are taken 8 at a time: their cos and sin are computed once per workgroup
 // and serve all its heads, and 8 positions of a channel are what V keeps together.
 // Bound by memory where there are many tokens: kq_rope of 6001 x 32 x 128 bf16 24 us
-// (4.1 TB/s read and written; a copy of as much 20); seven prompts of up to 700
-// tokens, 32 + 8 + 8 heads x 128, into bf16 pages 39 us (3.1 TB/s: the 64-bit products
-// and LDS share the time), read back in 21. Few tokens: kq_rope of 16 5.5 us, most of
-// it the launch and the sines; 16 tokens into 8-bit pages 8.9 us, one after another
-// the batch's arrays, the page table, the sines and the rows.
+// (4.1 TB/s read and written; a copy of as much 20); seven prompts of up to 1100
+// tokens (4879), 32 + 8 + 8 heads x 128, into bf16 pages 39 us (3.1 TB/s; vector
+// instructions take 69 % of the cycles), read back in 21 (V in single elements). Few
+// tokens: kq_rope of 16 5.5 us, most of it the launch and the sines; 16 tokens into
+// 8-bit pages 8.9 us, one after another the batch's arrays, the page table, the sines
+// and the rows.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

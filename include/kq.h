@@ -460,7 +460,12 @@ typedef struct kq_rope_spec {
  *   YARN    g f_i + (1 - g) f_i / factor, g = (n - beta_slow) / (beta_fast -
  *           beta_slow) held in [0, 1], n = original_length f_i / (2 pi) the
  *           turns of the pair over the original context; mscale = 0.1
- *           ln(factor) + 1 (1 for factor <= 1; for the others always 1) */
+ *           ln(factor) + 1 (1 for factor <= 1; for the others always 1).
+ *           The ramp is linear in the turns, as the method's paper has it. A
+ *           checkpoint that was trained with a ramp linear in the pair's number i,
+ *           between the two (rounded) at which the turns are beta_fast and
+ *           beta_slow, needs other frequencies between those: its caller fills
+ *           freqs itself. */
 typedef enum kq_rope_scaling {
   KQ_ROPE_NONE = 0, KQ_ROPE_LINEAR = 1, KQ_ROPE_NTK = 2, KQ_ROPE_YARN = 3
 } kq_rope_scaling;
@@ -573,7 +578,9 @@ int64_t kq_attn_prompt_workspace_bytes(const kq_kv_cache* cache, const kq_kv_bat
  *   out = sum_j w_j v_j / sum_j w_j, w_j = exp(scale q . k_j),
  * over positions j <= at, with window > 0 only j > at - window, and with tree
  * only those of the sequence's new tokens whose bit is set: bit i of tree[row]
- * says that the row's query sees new token i (older positions are all seen).
+ * says that the row's query sees new token i (older positions are all seen). The
+ * window counts places in the cache, in trees too: branches that a query does not
+ * see use it up, and a token's depth in the tree plays no part.
  * The new tokens' own keys and values have to be in the cache (kq_kv_append).
  *   q, out: device, [rows][heads * head_dim] of type (KQ_F16 or KQ_BF16), ldq
  *   and ldo apart; the cache holds the same type or Q8_0. heads: a multiple of
@@ -586,13 +593,16 @@ int64_t kq_attn_prompt_workspace_bytes(const kq_kv_cache* cache, const kq_kv_bat
  * What a query does not see does not reach it, infinities and NaN included.
  * What it sees of them makes its results infinite or NaN: which of the two, where
  * an infinity of V meets a weight below the range of 16 bits, is not defined; nor
- * is it for a query that itself holds them, or whose scores pass the range of fp32.
+ * is it for a query that itself holds them, or whose scores, or sums of weights
+ * times V, pass the range of fp32.
  * One that sees a key in a page whose id is invalid gives NaN, as do all
  * queries of a sequence longer than its table. Scores, softmax and sums are
- * fp32; weights enter the products with V as two 16-bit parts; results are
- * rounded once. The cache is split over its length where there are few
- * sequences and heads; the order of the sums depends on the batch's shape and
- * lengths alone, so results are deterministic.
+ * fp32; weights enter the products with V as two 16-bit parts (fp16: those below a
+ * 2^-18th of the largest with fewer bits, below a 2^-40th none); 8-bit codes are
+ * summed with 128 added, so results are off by some 2^-23 of the largest |v| of a
+ * block; results are rounded once. The cache is split over its length where there
+ * are few sequences and heads; the order of the sums depends on the batch's shape
+ * and lengths alone, so results are deterministic.
  * Errors: KQ_ERR_ARG, KQ_ERR_SHAPE, KQ_ERR_ALIGN, KQ_ERR_HIP. */
 int kq_attn_decode(int type, const void* q, int64_t ldq, const kq_kv_cache* cache, const kq_kv_batch* batch, void* out,
                    int64_t ldo, int heads, float scale, int window, const uint64_t* tree, void* workspace,
@@ -602,8 +612,9 @@ int kq_attn_decode(int type, const void* q, int64_t ldq, const kq_kv_cache* cach
  * different lengths packed into one batch, or the next part of prompts whose
  * beginning is in the cache. Arguments and results as kq_attn_decode, without
  * trees, up to KQ_MAX_TOKENS rows and KQ_MAX_SEQS sequences. Weights enter the
- * products with V rounded to 16 bits and are summed as rounded (8-bit caches:
- * two 16-bit parts, and the sum of the weights themselves).
+ * products with V rounded to 16 bits and are summed as rounded (fp16: those below a
+ * 2^-29th of the largest with fewer bits; 8-bit caches: two 16-bit parts of the
+ * weight times V's scale, and the sum of the weights themselves).
  * Errors: as kq_attn_decode, and KQ_ERR_ARG where the batch is beyond the grid. */
 int kq_attn_prompt(int type, const void* q, int64_t ldq, const kq_kv_cache* cache, const kq_kv_batch* batch, void* out,
                    int64_t ldo, int heads, float scale, int window, void* workspace, int64_t workspace_bytes,
