@@ -493,10 +493,16 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_attn_prompt(AttnArgs a) {
 
   // Where scores are far from zero the walk is taken again, by the waves that have
   // such columns, a page at a time from memory. (m only rises: what it passed on its
-  // way up from below -FAR has no weight, or left l infinite or NaN. 4000 bf16 tokens
-  // of 32 x 128 that all have such scores 452 us, 178 without. A branch in every
-  // step instead: 8191 tokens 568 -> 619 us, heads of 256 870 -> 1400.)
-  if (__any(have && m != -__builtin_inff() && !(__builtin_fabsf(m) < FAR && l < __builtin_inff()))) {
+  // way up from below -FAR has no weight, or left l or o infinite or NaN. 4000 bf16
+  // tokens of 32 x 128 that all have such scores 452 us, 178 without. A branch in
+  // every step instead: 8191 tokens 568 -> 619 us, heads of 256 870 -> 1400.)
+  float zero[4] = {l * 0.0f, 0.0f, 0.0f, 0.0f};   // NaN where one of l and o is infinite or NaN
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) zero[i & 3] = __builtin_fmaf(o[d][i], 0.0f, zero[i & 3]);
+  const bool finite = (zero[0] + zero[1]) + (zero[2] + zero[3]) == 0.0f;
+  if (__any(have && m != -__builtin_inff() && !(finite && __builtin_fabsf(m) < FAR))) {
     m = -__builtin_inff();
     l = 0.0f;
 #pragma unroll

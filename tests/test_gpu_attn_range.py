@@ -202,3 +202,31 @@ def test_a_long_tail_far_below():
             # its rounding; the weights' (2^-11 and 2^-8 at most); sums of 131071 in 512 parts of at most 1024 in fp32
             tol = want * (A.HALF_STEP[kind] + (TWO["q8_0" if cache_kind == "q8_0" else kind] if decode else ONE[kind]) + 2 * 1024 * 2.0 ** -24)
             assert (np.abs(got - want) <= tol).all(), (kind, cache_kind, decode, got, want)
+
+
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("kind,cache_kind", BOTH)
+@pytest.mark.parametrize("far", [1.0 / 64, 1.0 / 16, 1.0 / 8, 1.0])
+@pytest.mark.parametrize("new,lens,heads,kv_heads,D", [([40], [160], 32, 1, 64), ([50], [700], 16, 1, 128)])
+def test_scores_that_rise_from_far_below(decode, kind, cache_kind, far, new, lens, heads, kv_heads, D):
+    """The first pages' scores are hugely negative, at many sizes, and their V large; the others' are ordinary."""
+    rng = np.random.default_rng(90)
+    b = T.Batch(91, new, lens)
+    top = LARGE[kind]
+
+    def rows(is_v, length):
+        first = (np.arange(length) < 70)[:, None, None]
+        if is_v:
+            return np.where(first, 300.0, 1.0) * rng.standard_normal((length, kv_heads, D))
+        return np.broadcast_to(np.where(first, -top * far, rng.uniform(0.5, 2.0, (length, kv_heads, 1)) / (top * D)), (length, kv_heads, D))
+    pools, values = T.cache_with(b, cache_kind, kv_heads, D, rows)
+    q = T.narrow(np.broadcast_to(top * rng.uniform(0.5, 1.0, (b.T, heads, 1)), (b.T, heads, D)).reshape(b.T, heads * D), kind)
+    got = attend(decode, kind, cache_kind, b, pools, q, kv_heads, D, 1.0)
+    step = TWO["q8_0" if cache_kind == "q8_0" else kind] if decode or cache_kind == "q8_0" else ONE[kind]
+    wide, want = A.widen(q).reshape(b.T, heads, D), {}
+    for row, s, i, at in b.tokens():
+        ok = A.visible(at, b.lens[s], 0)
+        ok[:70] = False        # their weights are below 2^-10000
+        outs = [A.attend(wide[row, h], values[0][s][:, 0], values[1][s][:, 0], 1.0, ok) for h in range(heads)]
+        want[row] = (np.array([o[0] for o in outs]), np.array([A.attention_tolerance(*o[:2], *o[3:], int(ok.sum()), kind, step, LOST) for o in outs]))
+    T.check_rows(got, want, b.T, got, f"{new} {lens}")
